@@ -12,6 +12,7 @@ _lib = None
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
+F32 = ctypes.c_float
 INT = ctypes.c_int
 SZ = ctypes.c_size_t
 
@@ -44,6 +45,19 @@ SIGNATURES = {
     "tq_qgemv_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
     "tq_qgemm_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
     "tq_matmul_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
+    "tq_qk_norm_rope": (INT, [INT, P, I64, I64, I64, P, I64, I64, I64, I64, I64, I64, INT, INT, P,
+                              P, F32, P, P, P, I64, I64, P, I64, I64, P]),
+    "tq_cache_bytes": (SZ, [INT, I64, I64, I64, I64]),
+    "tq_cache_write": (INT, [INT, INT, P, I64, I64, P, I64, I64, I64, I64, I64, P, P, P, I64, I64,
+                             P]),
+    "tq_cache_read": (INT, [INT, INT, P, P, I64, I64, I64, I64, P, I64, P, P, P]),
+    "tq_tree_attention_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64]),
+    "tq_tree_attention": (INT, [INT, INT, P, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64,
+                                I64, I64, P, P, P, I64, I64, I64, I64, F32, P, I64, I64, P, SZ,
+                                P]),
+    "tq_verify_draft_workspace_bytes": (SZ, [I64, I64]),
+    "tq_verify_draft": (INT, [INT, P, I64, P, I64, I64, I64, P, P, P, I64, P, P, I64, P, P, P, P,
+                              SZ, P]),
 }
 
 

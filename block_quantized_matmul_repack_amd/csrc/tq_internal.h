@@ -111,6 +111,34 @@ __device__ __forceinline__ void load_x8(float (&v)[8], const void *x, int64_t i)
     }
 }
 
+// fp32 rounded to nearest even in a 16-bit type (TQ_BF16 or TQ_F16), its bits.
+template <int DT>
+__device__ __forceinline__ uint16_t f32_to_16(float f)
+{
+    if constexpr (DT == TQ_BF16)
+        return __builtin_bit_cast(uint16_t, (__bf16)f);
+    else
+        return f32_to_f16_bits(f);
+}
+
+// Eight consecutive elements of dtype DT from index i, rounded once; y needs
+// only element alignment.
+template <int DT>
+__device__ __forceinline__ void store_x8(void *y, int64_t i, const float (&v)[8])
+{
+    if constexpr (DT == TQ_F32) {
+        float *p = (float *)y + i;
+        *(f32x4u *)p = f32x4u{v[0], v[1], v[2], v[3]};
+        *(f32x4u *)(p + 4) = f32x4u{v[4], v[5], v[6], v[7]};
+    } else {
+        u16x8u h;
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            h[e] = f32_to_16<DT>(v[e]);
+        *(u16x8u *)((uint16_t *)y + i) = h;
+    }
+}
+
 // Max over the 4 lanes of a quad (DPP quad permutations, no LDS).
 __device__ __forceinline__ float quad_max(float v)
 {
@@ -339,5 +367,83 @@ hipError_t launch_quantize_mx(int dtype, const void *x, int64_t M, int64_t K, in
 hipError_t launch_qgemm_mx(const void *tiles, int64_t K, int64_t N, const uint8_t *q,
                            const uint8_t *e, int64_t M, float *y, int64_t ldy, int S, float *part,
                            hipStream_t s);
+
+// The paged block-quantized cache (cache_layout.h).
+struct CacheShape {
+    int type, heads, D;              // heads: key / value heads
+    int64_t pages, page_size;
+};
+
+inline int log2_of(int64_t p)
+{
+    int l = 0;
+    while ((int64_t(1) << l) < p)
+        l++;
+    return l;
+}
+
+// ts, hs: token and head strides in elements.
+hipError_t launch_cache_write(const CacheShape &c, int dtype, const void *k, int64_t k_ts,
+                              int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                              int64_t tokens, const int32_t *slots, void *k_cache, void *v_cache,
+                              hipStream_t s);
+hipError_t launch_cache_read(const CacheShape &c, int dtype, const void *k_cache,
+                             const void *v_cache, const int32_t *slots, int64_t tokens, void *k,
+                             void *v, hipStream_t s);
+
+// Per-head RMS norm and position rotation of queries and keys.
+struct NormRopeArgs {
+    const void *x[2];                // queries, keys
+    void *y[2];
+    int64_t xts[2], xhs[2], yts[2], yhs[2];
+    const void *w[2];                // norm weights [D], or null: no norm
+    int heads[2];
+    int w_dtype;
+    int64_t tokens;
+    int D, rot, interleaved;
+    float eps;
+    const int32_t *pos;
+    const float *freq;               // [rot / 2]
+};
+hipError_t launch_norm_rope(int dtype, const NormRopeArgs &a, hipStream_t s);
+
+// Attention of the new tokens of each sequence over the cache.
+struct AttnArgs {
+    const void *q;
+    void *y;
+    int64_t qts, qhs, yts, yhs;      // token and head strides, elements
+    const uint8_t *kc, *vc;
+    const int32_t *table;            // [batch][table_pages] at row stride table_stride
+    int64_t table_stride;
+    const int32_t *ctx, *starts;
+    const uint32_t *mask;            // [tokens][mask_words] or null
+    int64_t mask_stride;             // words
+    int64_t pages, tokens;
+    int table_pages, log_page, batch, heads, kv_heads, max_nodes, mask_words, dtype;
+    float scale;
+};
+// Keys a launch splits each sequence over, for a fixed launch geometry.
+struct AttnPlan {
+    int qt, row_blocks, splits, chunk;   // query tiles of 16 per wave; key ranges of `chunk`
+};
+AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
+                   int64_t max_keys);
+size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads);
+hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
+                            uint32_t *counters, void *scratch, hipStream_t s);
+
+// Verification of drafted tokens.
+struct VerifyArgs {
+    const void *target, *draft;      // [nodes][vocab] at row strides; draft may be null
+    int64_t target_stride, draft_stride;
+    const int32_t *tokens, *parents, *starts;
+    const float *u, *r;
+    int64_t nodes, vocab;
+    int batch, width;
+    int32_t *count, *out_tokens, *out_nodes;
+};
+size_t verify_scratch_bytes(int64_t batch, int64_t vocab);
+hipError_t launch_verify(int dtype, const VerifyArgs &a, uint32_t *counters, void *scratch,
+                         hipStream_t s);
 
 }  // namespace tq

@@ -417,6 +417,231 @@ def block_dots(qtype, tiles, K, N, q, lut=None, path=PATH_GEMV, out=None):
     return out
 
 
+def _need_int32(name, what, t, n, dims=1):
+    if t.dtype != torch.int32 or t.dim() != dims or t.numel() < n:
+        raise TiledqError(f"{name}: {what} must be int32 with {dims} dimension(s) and at least "
+                          f"{n} elements, got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_rows(name, what, t, heads=None, D=None, dtypes=_DTYPES):
+    """t is [tokens, heads, D] on the GPU with contiguous rows of D; returns
+    (token stride, head stride)."""
+    if t.dim() != 3 or t.dtype not in dtypes or (heads is not None and t.shape[1] != heads) or \
+            (D is not None and t.shape[2] != D):
+        want = f"[tokens, {'heads' if heads is None else heads}, {'D' if D is None else D}]"
+        raise TiledqError(f"{name}: {what} must be {want} of {[str(d) for d in dtypes]}, got "
+                          f"{t.dtype} {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise TiledqError(f"{name}: {what} must have contiguous rows")
+    if not t.is_cuda:
+        raise TiledqError("tiledq operates on GPU tensors only")
+    return t.stride(0), t.stride(1)
+
+
+def _same_device(name, *ts):
+    devices = {t.device for t in ts if t is not None}
+    if len(devices) > 1:
+        raise TiledqError(f"{name}: tensors on several devices: {sorted(map(str, devices))}")
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None):
+    """RMS norm of each head of q [T, Hq, D] and k [T, Hk, D] (fp32 / bf16 /
+    fp16, any token and head strides) with weights [D] (None: no norm), then
+    the rotation of its first 2 * len(inv_freq) elements by the angles
+    positions [T] (int32) * inv_freq (fp32): pairs (i, i + half), or
+    neighbours if interleaved.  q_out, k_out may be q, k.  Returns both."""
+    name = "tq_qk_norm_rope"
+    qs = _check_rows(name, "q", q)
+    T, Hq, D = q.shape
+    ks = _check_rows(name, "k", k, D=D, dtypes=(q.dtype,))
+    if k.shape[0] != T:
+        raise TiledqError(f"{name}: q has {T} tokens, k {k.shape[0]}")
+    Hk = k.shape[1]
+    _need_int32(name, "positions", positions, T)
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        raise TiledqError(f"{name}: inv_freq must be 1-D float32")
+    wdt = q.dtype
+    for w in (q_weight, k_weight):
+        if w is not None:
+            wdt = w.dtype
+            if w.dtype not in _DTYPES or w.dim() != 1 or w.shape[0] != D:
+                raise TiledqError(f"{name}: norm weights must be [{D}] fp32, bf16 or fp16")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TiledqError(f"{name}: q_weight and k_weight must share a type")
+    _need_cuda(positions, inv_freq, q_weight, k_weight)
+    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device) if k_out is None else k_out
+    qo = _check_rows(name, "q_out", q_out, Hq, D, dtypes=(q.dtype,))
+    ko = _check_rows(name, "k_out", k_out, Hk, D, dtypes=(q.dtype,))
+    if q_out.shape[0] != T or k_out.shape[0] != T:
+        raise TiledqError(f"{name}: outputs must have {T} tokens")
+    _same_device(name, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    check(lib().tq_qk_norm_rope(
+        _DTYPES[q.dtype], _ptr(q), *qs, Hq, _ptr(k), *ks, Hk, T, D, 2 * inv_freq.shape[0],
+        int(interleaved), _DTYPES[wdt], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions),
+        _ptr(inv_freq), _ptr(q_out), *qo, _ptr(k_out), *ko, _stream(q)), name)
+    return q_out, k_out
+
+
+def cache_bytes(ctype, n_pages, page_size, kv_heads, D):
+    """Bytes of one of the two buffers (keys, values) of a paged cache."""
+    return lib().tq_cache_bytes(ctype, n_pages, page_size, kv_heads, D)
+
+
+def _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D):
+    """Pages of a cache, from its buffers' size."""
+    page = _size_query("tq_cache_bytes", ctype, 1, page_size, kv_heads, D)
+    if page == 0:
+        raise TiledqError(f"{name}: no cache of type {ctype} with {kv_heads} heads of {D} and "
+                          f"pages of {page_size}")
+    _need_cuda(k_cache, v_cache)
+    n = _nbytes(k_cache)
+    if n != _nbytes(v_cache) or n == 0 or n % page:
+        raise TiledqError(f"{name}: caches hold {n} and {_nbytes(v_cache)} bytes, not the same "
+                          f"whole number of pages of {page}")
+    return n // page
+
+
+def cache_write(ctype, k, v, k_cache, v_cache, slots, page_size):
+    """Quantize k, v [T, H, D] (fp32 / bf16 / fp16) into slots [T] (int32,
+    page * page_size + position; one outside the cache is skipped) of a paged
+    Q8_0 or Q4_0 cache (uint8 buffers of cache_bytes)."""
+    name = "tq_cache_write"
+    ks = _check_rows(name, "k", k)
+    T, H, D = k.shape
+    vs = _check_rows(name, "v", v, H, D, dtypes=(k.dtype,))
+    if v.shape[0] != T:
+        raise TiledqError(f"{name}: k has {T} tokens, v {v.shape[0]}")
+    _need_int32(name, "slots", slots, T)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, H, D)
+    _need_cuda(slots)
+    _same_device(name, k, v, k_cache, v_cache, slots)
+    check(lib().tq_cache_write(ctype, _DTYPES[k.dtype], _ptr(k), *ks, _ptr(v), *vs, T, H, D,
+                               _ptr(slots), _ptr(k_cache), _ptr(v_cache), n_pages, page_size,
+                               _stream(k)), name)
+
+
+def cache_read(ctype, k_cache, v_cache, slots, kv_heads, D, page_size, dtype=torch.float32):
+    """The values of cache slots [T]: (k, v) [T, kv_heads, D] of dtype; a slot
+    outside the cache reads as zeros."""
+    name = "tq_cache_read"
+    if dtype not in _DTYPES:
+        raise TiledqError(f"{name}: dtype must be float32, bfloat16 or float16")
+    if slots.dim() != 1:
+        raise TiledqError(f"{name}: slots must have one dimension")
+    T = slots.shape[0]
+    _need_int32(name, "slots", slots, T)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D)
+    _need_cuda(slots)
+    _same_device(name, k_cache, v_cache, slots)
+    k = torch.empty((T, kv_heads, D), dtype=dtype, device=k_cache.device)
+    v = torch.empty_like(k)
+    check(lib().tq_cache_read(ctype, _DTYPES[dtype], _ptr(k_cache), _ptr(v_cache), n_pages,
+                              page_size, kv_heads, D, _ptr(slots), T, _ptr(k), _ptr(v),
+                              _stream(k_cache)), name)
+    return k, v
+
+
+_ATTN_DTYPES = (torch.bfloat16, torch.float16)
+
+
+def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_heads, page_size,
+                   max_nodes=None, max_ctx=None, scale=None, mask=None, out=None):
+    """Attention of new tokens q [T, Hq, D] (bf16 / fp16) over a paged cache
+    that already holds their keys and values.  Sequence b: rows starts[b] ..
+    starts[b+1]-1 of q, pages page_table[b] (int32 [B, pages]), ctx_lens[b]
+    tokens before the new ones.  mask: int32 [T, words], bit j of a row = new
+    token j of the sequence is seen (None: the chain, j <= i).  max_nodes and
+    max_ctx bound the new and the cached tokens of a sequence; they default
+    to all rows of q and all of the table.  scale defaults to D ** -0.5."""
+    name = "tq_tree_attention"
+    qs = _check_rows(name, "q", q, dtypes=_ATTN_DTYPES)
+    T, Hq, D = q.shape
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise TiledqError(f"{name}: page_table must be int32 [batch, pages], rows contiguous")
+    B, width = page_table.shape
+    _need_int32(name, "ctx_lens", ctx_lens, B)
+    _need_int32(name, "starts", starts, B + 1)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D)
+    _need_cuda(ctx_lens, starts)
+    if not page_table.is_cuda or (mask is not None and not mask.is_cuda):
+        raise TiledqError("tiledq operates on GPU tensors only")
+    words = stride = 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] < T or \
+                (mask.shape[1] > 1 and mask.stride(1) != 1):
+            raise TiledqError(f"{name}: mask must be int32 [{T}, words], rows contiguous")
+        words, stride = mask.shape[1], mask.stride(0)
+    max_nodes = max(T, 1) if max_nodes is None else max_nodes
+    max_ctx = width * page_size if max_ctx is None else max_ctx
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    os = _check_rows(name, "out", out, Hq, D, dtypes=(q.dtype,))
+    if out.shape[0] < T:
+        raise TiledqError(f"{name}: out has {out.shape[0]} tokens, needs {T}")
+    _same_device(name, q, k_cache, v_cache, page_table, ctx_lens, starts, mask, out)
+    st = _stream(q)
+    need = _size_query("tq_tree_attention_workspace_bytes", B, Hq, kv_heads, D, max_nodes, max_ctx)
+    ws = workspace(q.device, st, need) if need else None
+    check(lib().tq_tree_attention(
+        ctype, _DTYPES[q.dtype], _ptr(q), *qs, T, Hq, kv_heads, D, _ptr(k_cache), _ptr(v_cache),
+        n_pages, page_size, _ptr(page_table), page_table.stride(0), width, B, _ptr(ctx_lens),
+        _ptr(starts), _ptr(mask), stride, words, max_nodes, max_ctx,
+        D ** -0.5 if scale is None else scale, _ptr(out), *os, _ptr(ws), need, st), name)
+    return out
+
+
+def verify_draft(target, tokens, starts, uniforms, final_uniforms, draft=None, parents=None,
+                 max_nodes=None):
+    """Accept drafted tokens against the target's probabilities.  Sequence b:
+    nodes starts[b] .. starts[b+1]-1, node 0 the last certain token; target
+    [N, V] (fp32 / bf16 / fp16): row n the target's distribution after node n;
+    draft [N, V]: the one n's children were drawn from (None: tokens chosen
+    without chance); tokens, parents int32 [N] (parents None: chains);
+    uniforms fp32 [N], final_uniforms fp32 [B].  Returns int32 (accepted [B],
+    tokens [B, max_nodes]: the accepted tokens, the next one, -1s; nodes [B,
+    max_nodes]: the accepted nodes, -1s).  max_nodes bounds the nodes of a
+    sequence; it defaults to all of them."""
+    name = "tq_verify_draft"
+    for what, t in (("target", target), ("draft", draft)):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.dtype not in _DTYPES or t.dtype != target.dtype or \
+                t.shape != target.shape or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise TiledqError(f"{name}: {what} must be [nodes, vocab] fp32, bf16 or fp16 with "
+                              f"contiguous rows, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise TiledqError("tiledq operates on GPU tensors only")
+    N, V = target.shape
+    _need_int32(name, "tokens", tokens, N)
+    if parents is not None:
+        _need_int32(name, "parents", parents, N)
+    _need_int32(name, "starts", starts, 1)
+    B = starts.shape[0] - 1
+    for what, t, n in (("uniforms", uniforms, N), ("final_uniforms", final_uniforms, B)):
+        if t.dtype != torch.float32 or t.dim() != 1 or t.numel() < n:
+            raise TiledqError(f"{name}: {what} must be float32 with at least {n} elements")
+    _need_cuda(tokens, parents, starts, uniforms, final_uniforms)
+    _same_device(name, target, draft, tokens, parents, starts, uniforms, final_uniforms)
+    width = max(N, 1) if max_nodes is None else max_nodes
+    if width < 1:
+        raise TiledqError(f"{name}: max_nodes must be at least 1")
+    accepted = torch.empty(B, dtype=torch.int32, device=target.device)
+    out_tokens = torch.empty((B, width), dtype=torch.int32, device=target.device)
+    nodes = torch.empty_like(out_tokens)
+    st = _stream(target)
+    need = _size_query("tq_verify_draft_workspace_bytes", B, V)
+    ws = workspace(target.device, st, need) if need else None
+    check(lib().tq_verify_draft(
+        _DTYPES[target.dtype], _ptr(target), target.stride(0), _ptr(draft),
+        draft.stride(0) if draft is not None else 0, N, V, _ptr(tokens), _ptr(parents),
+        _ptr(starts), B, _ptr(uniforms), _ptr(final_uniforms), width, _ptr(accepted),
+        _ptr(out_tokens), _ptr(nodes), _ptr(ws), need, st), name)
+    return accepted, out_tokens, nodes
+
+
 STREAM_READ_BLOCKS = 2048       # TQ_STREAM_READ_BLOCKS: words of the sink
 
 

@@ -420,6 +420,145 @@ int tq_matmul_mx(const void *tiles, int64_t K, int64_t N, const uint8_t *q,
                  const uint8_t *e, int64_t M, float *y, int64_t ldy,
                  void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- One step of decoding between the projections and the next token ----
+ *
+ * The products above give a model's projections and its logits; the four
+ * operators below are what a decode step, plain or speculative (several
+ * drafted tokens checked in one pass), does between them: norm and rotation
+ * of queries and keys, the quantized key / value cache, attention over it,
+ * and the choice of the next tokens.  Calling convention as above; strides
+ * count elements, rows of the innermost dimension are contiguous.  Index
+ * arrays live on the device and cannot be checked before the launch: the
+ * kernels keep every access inside the buffers whatever they hold, as each
+ * entry point states.
+ *
+ * tq_qk_norm_rope: per-head RMS norm of queries and keys and their position
+ * rotation, one pass.  For each head x of D elements of token t:
+ *   z = x * w / sqrt(mean(x^2) + eps)  (w NULL: z = x);
+ *   pair i < rot/2 is (z[i], z[rot/2 + i]), or with `interleaved` (z[2i],
+ *   z[2i + 1]); (a, b) -> (a cos h - b sin h, b cos h + a sin h) with
+ *   h = positions[t] * inv_freq[i]; elements rot .. D-1 stay.
+ * Statistics and products in fp32, angles in fp64, each output rounded once.
+ *   dtype : of q, k and both outputs;  w_dtype : of q_weight, k_weight [D].
+ *   q     : device, [tokens][q_heads][D] at strides q_ts, q_hs; k likewise.
+ *   q_out, k_out : at strides *_ts, *_hs; may be q and k themselves (same
+ *           strides), otherwise must not overlap the inputs.
+ *   positions : device int32 [tokens];  inv_freq : device fp32 [rot / 2].
+ * Domain: D even, 2..512; rot even, 0..D; heads 0..1024 (not both 0);
+ * tokens 0..2^20. */
+int tq_qk_norm_rope(int dtype, const void *q, int64_t q_ts, int64_t q_hs, int64_t q_heads,
+                    const void *k, int64_t k_ts, int64_t k_hs, int64_t k_heads,
+                    int64_t tokens, int64_t D, int64_t rot, int interleaved,
+                    int w_dtype, const void *q_weight, const void *k_weight, float eps,
+                    const int32_t *positions, const float *inv_freq,
+                    void *q_out, int64_t qo_ts, int64_t qo_hs,
+                    void *k_out, int64_t ko_ts, int64_t ko_hs, hipStream_t stream);
+
+/* The paged cache.  One buffer for keys and one for values, each n_pages
+ * pages of page_size tokens (16..1024, a power of two) of kv_heads heads of
+ * D (64, 96, 128 or 256) elements, every 32 elements a block with an fp16
+ * scale: TQ_Q8_0 (tq_quantize_act's rule) or TQ_Q4_0 (GGML's: m = the first
+ * element of the largest magnitude, d = m / -8, code = min(15, trunc(x *
+ * (1 / d) + 8.5)), value = fp16(d) * (code - 8); fp32 steps).  Elements past
+ * +-65472 count as +-65472 and NaN as 0, so a cache holds finite numbers
+ * (finite in fp16, too).  The order inside a buffer is the library's own.
+ * tq_cache_bytes: bytes of ONE of the two buffers; 0 for invalid arguments.
+ *
+ * tq_cache_write quantizes tokens' keys and values into their slots (slot =
+ * page * page_size + position); a slot outside the cache is skipped (-1:
+ * padding).  Slots of one call must differ.
+ *   k, v : device, [tokens][kv_heads][D] of dtype at strides ts, hs.
+ *   slots : device int32 [tokens];  k_cache, v_cache : 16-byte aligned.
+ * tq_cache_read gives back the values of slots, [tokens][kv_heads][D]
+ * contiguous, rounded once to dtype; a slot outside the cache reads as zeros.
+ * kv_heads 1..1024, n_pages 1..2^26 with n_pages * page_size < 2^31. */
+size_t tq_cache_bytes(int type, int64_t n_pages, int64_t page_size, int64_t kv_heads, int64_t D);
+int tq_cache_write(int type, int dtype, const void *k, int64_t k_ts, int64_t k_hs,
+                   const void *v, int64_t v_ts, int64_t v_hs, int64_t tokens,
+                   int64_t kv_heads, int64_t D, const int32_t *slots,
+                   void *k_cache, void *v_cache, int64_t n_pages, int64_t page_size,
+                   hipStream_t stream);
+int tq_cache_read(int type, int dtype, const void *k_cache, const void *v_cache,
+                  int64_t n_pages, int64_t page_size, int64_t kv_heads, int64_t D,
+                  const int32_t *slots, int64_t tokens, void *k, void *v, hipStream_t stream);
+
+/* Attention of new tokens over the cache.  Sequence b's new tokens are rows
+ * starts[b] .. starts[b+1]-1 of q (one for plain decoding, a chain or a tree
+ * of drafted ones otherwise); their keys and values lie in the cache already,
+ * at positions ctx_lens[b], ctx_lens[b] + 1, ...  Token i of a sequence sees
+ * every position below ctx_lens[b], and position ctx_lens[b] + j where bit
+ * j & 31 of word j >> 5 of its mask row is set (mask NULL: where j <= i).
+ * Query head h uses key head h / (heads / kv_heads).  out = softmax(scale *
+ * q k^T) v; a token that sees nothing gets zeros.
+ *   dtype : TQ_BF16 or TQ_F16, of q and out.
+ *   q, out : device, [tokens][heads][D] at strides ts, hs.
+ *   page_table : device int32, row b the pages of sequence b, table_pages of
+ *           them at row stride table_stride.  Positions on a page outside the
+ *           cache, or past the row, are not seen.
+ *   starts : device int32 [batch + 1], not decreasing;  ctx_lens : [batch].
+ *   mask  : device uint32, one row per token (row stride mask_stride words,
+ *           mask_words of them), or NULL.
+ *   max_nodes, max_ctx : at least every sequence's new tokens and cached
+ *           ones; they shape the launch only.  Tokens past max_nodes of a
+ *           sequence are not computed (their rows stay as they were); a
+ *           longer cache than max_ctx costs speed, nothing else.
+ *   workspace : 256-byte aligned, tq_tree_attention_workspace_bytes() bytes
+ *           (0: may be NULL), laid out as tq_matmul's: the first
+ *           TQ_NOALLOC_SCRATCH_BYTES zero before the first use and after
+ *           every call, scratch behind.  A smaller one: TQ_E_SHAPE.
+ * Queries enter the matrix cores as fp16 after an exact scaling of each row,
+ * codes times scales and probabilities rounded once to fp16; sums in fp32.
+ * Deterministic.  Domain: heads a multiple of kv_heads, both 1..1024; tokens
+ * 0..2^20; batch 0..65535; table_pages * page_size and max_ctx up to 2^30;
+ * scale finite and > 0. */
+size_t tq_tree_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t kv_heads,
+                                         int64_t D, int64_t max_nodes, int64_t max_ctx);
+int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs,
+                      int64_t tokens, int64_t heads, int64_t kv_heads, int64_t D,
+                      const void *k_cache, const void *v_cache, int64_t n_pages,
+                      int64_t page_size, const int32_t *page_table, int64_t table_stride,
+                      int64_t table_pages, int64_t batch, const int32_t *ctx_lens,
+                      const int32_t *starts, const uint32_t *mask, int64_t mask_stride,
+                      int64_t mask_words, int64_t max_nodes, int64_t max_ctx, float scale,
+                      void *out, int64_t o_ts, int64_t o_hs,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Verification of drafted tokens from given uniform numbers.  Sequence b's
+ * nodes are starts[b] .. starts[b+1]-1; its node 0 is the last token already
+ * certain, the others were drafted (tokens[n]) after the node parents[n] <
+ * n (numbers within the sequence; parents NULL: a chain, parent n - 1).  Row
+ * n of target is the target's distribution after node n; row n of draft (may
+ * be NULL: tokens chosen without chance, such as the most likely ones) the
+ * one that n's children were drawn from.  From node 0, with w = its target
+ * row, the children c of the node reached are tried in order:
+ *   draft given: c is accepted if uniforms[c] * draft(x_c) < w(x_c), else w
+ *     becomes max(w - draft, 0) over its sum (unless that is 0);
+ *   none: c is accepted if uniforms[c] * (1 - the target's probability of
+ *     the children refused before) < w(x_c), else w(x_c) becomes 0;
+ * an accepted child is the next node, with its own row.  After the last one
+ * the next token is the first index whose running sum of w exceeds
+ * final_uniforms[b] times the sum (the last index of positive weight if none
+ * does, -1 if the row has none).  Arithmetic in fp64.  A token outside the
+ * vocabulary or a parent that does not come before its child is never
+ * accepted; probabilities that are negative or NaN count as 0.
+ *   dtype : of target and draft, rows of vocab at the given row strides.
+ *   uniforms : device fp32 [nodes], final_uniforms [batch], in [0, 1).
+ *   width : columns of the outputs, 1..1024, at least every sequence's nodes
+ *           (nodes past it are left out).
+ *   accepted : device int32 [batch], how many drafted tokens were accepted;
+ *   out_tokens [batch][width]: those tokens, then the next one, then -1;
+ *   out_nodes [batch][width]: the accepted nodes, then -1.  A sequence of no
+ *           nodes gives 0 and -1s.
+ *   workspace : as tq_tree_attention's, tq_verify_draft_workspace_bytes().
+ * Deterministic.  Domain: nodes 0..2^20, batch 0..65535, vocab 1..2^27. */
+size_t tq_verify_draft_workspace_bytes(int64_t batch, int64_t vocab);
+int tq_verify_draft(int dtype, const void *target, int64_t target_stride,
+                    const void *draft, int64_t draft_stride, int64_t nodes, int64_t vocab,
+                    const int32_t *tokens, const int32_t *parents, const int32_t *starts,
+                    int64_t batch, const float *uniforms, const float *final_uniforms,
+                    int64_t width, int32_t *accepted, int32_t *out_tokens, int32_t *out_nodes,
+                    void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Test instrument for the per-block integer dot ("Q2_0 Format" > "HVX
  * Vector Dot-Product": int8 products accumulated in 32-bit words, before the
  * row scale d of "Block-32 Quantized Formats" is applied): run the tq_qgemv
