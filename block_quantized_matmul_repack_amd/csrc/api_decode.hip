@@ -211,8 +211,8 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
     const tq::AttnArgs a{q, out, q_ts, q_hs, o_ts, o_hs, (const uint8_t *)k_cache,
                          (const uint8_t *)v_cache, page_table, table_stride, ctx_lens, starts,
                          mask, mask_stride, n_pages, tokens, (int)table_pages,
-                         tq::log2_of(page_size), (int)batch, (int)heads, (int)kv_heads,
-                         (int)max_nodes, (int)mask_words, dtype, scale};
+                         tq::log2_of(page_size), (int)batch, (int)kv_heads,
+                         (int)(heads / kv_heads), (int)max_nodes, (int)mask_words, dtype, scale};
     return launch_status(tq::launch_attention(type, (int)D, a, p, counters, scratch, stream));
 }
 

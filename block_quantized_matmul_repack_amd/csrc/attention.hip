@@ -13,16 +13,17 @@
 // the matrix cores and the vector work around them.
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
-// tile, QT tiles per wave, so a cached byte serves all the query heads and
-// tokens of its head.  The four waves of a workgroup take every fourth group
-// of 32 keys of the workgroup's key range; the ranges of a long cache go to
-// several workgroups, whose sums k_attn_combine joins.
-//
-// Keys and values go from memory through registers into the matrix cores
-// (v_mfma_f32_16x16x32_f16), without LDS: S^T = K Q^T leaves query columns in
+// tile, so a cached byte serves all the query heads and tokens of its head;
+// the key ranges of a long cache go to several workgroups, whose sums
+// k_attn_combine joins.  Up to 32 rows (k_attn) the four waves of a workgroup
+// hold the same rows and take every fourth group of 32 keys: keys and values
+// go from memory through registers into the matrix cores
+// (v_mfma_f32_16x16x32_f16), without LDS.  S^T = K Q^T leaves query columns in
 // lanes and keys in registers, which is the operand layout of O^T = V^T P^T
 // once lane group g's tokens are 4g..4g+3 of each 16 (cache_layout.h places
-// the codes to match).
+// the codes to match).  With more rows (k_attn_rows) the waves share the
+// dequantized operands of 64 keys through LDS, stored as the fragments that
+// the matrix instructions read.
 //
 // Rounding: the queries enter as fp16 after a scaling of each row by a power
 // of two that puts its largest element in [2^14, 2^15) (bf16 elements down to
@@ -45,10 +46,17 @@ constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -1e30f;
 constexpr int RED = 8;                           // fragments joined at a time
+#ifndef TG
+#define TG 1024
+#define MC 256
+#endif
+constexpr int64_t TARGET_GROUPS = TG, MIN_CHUNK = MC;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 template <int CT, int D> struct Geo {
     static constexpr int NB = D / 32;            // 32-element blocks = matrix steps of Q K^T
@@ -62,66 +70,67 @@ template <int CT, int D> struct Geo {
     static constexpr int TB = (int)token_code_bytes(CT, D);
 };
 
-// 32 keys' codes and scales as one lane loads them (two 16-key tiles).
-template <int CT, int D> struct Raw {
+// 16 keys' codes and scales as one lane loads them.
+template <int CT, int D> struct Tile {
     using G = Geo<CT, D>;
-    uint32_t k[2][G::KW], ks[2][(G::NB + 1) / 2];
-    uint32_t v[2][G::KW];
-    uint2 vs[2][G::NH];
+    uint32_t k[G::KW], ks[(G::NB + 1) / 2];
+    uint32_t v[G::KW];
+    uint32_t vs[2 * G::NH];
 };
 
 template <int N> __device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *p)
 {
     if constexpr (N == 4) {
-        const uint4 x = *(const uint4 *)p;
+        const u4 x = *(const u4 *)p;
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     } else if constexpr (N == 3) {
         const uint32_t *q = (const uint32_t *)p;
         w[0] = q[0]; w[1] = q[1]; w[2] = q[2];
     } else if constexpr (N == 2) {
-        const uint2 x = *(const uint2 *)p;
+        const u2 x = *(const u2 *)p;
         w[0] = x.x; w[1] = x.y;
     } else {
         w[0] = *(const uint32_t *)p;
     }
 }
 
-// Tile T (16 keys at position pos of its page) of a step.
-template <int CT, int D, int T>
-__device__ __forceinline__ void load_tile(Raw<CT, D> &raw, const uint8_t *kc, const uint8_t *vc,
+// The 16 keys at position pos (uniform) of the page whose chunks start at kc
+// and vc (uniform): uniform bases, one lane offset each.
+template <int CT, int D>
+__device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const uint8_t *kc, const uint8_t *vc,
                                           int pos, int P, int lane)
 {
     using G = Geo<CT, D>;
     const int r = lane & 15, g = lane >> 4;
-    const int key = pos + r;
+    const uint8_t *kp = kc + pos * G::TB;
     if constexpr (CT == TQ_Q8_0 && D % 64 != 0) {
 #pragma unroll
         for (int s = 0; s < G::NB; s++)
-            load_words<2>(raw.k[T] + 2 * s, kc + key * G::TB + k_piece_off<CT, D>(s, g));
+            load_words<2>(raw.k + 2 * s, kp + (r * G::TB + k_piece_off<CT, D>(s, g)));
     } else if constexpr (CT == TQ_Q4_0 && D % 128 != 0) {
-        load_words<G::KW>(raw.k[T], kc + key * G::TB + k_piece_off<CT, D>(0, g));
+        load_words<G::KW>(raw.k, kp + (r * G::TB + k_piece_off<CT, D>(0, g)));
     } else {
         constexpr int PER = CT == TQ_Q8_0 ? 2 : 4;           // blocks per 16 bytes
 #pragma unroll
         for (int s = 0; s < G::NB; s += PER)
-            load_words<4>(raw.k[T] + s * (4 / PER), kc + key * G::TB + k_piece_off<CT, D>(s, g));
+            load_words<4>(raw.k + s * (4 / PER), kp + (r * G::TB + k_piece_off<CT, D>(s, g)));
     }
-    const uint8_t *ks = kc + P * G::TB + key * (G::NB * 2);
+    const uint8_t *ks = kc + (P * G::TB + pos * (G::NB * 2)) + r * (G::NB * 2);
     if constexpr (G::NB == 3) {
         const uint16_t *q = (const uint16_t *)ks;
-        raw.ks[T][0] = q[0] | ((uint32_t)q[1] << 16);
-        raw.ks[T][1] = q[2];
+        raw.ks[0] = q[0] | ((uint32_t)q[1] << 16);
+        raw.ks[1] = q[2];
     } else {
-        load_words<G::NB / 2>(raw.ks[T], ks);
+        load_words<G::NB / 2>(raw.ks, ks);
     }
-    const int quad = (pos >> 2) + g;
-    const uint8_t *vs = vc + P * G::TB;
+    const uint8_t *vp = vc + pos * G::TB;
+    const uint8_t *vs = vc + (P * G::TB + pos * 2);
 #pragma unroll
     for (int h = 0; h < G::NH; h++) {
-        load_words<G::VL>(raw.v[T] + h * G::VL,
-                          vc + (quad * (4 * G::TB) + (16 * h + r) * (G::VL * 4)));
+        load_words<G::VL>(raw.v + h * G::VL,
+                          vp + (g * (4 * G::TB) + (16 * h + r) * (G::VL * 4)));
         const int block = (16 * G::CW * h + G::CW * r) / 32;
-        raw.vs[T][h] = *(const uint2 *)(vs + (block * P + pos + 4 * g) * 2);
+        load_words<2>(raw.vs + 2 * h, vs + (block * P + 4 * g) * 2);
     }
 }
 
@@ -148,78 +157,93 @@ union Frag {
     h8 v;
 };
 
-// Block s of the lane's key in tile T: 8 elements.
+// Block s of the lane's key: 8 elements.
 template <int CT, int D>
-__device__ __forceinline__ h8 key_frag(const Raw<CT, D> &raw, int T, int s)
+__device__ __forceinline__ h8 key_frag(const Tile<CT, D> &raw, int s)
 {
     Frag f;
     if constexpr (CT == TQ_Q8_0) {
-        codes8(raw.k[T][2 * s], f.p[0], f.p[1]);
-        codes8(raw.k[T][2 * s + 1], f.p[2], f.p[3]);
+        codes8(raw.k[2 * s], f.p[0], f.p[1]);
+        codes8(raw.k[2 * s + 1], f.p[2], f.p[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            f.p[i] = codes4(raw.k[T][s] >> (4 * i));
+            f.p[i] = codes4(raw.k[s] >> (4 * i));
     }
-    const h2 two = as_h2(raw.ks[T][s >> 1]);
-    const _Float16 d = s & 1 ? two.y : two.x;
-    const h2 dd = {d, d};
+    const h2 two = as_h2(raw.ks[s >> 1]);
+    const h2 dd = s & 1 ? two.yy : two.xx;
 #pragma unroll
     for (int i = 0; i < 4; i++)
         f.p[i] *= dd;
     return f.v;
 }
 
-// Element j of the lane's group h of values: 8 tokens (4 of each tile).
+// Output tile t's element of the lane: 4 tokens.
 template <int CT, int D>
-__device__ __forceinline__ h8 value_frag(const Raw<CT, D> &raw, int h, int j)
+__device__ __forceinline__ void value_half(const Tile<CT, D> &raw, int t, h2 &a, h2 &b)
 {
     using G = Geo<CT, D>;
-    Frag f;
-#pragma unroll
-    for (int T = 0; T < 2; T++) {
-        if constexpr (CT == TQ_Q8_0) {
-            codes8(raw.v[T][h * G::VL + j], f.p[2 * T], f.p[2 * T + 1]);
-        } else {
-            const uint32_t w = raw.v[T][h * G::VL + (j >> 1)] >> (4 * (j & 1));
-            f.p[2 * T] = codes4(w);
-            f.p[2 * T + 1] = codes4(w >> 8);
-        }
-        f.p[2 * T] *= as_h2(raw.vs[T][h].x);
-        f.p[2 * T + 1] *= as_h2(raw.vs[T][h].y);
+    const int h = t / G::CW, j = t % G::CW;
+    if constexpr (CT == TQ_Q8_0) {
+        codes8(raw.v[h * G::VL + j], a, b);
+    } else {
+        const uint32_t w = raw.v[h * G::VL + (j >> 1)] >> (4 * (j & 1));
+        a = codes4(w);
+        b = codes4(w >> 8);
     }
-    return f.v;
+    a *= as_h2(raw.vs[2 * h]);
+    b *= as_h2(raw.vs[2 * h + 1]);
+}
+
+// What the value blocks of a tile hold must not meet a probability of 0 as
+// NaN or infinity: of the lane's four tokens (keys key .. key + 3), those not
+// there count as zeros, and so do new ones whose scale is no number.
+template <int CT, int D>
+__device__ __forceinline__ void drop_values(Tile<CT, D> &raw, int key, bool there, int ctx, int L)
+{
+    auto keep = [&](uint32_t w, int k) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t half = 0xFFFFu << (16 * i), e = 0x7C00u << (16 * i);
+            const bool in = there && k + i < L;
+            w = !in || (k + i >= ctx && (w & e) == e) ? w & ~half : w;
+        }
+        return w;
+    };
+#pragma unroll
+    for (int h = 0; h < 2 * Geo<CT, D>::NH; h++)
+        raw.vs[h] = keep(raw.vs[h], key + 2 * (h & 1));
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-__device__ __forceinline__ float load_16(const void *p, int64_t i, int dtype)
+// A read-only word at a uniform address, through the scalar cache: it does
+// not wait behind the tile loads in flight.
+__device__ __forceinline__ int load_uniform(const int32_t *p)
 {
-    const uint16_t b = ((const uint16_t *)p)[i];
-    return dtype == TQ_BF16 ? __builtin_bit_cast(float, (uint32_t)b << 16) : f16_bits_to_f32(b);
+    return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
 }
 
 // The rows of one workgroup: sequence b, key head h, row block rb; row r is
 // (token r / group, query head h * group + r % group).
 struct Rows {
-    int b, h, rb, group, T, ctx, L;
+    int b, h, rb, T, ctx, L;
     int64_t tok0;
 };
 
-__device__ __forceinline__ Rows rows_of(const AttnArgs &a, int row_blocks, int64_t unit)
+__device__ __forceinline__ Rows rows_of(const AttnArgs &a, uint32_t row_blocks, uint32_t unit)
 {
     Rows w;
-    w.rb = (int)(unit % row_blocks);
-    const int64_t bh = unit / row_blocks;
-    w.h = (int)(bh % a.kv_heads);
-    w.b = (int)(bh / a.kv_heads);
-    w.group = a.heads / a.kv_heads;
+    const uint32_t bh = unit / row_blocks;
+    w.rb = (int)(unit - bh * row_blocks);
+    w.b = (int)(bh / (uint32_t)a.kv_heads);
+    w.h = (int)(bh - w.b * (uint32_t)a.kv_heads);
     // lengths and starts are held inside the buffers whatever they say
-    const int64_t s0 = min(max((int64_t)uniform(a.starts[w.b]), (int64_t)0), a.tokens);
-    const int64_t s1 = min((int64_t)uniform(a.starts[w.b + 1]), a.tokens);
+    const int64_t s0 = min(max((int64_t)load_uniform(a.starts + w.b), (int64_t)0), a.tokens);
+    const int64_t s1 = min((int64_t)load_uniform(a.starts + w.b + 1), a.tokens);
     w.tok0 = s0;
     w.T = (int)min(max(s1 - s0, (int64_t)0), (int64_t)a.max_nodes);
-    w.ctx = max(uniform(a.ctx[w.b]), 0);
+    w.ctx = max(load_uniform(a.ctx + w.b), 0);
     const int64_t most = (int64_t)a.table_pages << a.log_page;
     w.L = (int)min((int64_t)w.ctx + w.T, most);
     return w;
@@ -229,21 +253,58 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs &a, int row_blocks, int64
 // takes what the launch did not foresee.
 __device__ __forceinline__ int ranges_of(const Rows &w, int splits, int chunk)
 {
-    return (int)max((int64_t)1, min((int64_t)splits, ((int64_t)w.L + chunk - 1) / chunk));
+    return (int)max(1u, min((uint32_t)splits, ((uint32_t)w.L + chunk - 1) / (uint32_t)chunk));
 }
 
-// Fragment (query tile qt, output tile t) of a row block, as every wave holds
-// it: lane's query column lane & 15, elements of rows 4 (lane >> 4) + 0..3.
+// A workgroup's rows and keys; false: it has none.
+struct Work {
+    Rows w;
+    uint32_t unit;
+    int range, ranges, begin, end;               // keys begin .. end - 1
+};
+
+__device__ __forceinline__ bool work_of(const AttnArgs &a, const AttnPlan &p, Work &k)
+{
+    // consecutive workgroups go to the 8 dies in turn: the row blocks of one
+    // key range follow each other on one die, whose cache then serves them
+    const uint32_t keyed = (uint32_t)a.batch * a.kv_heads * p.splits;    // (b, h, range)
+    const uint32_t id = blockIdx.x, nrb = p.row_blocks, whole = keyed / 8 * 8;
+    uint32_t kr, rb;
+    if (id < whole * nrb) {
+        const uint32_t q = id >> 3, n = q / nrb;
+        kr = n * 8 + (id & 7);
+        rb = q - n * nrb;
+    } else {
+        const uint32_t left = id - whole * nrb, n = left / nrb;
+        kr = whole + n;
+        rb = left - n * nrb;
+    }
+    const uint32_t bh = kr / (uint32_t)p.splits;
+    k.range = (int)(kr - bh * p.splits);
+    k.unit = bh * nrb + rb;
+    k.w = rows_of(a, nrb, k.unit);
+    if (k.w.rb * p.tiles * 16 >= k.w.T * a.group)
+        return false;
+    k.ranges = ranges_of(k.w, p.splits, p.chunk);
+    if (k.range >= k.ranges)
+        return false;
+    k.begin = k.range * p.chunk;
+    k.end = k.range == k.ranges - 1 ? k.w.L : k.begin + p.chunk;
+    return true;
+}
+
+// Fragment (16-row tile, output tile t) of a row block, as every wave holds
+// it: lane's row lane & 15, elements of rows 4 (lane >> 4) + 0..3 of the tile.
 template <int CT, int D>
-__device__ __forceinline__ void store_frag(const AttnArgs &a, const Rows &w, int QT, int qt, int t,
-                                           int lane, f4 o)
+__device__ __forceinline__ void store_frag(const AttnArgs &a, const Rows &w, int tiles, int tile,
+                                           int t, int lane, f4 o)
 {
     using G = Geo<CT, D>;
-    const int r = (w.rb * QT + qt) * 16 + (lane & 15);
-    if (r >= w.T * w.group)
+    const int r = (w.rb * tiles + tile) * 16 + (lane & 15);
+    if (r >= w.T * a.group)
         return;
-    const int node = r / w.group;
-    const int64_t at = (w.tok0 + node) * a.yts + (w.h * w.group + r - node * w.group) * a.yhs;
+    const int node = r / a.group;
+    const int64_t at = (w.tok0 + node) * a.yts + (w.h * a.group + r - node * a.group) * a.yhs;
     const int d0 = 16 * G::CW * (t / G::CW) + t % G::CW + 4 * (lane >> 4) * G::CW;
     uint16_t *y = (uint16_t *)a.y + at + d0;
 #pragma unroll
@@ -251,322 +312,502 @@ __device__ __forceinline__ void store_frag(const AttnArgs &a, const Rows &w, int
         y[G::CW * e] = a.dtype == TQ_BF16 ? f32_to_16<TQ_BF16>(o[e]) : f32_to_16<TQ_F16>(o[e]);
 }
 
+// One 16-row tile of a wave: queries in fp16 after the row's power of two, c
+// = what a score is times, and the running sums.
+template <int D> struct Query {
+    h8 q[D / 32];
+    float c, m, l;
+    int node;
+    f4 o[D / 16];
+};
+
+template <int D>
+__device__ __forceinline__ void load_query(Query<D> &x, const AttnArgs &a, const Rows &w, int tiles,
+                                           int tile, int lane)
+{
+    constexpr int NB = D / 32;
+    const int g = lane >> 4, r = (w.rb * tiles + tile) * 16 + (lane & 15);
+    const bool live = r < w.T * a.group;
+    x.node = live ? r / a.group : 0;
+    const int64_t at =
+        (w.tok0 + x.node) * a.qts + (w.h * a.group + (live ? r - x.node * a.group : 0)) * a.qhs;
+    float v[NB][8], big = 0.0f;
+#pragma unroll
+    for (int s = 0; s < NB; s++) {
+        if (a.dtype == TQ_BF16)
+            load_x8<TQ_BF16>(v[s], a.q, at + 32 * s + 8 * g);
+        else
+            load_x8<TQ_F16>(v[s], a.q, at + 32 * s + 8 * g);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            v[s][e] = live ? v[s][e] : 0.0f;
+            big = fmaxf(big, fabsf(v[s][e]));
+        }
+    }
+    big = fmaxf(big, __shfl_xor(big, 16));
+    big = fmaxf(big, __shfl_xor(big, 32));
+    // 2^k with big * 2^k in [2^14, 2^15); 1 for a row of zeros or with an infinity
+    const int ex = (int)(__builtin_bit_cast(uint32_t, big) >> 23);
+    const int k = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -126), 126);
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + k) << 23);
+    const float down = __builtin_bit_cast(float, (uint32_t)(127 - k) << 23);
+#pragma unroll
+    for (int s = 0; s < NB; s++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            x.q[s][e] = (_Float16)(v[s][e] * up);
+    x.c = a.scale * 1.44269504088896f * down;
+    x.m = NO_REF;
+    x.l = 0.0f;
+#pragma unroll
+    for (int t = 0; t < D / 16; t++)
+        x.o[t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// Whether new token n (counted from the cached ones) is seen by token node.
+__device__ __forceinline__ bool sees(const AttnArgs &a, const Rows &w, int node, int n)
+{
+    if (!a.mask)
+        return n <= node;
+    return (n >> 5) < a.mask_words &&
+           ((a.mask[(w.tok0 + node) * a.mask_stride + (n >> 5)] >> (n & 31)) & 1u);
+}
+
+// Scores of 32 keys from kb (some are new tokens, past the end, or on pages
+// that are not there): -inf where not seen.
+template <int D>
+__device__ __forceinline__ void mask_scores(f4 (&s)[2], const Query<D> &x, const AttnArgs &a,
+                                            const Rows &w, int kb, bool oka, bool okb, int g)
+{
+#pragma unroll
+    for (int T = 0; T < 2; T++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int key = kb + 16 * T + 4 * g + e, n = key - w.ctx;
+            bool see = key < w.L && (T ? okb : oka);
+            if (see && n >= 0)
+                see = sees(a, w, x.node, n);
+            if (!see)
+                s[T][e] = -__builtin_inff();
+        }
+}
+
+// Probabilities of 32 keys as the operand of the second product; the
+// reference, sum and outputs follow where a score passes it.
+template <int D>
+__device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
+{
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    top *= x.c;
+    if (__any(top > x.m + RAISE)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(x.m, top);
+        const float f = __builtin_amdgcn_exp2f(x.m - mn);
+        x.m = mn;
+        x.l *= f;
+#pragma unroll
+        for (int t = 0; t < D / 16; t++)
+            x.o[t] *= f;
+    }
+    const float ref = BIAS - x.m;
+    h8 p;
+    float sum = 0.0f;
+#pragma unroll
+    for (int T = 0; T < 2; T++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float y = __builtin_amdgcn_exp2f(fmaf(s[T][e], x.c, ref));
+            sum += y;
+            p[4 * T + e] = (_Float16)y;
+        }
+    x.l += sum;
+    return p;
+}
+
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Joins the KG waves that hold the same rows (rg, of RG groups) and stores
+// the outputs, or the range's sums where there are several.  red: RED
+// fragments of 64 lanes per wave.
+template <int CT, int D, int QT, int RG, int KG>
+__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const Work &k,
+                                       const AttnPlan &p, int rg, int kg, int lane, f4 *red,
+                                       float *ml, float *__restrict__ part,
+                                       float *__restrict__ part_ml)
+{
+    constexpr int NT = D / 16, TILES = RG * QT, F = TILES * NT, MINE = QT * NT;
+    const int col = lane & 15, g = lane >> 4;
+    float f[QT];
+#pragma unroll
+    for (int i = 0; i < QT; i++) {
+        x[i].l += __shfl_xor(x[i].l, 16);
+        x[i].l += __shfl_xor(x[i].l, 32);
+        f[i] = 1.0f;
+    }
+    if constexpr (KG > 1) {
+        const int mine = ((rg * KG + kg) * QT * 16 + col) * 2;
+        __syncthreads();
+        if (g == 0)
+#pragma unroll
+            for (int i = 0; i < QT; i++) {
+                ml[mine + i * 32] = x[i].m;
+                ml[mine + i * 32 + 1] = x[i].l;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < QT; i++) {
+            const float *q = ml + (rg * KG * QT * 16 + i * 16 + col) * 2;
+            float mm = NO_REF, ll = 0.0f;
+#pragma unroll
+            for (int n = 0; n < KG; n++)
+                mm = fmaxf(mm, q[n * QT * 32]);
+#pragma unroll
+            for (int n = 0; n < KG; n++)
+                ll += q[n * QT * 32 + 1] * __builtin_amdgcn_exp2f(q[n * QT * 32] - mm);
+            f[i] = __builtin_amdgcn_exp2f(x[i].m - mm);
+            x[i].m = mm;
+            x[i].l = ll;
+        }
+    }
+    const int64_t slot = (int64_t)k.unit * p.splits + k.range;
+    if (k.ranges > 1 && kg == 0 && g == 0) {
+#pragma unroll
+        for (int i = 0; i < QT; i++) {
+            float2 *q = (float2 *)part_ml + slot * (TILES * 16) + (rg * QT + i) * 16 + col;
+            *q = make_float2(x[i].m, x[i].l);
+        }
+    }
+    auto put = [&](int i, int t, f4 sum) {
+        if (k.ranges > 1) {
+            const int ff = (rg * QT + i) * NT + t;
+            *(f4 *)(part + ((slot * F + ff) * 64 + lane) * 4) = sum;
+        } else {
+            // nothing seen: zeros
+            store_frag<CT, D>(a, k.w, TILES, rg * QT + i, t, lane,
+                              x[i].l == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / x[i].l));
+        }
+    };
+    if constexpr (KG == 1) {
+#pragma unroll
+        for (int n = 0; n < MINE; n++)
+            put(n / NT, n % NT, x[n / NT].o[n % NT]);
+    } else {
+        constexpr int SHARE = RED / KG;
+        f4 *own = red + (rg * KG + kg) * (RED * 64) + lane;
+#pragma unroll
+        for (int f0 = 0; f0 < MINE; f0 += RED) {
+            if (f0)
+                __syncthreads();
+#pragma unroll
+            for (int n = 0; n < RED; n++)
+                if (f0 + n < MINE)
+                    own[n * 64] = x[(f0 + n) / NT].o[(f0 + n) % NT] * f[(f0 + n) / NT];
+            __syncthreads();
+            // wave kg adds fragments kg * SHARE ..; their tile is known at
+            // compile time only through the loop over waves
+#pragma unroll
+            for (int n = 0; n < RED; n++) {
+                if (f0 + n >= MINE || n / SHARE != kg)
+                    continue;
+                const f4 *q = red + rg * KG * (RED * 64) + n * 64 + lane;
+                f4 sum = q[0];
+#pragma unroll
+                for (int e = 1; e < KG; e++)
+                    sum += q[e * (RED * 64)];
+                put((f0 + n) / NT, (f0 + n) % NT, sum);
+            }
+        }
+    }
+}
+
+// Page numbers of two neighbouring tiles; -1 where there is nothing to read.
+struct Pages {
+    int a, b;
+};
+
+__device__ __forceinline__ int page_at(const AttnArgs &a, const int32_t *table, int key, int end)
+{
+    const int i = key >> a.log_page;
+    if (key >= end || i >= a.table_pages)
+        return -1;
+    const int page = load_uniform(table + i);
+    return (int64_t)(uint32_t)page < a.pages ? page : -1;
+}
+
+// Up to 32 rows: every wave has its own keys.
 template <int CT, int D, int QT>
-__global__ __launch_bounds__(THREADS) void k_attn(AttnArgs a, int row_blocks, int splits, int chunk,
-                                                  float *__restrict__ part,
+__global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(AttnArgs a, AttnPlan p, float *__restrict__ part,
                                                   float *__restrict__ part_ml)
 {
     using G = Geo<CT, D>;
-    __shared__ f4 red[WAVES][RED][64];
-    __shared__ float ml[WAVES][QT * 16][2];
-
-    // consecutive workgroups go to the 8 dies in turn: the row blocks of one
-    // key range follow each other on one die, whose cache then serves them
-    const int64_t keyed = (int64_t)a.batch * a.kv_heads * splits;    // (b, h, range)
-    const int64_t id = blockIdx.x;
-    int64_t kr;
-    int rb;
-    if (id < keyed / 8 * 8 * row_blocks) {
-        const int64_t q = id >> 3;
-        kr = q / row_blocks * 8 + (id & 7);
-        rb = (int)(q % row_blocks);
-    } else {
-        const int64_t left = id - keyed / 8 * 8 * row_blocks;
-        kr = keyed / 8 * 8 + left / row_blocks;
-        rb = (int)(left % row_blocks);
-    }
-    const int range = (int)(kr % splits);
-    const int64_t unit = kr / splits * row_blocks + rb;
-    const Rows w = rows_of(a, row_blocks, unit);
-    if (rb * (16 * QT) >= w.T * w.group)
+    __shared__ f4 red[WAVES * RED * 64];
+    __shared__ float ml[WAVES * QT * 16 * 2];
+    Work k;
+    if (!work_of(a, p, k))
         return;
-    const int ranges = ranges_of(w, splits, chunk);
-    if (range >= ranges)
-        return;
-    const int begin = range * chunk;
-    const int end = range == ranges - 1 ? w.L : begin + chunk;
-
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int col = lane & 15, g = lane >> 4;
+    const Rows &w = k.w;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
     const int P = 1 << a.log_page;
     const int64_t cb = chunk_bytes(CT, D, P);
     const int32_t *table = a.table + w.b * a.table_stride;
 
-    // queries: fp16 after the row's power of two, c = what a score is times
-    h8 q[QT][G::NB];
-    float c[QT], m[QT], l[QT];
-    int node[QT];
-    f4 o[QT][G::NT];
+    Query<D> x[QT];
 #pragma unroll
-    for (int i = 0; i < QT; i++) {
-        const int r = (rb * QT + i) * 16 + col;
-        const bool live = r < w.T * w.group;
-        node[i] = live ? r / w.group : 0;
-        const int64_t at =
-            (w.tok0 + node[i]) * a.qts + (w.h * w.group + (live ? r - node[i] * w.group : 0)) * a.qhs;
-        float x[G::NB][8], big = 0.0f;
-#pragma unroll
-        for (int s = 0; s < G::NB; s++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                x[s][e] = live ? load_16(a.q, at + 32 * s + 8 * g + e, a.dtype) : 0.0f;
-                big = fmaxf(big, fabsf(x[s][e]));
-            }
-        big = fmaxf(big, __shfl_xor(big, 16));
-        big = fmaxf(big, __shfl_xor(big, 32));
-        // 2^k with big * 2^k in [2^14, 2^15); 1 for a row of zeros or with an infinity
-        const int ex = (int)(__builtin_bit_cast(uint32_t, big) >> 23);
-        const int k = ex == 0 || ex == 255 ? 0 : min(max(141 - ex, -126), 126);
-        const float up = __builtin_bit_cast(float, (uint32_t)(127 + k) << 23);
-        const float down = __builtin_bit_cast(float, (uint32_t)(127 - k) << 23);
-#pragma unroll
-        for (int s = 0; s < G::NB; s++)
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                q[i][s][e] = (_Float16)(x[s][e] * up);
-        c[i] = a.scale * 1.44269504088896f * down;
-        m[i] = NO_REF;
-        l[i] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < G::NT; t++)
-            o[i][t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int i = 0; i < QT; i++)
+        load_query<D>(x[i], a, w, QT, i, lane);
 
-    // page of each of the two tiles at key kb; -1 where the table has none
-    auto page_at = [&](int key) {
-        const int i = key >> a.log_page;
-        return i < a.table_pages && key < end ? table[i] : -1;
+    auto pages_at = [&](int kb) {
+        return Pages{page_at(a, table, kb, k.end), page_at(a, table, kb + 16, k.end)};
     };
-    auto mapped = [&](int page) { return page >= 0 && page < a.pages; };
-    struct Pages {
-        int a, b;
-    };
-    auto pages_at = [&](int kb) { return Pages{page_at(kb), page_at(kb + 16)}; };
-
-    auto load = [&](Raw<CT, D> &raw, Pages &pg, int kb) {
-        pg.a = uniform(pg.a);
-        pg.b = uniform(pg.b);
-        if (kb >= end)
+    auto load = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
+        if (kb >= k.end)
             return;
-        // an unmapped tile's loads go to page 0; its keys are masked
-        const int64_t pa = mapped(pg.a) ? pg.a : 0, pb = mapped(pg.b) ? pg.b : 0;
-        const int64_t oa = (pa * a.kv_heads + w.h) * cb, ob = (pb * a.kv_heads + w.h) * cb;
-        load_tile<CT, D, 0>(raw, a.kc + oa, a.vc + oa, kb & (P - 1), P, lane);
-        load_tile<CT, D, 1>(raw, a.kc + ob, a.vc + ob, (kb + 16) & (P - 1), P, lane);
+        // a tile that is not there reads page 0; its keys are masked
+        const int64_t oa = ((int64_t)max(pg.a, 0) * a.kv_heads + w.h) * cb;
+        const int64_t ob = ((int64_t)max(pg.b, 0) * a.kv_heads + w.h) * cb;
+        load_tile<CT, D>(raw[0], a.kc + oa, a.vc + oa, kb & (P - 1), P, lane);
+        load_tile<CT, D>(raw[1], a.kc + ob, a.vc + ob, (kb + 16) & (P - 1), P, lane);
     };
-
-    auto compute = [&](Raw<CT, D> &raw, const Pages &pg, int kb) {
+    auto compute = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
         f4 s[QT][2];
-#pragma unroll
-        for (int T = 0; T < 2; T++) {
+        auto scores = [&](const Tile<CT, D> &tile, int T) {
 #pragma unroll
             for (int i = 0; i < QT; i++)
                 s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int b = 0; b < G::NB; b++) {
-                const h8 kf = key_frag<CT, D>(raw, T, b);
+                const h8 kf = key_frag<CT, D>(tile, b);
 #pragma unroll
                 for (int i = 0; i < QT; i++)
-                    s[i][T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[i][b], s[i][T], 0, 0, 0);
+                    s[i][T] = mfma(kf, x[i].q[b], s[i][T]);
             }
-        }
-        const bool oka = mapped(pg.a), okb = mapped(pg.b);
-        if (kb + STEP > w.ctx || !oka || !okb) {
-            // some keys are new tokens, past the end or unmapped
-#pragma unroll
-            for (int T = 0; T < 2; T++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int key = kb + 16 * T + 4 * g + e;
-                    const bool there = key < w.L && (T ? okb : oka);
-                    const int n = key - w.ctx;
-#pragma unroll
-                    for (int i = 0; i < QT; i++) {
-                        bool see = there;
-                        if (there && n >= 0) {
-                            if (!a.mask)
-                                see = n <= node[i];
-                            else
-                                see = (n >> 5) < a.mask_words &&
-                                      ((a.mask[(w.tok0 + node[i]) * a.mask_stride + (n >> 5)] >>
-                                        (n & 31)) & 1u);
-                        }
-                        if (!see)
-                            s[i][T][e] = -__builtin_inff();
-                    }
-                    // what a value block holds where no token was written
-                    // must not meet a probability of 0 as NaN
-#pragma unroll
-                    for (int h = 0; h < G::NH; h++) {
-                        uint32_t &word = e < 2 ? raw.vs[T][h].x : raw.vs[T][h].y;
-                        const int sh = 16 * (e & 1);
-                        const bool odd = ((word >> sh) & 0x7C00u) == 0x7C00u;
-                        if (!there || (n >= 0 && odd))
-                            word &= ~(0xFFFFu << sh);
-                    }
-                }
-        }
-        h8 p[QT];
-#pragma unroll
-        for (int i = 0; i < QT; i++) {
-            float top = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                              fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
-            top *= c[i];
-            if (__any(top > m[i] + RAISE)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float mn = fmaxf(m[i], top);
-                const float f = __builtin_amdgcn_exp2f(m[i] - mn);
-                m[i] = mn;
-                l[i] *= f;
-#pragma unroll
-                for (int t = 0; t < G::NT; t++)
-                    o[i][t] *= f;
-            }
-            const float ref = BIAS - m[i];
-#pragma unroll
-            for (int T = 0; T < 2; T++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(s[i][T][e], c[i], ref));
-                    l[i] += x;
-                    p[i][4 * T + e] = (_Float16)x;
-                }
-        }
-#pragma unroll
-        for (int t = 0; t < G::NT; t++) {
-            const h8 vf = value_frag<CT, D>(raw, t / G::CW, t % G::CW);
+        };
+        scores(raw[0], 0);
+        scores(raw[1], 1);
+        if (kb + STEP > w.ctx || pg.a < 0 || pg.b < 0) {
 #pragma unroll
             for (int i = 0; i < QT; i++)
-                o[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[i], o[i][t], 0, 0, 0);
+                mask_scores<D>(s[i], x[i], a, w, kb, pg.a >= 0, pg.b >= 0, g);
+            drop_values<CT, D>(raw[0], kb + 4 * g, pg.a >= 0, w.ctx, w.L);
+            drop_values<CT, D>(raw[1], kb + 16 + 4 * g, pg.b >= 0, w.ctx, w.L);
+        }
+        h8 pr[QT];
+#pragma unroll
+        for (int i = 0; i < QT; i++)
+            pr[i] = softmax_step<D>(s[i], x[i]);
+#pragma unroll
+        for (int t = 0; t < G::NT; t++) {
+            Frag f;
+            value_half<CT, D>(raw[0], t, f.p[0], f.p[1]);
+            value_half<CT, D>(raw[1], t, f.p[2], f.p[3]);
+#pragma unroll
+            for (int i = 0; i < QT; i++)
+                x[i].o[t] = mfma(f.v, pr[i], x[i].o[t]);
         }
     };
 
-    // two steps in flight: one computed, the next one's codes and the page
-    // numbers of the one after that being loaded
-    int kb = begin + wave * STEP;
-    if (kb < end) {
-        Raw<CT, D> ra, rb2;
+    // one step computed, the next one's codes on their way, and the page
+    // numbers of the one after that
+    int kb = k.begin + wave * STEP;
+    if (kb < k.end) {
+        Tile<CT, D> ra[2], rb[2];
         Pages pa = pages_at(kb), pb = pages_at(kb + STRIDE);
         load(ra, pa, kb);
         for (;;) {
-            load(rb2, pb, kb + STRIDE);
+            load(rb, pb, kb + STRIDE);
             Pages pn = pages_at(kb + 2 * STRIDE);
             compute(ra, pa, kb);
             pa = pn;
             kb += STRIDE;
-            if (kb >= end)
+            if (kb >= k.end)
                 break;
             load(ra, pa, kb + STRIDE);
             pn = pages_at(kb + 2 * STRIDE);
-            compute(rb2, pb, kb);
+            compute(rb, pb, kb);
             pb = pn;
             kb += STRIDE;
-            if (kb >= end)
+            if (kb >= k.end)
                 break;
         }
     }
+    finish<CT, D, QT, 1, WAVES>(x, a, k, p, 0, wave, lane, red, ml, part, part_ml);
+}
 
-    // join the four waves: references, then the outputs RED fragments at a time
+// More rows: RG groups of waves with QT * 16 rows each, KG = 4 / RG waves per
+// group.  Every wave dequantizes one 16-key tile of 64 keys into LDS, in the
+// fragments of the matrix instructions, while the codes of the next 64 are on
+// their way; then each reads what its rows need (KG = 2: one 32-key half).
+template <int CT, int D, int QT, int RG>
+__global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p,
+                                                       float *__restrict__ part,
+                                                       float *__restrict__ part_ml)
+{
+    using G = Geo<CT, D>;
+    constexpr int KG = WAVES / RG, KEYS = 16 * WAVES;
+    constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
+    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
+    __shared__ h8 lds[STAGE > JOIN ? STAGE : JOIN];
+    __shared__ float ml[WAVES * QT * 16 * 2];
+    h8 *kf = lds, *vf = lds + K_FRAGS * 64;
+    Work k;
+    if (!work_of(a, p, k))
+        return;
+    const Rows &w = k.w;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
+    const int rg = wave / KG, kg = wave % KG;
+    const int P = 1 << a.log_page;
+    const int64_t cb = chunk_bytes(CT, D, P);
+    const int32_t *table = a.table + w.b * a.table_stride;
+
+    Query<D> x[QT];
 #pragma unroll
-    for (int i = 0; i < QT; i++) {
-        l[i] += __shfl_xor(l[i], 16);
-        l[i] += __shfl_xor(l[i], 32);
-        if (g == 0) {
-            ml[wave][i * 16 + col][0] = m[i];
-            ml[wave][i * 16 + col][1] = l[i];
+    for (int i = 0; i < QT; i++)
+        load_query<D>(x[i], a, w, RG * QT, rg * QT + i, lane);
+
+    Tile<CT, D> raw;
+    int page[WAVES];                             // of the tiles on their way
+    auto load = [&](int kb) {
+        if (kb >= k.end)
+            return;
+#pragma unroll
+        for (int n = 0; n < WAVES; n++)
+            page[n] = page_at(a, table, kb + 16 * n, k.end);
+        int mine = page[0];
+#pragma unroll
+        for (int n = 1; n < WAVES; n++)
+            mine = wave == n ? page[n] : mine;
+        const int64_t o = ((int64_t)max(mine, 0) * a.kv_heads + w.h) * cb;
+        load_tile<CT, D>(raw, a.kc + o, a.vc + o, (kb + 16 * wave) & (P - 1), P, lane);
+    };
+    load(k.begin);
+    for (int kb = k.begin; kb < k.end; kb += KEYS) {
+        bool ok[WAVES];
+        bool all = kb + KEYS <= w.ctx;
+#pragma unroll
+        for (int n = 0; n < WAVES; n++) {
+            ok[n] = page[n] >= 0;
+            all = all && ok[n];
         }
-    }
-    __syncthreads();
-    float all_m[QT], all_l[QT], f[QT];
+        if (!all) {
+            bool mine = ok[0];
 #pragma unroll
-    for (int i = 0; i < QT; i++) {
-        float mm = NO_REF;
-#pragma unroll
-        for (int k = 0; k < WAVES; k++)
-            mm = fmaxf(mm, ml[k][i * 16 + col][0]);
-        float ll = 0.0f;
-#pragma unroll
-        for (int k = 0; k < WAVES; k++)
-            ll += ml[k][i * 16 + col][1] * __builtin_amdgcn_exp2f(ml[k][i * 16 + col][0] - mm);
-        all_m[i] = mm;
-        all_l[i] = ll;
-        f[i] = __builtin_amdgcn_exp2f(m[i] - mm);
-    }
-    constexpr int F = QT * G::NT;
-    const int64_t slot = unit * splits + range;
-    if (ranges > 1 && wave == 0 && g == 0) {
-#pragma unroll
-        for (int i = 0; i < QT; i++) {
-            part_ml[(slot * (QT * 16) + i * 16 + col) * 2] = all_m[i];
-            part_ml[(slot * (QT * 16) + i * 16 + col) * 2 + 1] = all_l[i];
+            for (int n = 1; n < WAVES; n++)
+                mine = wave == n ? ok[n] : mine;
+            drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, mine, w.ctx, w.L);
         }
-    }
+        __syncthreads();                         // the last keys are used up
 #pragma unroll
-    for (int f0 = 0; f0 < F; f0 += RED) {
-        if (f0)
-            __syncthreads();
+        for (int b = 0; b < G::NB; b++)
+            kf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
 #pragma unroll
-        for (int k = 0; k < RED; k++)
-            if (f0 + k < F)
-                red[wave][k][lane] = o[(f0 + k) / G::NT][(f0 + k) % G::NT] * f[(f0 + k) / G::NT];
+        for (int t = 0; t < G::NT; t++) {
+            union {
+                h2 h[2];
+                u2 u;
+            } v;
+            value_half<CT, D>(raw, t, v.h[0], v.h[1]);
+            ((u2 *)&vf[((wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
+        }
+        load(kb + KEYS);
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < RED / WAVES; k++) {
-            const int kk = wave * (RED / WAVES) + k, ff = f0 + kk;
-            if (ff >= F)
+        for (int n = 0; n < 2; n++) {
+            if (KG == 2 && n != kg)
                 continue;
-            const f4 sum = (red[0][kk][lane] + red[1][kk][lane]) +
-                           (red[2][kk][lane] + red[3][kk][lane]);
-            if (ranges > 1) {
-                *(f4 *)(part + ((slot * F + ff) * 64 + lane) * 4) = sum;
-            } else {
-                float ll = all_l[0];
+            const int kp = kb + STEP * n;
+            if (kp >= k.end)
+                continue;
+            f4 s[QT][2];
 #pragma unroll
-                for (int i = 1; i < QT; i++)
-                    ll = ff / G::NT == i ? all_l[i] : ll;
-                // nothing seen: zeros
-                store_frag<CT, D>(a, w, QT, ff / G::NT, ff % G::NT, lane,
-                                  ll == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / ll));
+            for (int T = 0; T < 2; T++) {
+#pragma unroll
+                for (int i = 0; i < QT; i++)
+                    s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int b = 0; b < G::NB; b++) {
+                    const h8 kv = kf[((2 * n + T) * G::NB + b) * 64 + lane];
+#pragma unroll
+                    for (int i = 0; i < QT; i++)
+                        s[i][T] = mfma(kv, x[i].q[b], s[i][T]);
+                }
+            }
+            if (!all)
+#pragma unroll
+                for (int i = 0; i < QT; i++)
+                    mask_scores<D>(s[i], x[i], a, w, kp, ok[2 * n], ok[2 * n + 1], g);
+            h8 pr[QT];
+#pragma unroll
+            for (int i = 0; i < QT; i++)
+                pr[i] = softmax_step<D>(s[i], x[i]);
+#pragma unroll
+            for (int t = 0; t < G::NT; t++) {
+                const h8 vv = vf[(n * G::NT + t) * 64 + lane];
+#pragma unroll
+                for (int i = 0; i < QT; i++)
+                    x[i].o[t] = mfma(vv, pr[i], x[i].o[t]);
             }
         }
     }
+    finish<CT, D, QT, RG, KG>(x, a, k, p, rg, kg, lane, (f4 *)lds, ml, part, part_ml);
 }
 
-// One wave per fragment: the ranges' sums, each rescaled to the largest
-// reference, in range order.
+// One workgroup per fragment: the ranges' sums, each rescaled to the largest
+// reference.  Wave n adds ranges n, n + 4, ... (four loads in flight), the
+// waves' sums are joined through LDS.
 template <int CT, int D>
-__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, int QT, int row_blocks,
-                                                          int splits, int chunk,
+__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p,
                                                           const float *__restrict__ part,
                                                           const float *__restrict__ part_ml)
 {
-    using G = Geo<CT, D>;
-    const int64_t unit = blockIdx.x;
-    const Rows w = rows_of(a, row_blocks, unit);
-    if (w.rb * (16 * QT) >= w.T * w.group)
+    constexpr int NT = D / 16;
+    __shared__ f4 red[WAVES][64];
+    __shared__ float redl[WAVES][64];
+    const uint32_t unit = blockIdx.x;
+    const Rows w = rows_of(a, p.row_blocks, unit);
+    if (w.rb * p.tiles * 16 >= w.T * a.group)
         return;
-    const int ranges = ranges_of(w, splits, chunk);
-    const int F = QT * G::NT;
-    const int lane = threadIdx.x & 63, ff = blockIdx.y * WAVES + (threadIdx.x >> 6);
-    if (ranges == 1 || ff >= F)
+    const int ranges = ranges_of(w, p.splits, p.chunk);
+    if (ranges == 1)
         return;
-    const int qt = ff / G::NT;
-    const float *mlp = part_ml + (unit * splits * (QT * 16) + qt * 16 + (lane & 15)) * 2;
-    const int64_t ms = QT * 32;
+    const int F = p.tiles * NT, ff = blockIdx.y, tile = ff / NT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t slot = (int64_t)unit * p.splits;
+    const float2 *mlp = (const float2 *)part_ml + slot * (p.tiles * 16) + tile * 16 + (lane & 15);
+    const int ms = p.tiles * 16;
     float mm = NO_REF;
-    for (int k = 0; k < ranges; k++)
-        mm = fmaxf(mm, mlp[k * ms]);
+    for (int n = lane >> 4; n < ranges; n += 4)
+        mm = fmaxf(mm, mlp[n * ms].x);
+    mm = fmaxf(mm, __shfl_xor(mm, 16));
+    mm = fmaxf(mm, __shfl_xor(mm, 32));
     float ll = 0.0f;
     f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < ranges; k++) {
-        const float f = __builtin_amdgcn_exp2f(mlp[k * ms] - mm);
-        ll += f * mlp[k * ms + 1];
-        sum += f * *(const f4 *)(part + (((unit * splits + k) * F + ff) * 64 + lane) * 4);
+    const float *q = part + ((slot * F + ff) * 64 + lane) * 4;
+#pragma unroll 4
+    for (int n = wave; n < ranges; n += WAVES) {
+        const float2 t = mlp[n * ms];
+        const float f = __builtin_amdgcn_exp2f(t.x - mm);
+        ll += f * t.y;
+        sum += f * *(const f4 *)(q + (int64_t)n * F * 256);
     }
-    store_frag<CT, D>(a, w, QT, qt, ff % G::NT, lane,
+    red[wave][lane] = sum;
+    redl[wave][lane] = ll;
+    __syncthreads();
+    if (wave)
+        return;
+    sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    ll = (redl[0][lane] + redl[1][lane]) + (redl[2][lane] + redl[3][lane]);
+    store_frag<CT, D>(a, w, p.tiles, tile, ff % NT, lane,
                       ll == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / ll));
 }
+
+// Row tiles per wave with more than 32 rows: two share each fragment read;
+// with 256 elements a head the registers hold one.
+constexpr int rows_qt(int D) { return D <= 128 ? 2 : 1; }
 
 template <int CT, int D>
 hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStream_t s)
@@ -575,26 +816,23 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     const int64_t blocks = units * p.splits;
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
-    const int F = p.qt * (D / 16);
+    const int F = p.tiles * (D / 16);
     float *part = (float *)scratch;
     float *ml = part ? part + (size_t)units * p.splits * F * 256 : nullptr;
     const dim3 grid((unsigned)blocks);
-    switch (p.qt) {
-    case 1: k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(a, p.row_blocks, p.splits, p.chunk, part, ml); break;
-    case 2: k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p.row_blocks, p.splits, p.chunk, part, ml); break;
-    default:
-        if constexpr (D <= 128) {
-            k_attn<CT, D, 4><<<grid, THREADS, 0, s>>>(a, p.row_blocks, p.splits, p.chunk, part, ml);
-            break;
-        } else {
-            return hipErrorInvalidValue;
-        }
-    }
+    constexpr int QT = rows_qt(D);
+    if (p.row_groups == 4)
+        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+    else if (p.row_groups == 2)
+        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+    else if (p.tiles == 1)
+        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+    else if constexpr (D <= 128)
+        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p, part, ml);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    const dim3 cgrid((unsigned)units, (unsigned)((F + WAVES - 1) / WAVES));
-    k_attn_combine<CT, D><<<cgrid, THREADS, 0, s>>>(a, p.qt, p.row_blocks, p.splits, p.chunk, part, ml);
+    k_attn_combine<CT, D><<<dim3((unsigned)units, (unsigned)F), THREADS, 0, s>>>(a, p, part, ml);
     return hipGetLastError();
 }
 
@@ -617,11 +855,21 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
 {
     AttnPlan p;
     const int64_t rows = max_nodes * (heads / kv_heads);
-    p.qt = rows <= 16 ? 1 : (rows <= 32 || D > 128 ? 2 : 4);
-    p.row_blocks = (int)((rows + 16 * p.qt - 1) / (16 * p.qt));
+    const int qt = rows_qt(D);
+    if (rows <= 16) {
+        p.row_groups = 1;
+        p.tiles = 1;
+    } else if (rows <= 32 && D <= 128) {
+        p.row_groups = 1;
+        p.tiles = 2;
+    } else {
+        p.row_groups = rows <= 32 * qt ? 2 : 4;
+        p.tiles = p.row_groups * qt;
+    }
+    p.row_blocks = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
     const int64_t units = batch * kv_heads * p.row_blocks;
-    const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(units, 1));
-    const int64_t most = std::max<int64_t>(1, (max_keys + 255) / 256);
+    const int64_t want = std::max<int64_t>(1, TARGET_GROUPS / std::max<int64_t>(units, 1));
+    const int64_t most = std::max<int64_t>(1, (max_keys + MIN_CHUNK - 1) / MIN_CHUNK);
     const int64_t s = std::min(want, most);
     const int64_t chunk = ((max_keys + s - 1) / s + STRIDE - 1) / STRIDE * STRIDE;
     p.chunk = (int)std::max<int64_t>(chunk, STRIDE);
@@ -634,7 +882,7 @@ size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_he
     if (p.splits == 1)
         return 0;
     const size_t units = (size_t)batch * kv_heads * p.row_blocks * p.splits;
-    return units * ((size_t)p.qt * (D / 16) * 256 + p.qt * 32) * sizeof(float);
+    return units * p.tiles * ((size_t)(D / 16) * 256 + 32) * sizeof(float);
 }
 
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,

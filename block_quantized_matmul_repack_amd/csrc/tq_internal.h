@@ -419,12 +419,14 @@ struct AttnArgs {
     const uint32_t *mask;            // [tokens][mask_words] or null
     int64_t mask_stride;             // words
     int64_t pages, tokens;
-    int table_pages, log_page, batch, heads, kv_heads, max_nodes, mask_words, dtype;
+    int table_pages, log_page, batch, kv_heads, group, max_nodes, mask_words, dtype;
+                                     // group: query heads per key head
     float scale;
 };
-// Keys a launch splits each sequence over, for a fixed launch geometry.
+// Launch geometry, from host sizes alone: 16-row tiles per workgroup (in
+// row_groups groups of waves), row blocks of them, key ranges of `chunk`.
 struct AttnPlan {
-    int qt, row_blocks, splits, chunk;   // query tiles of 16 per wave; key ranges of `chunk`
+    int tiles, row_groups, row_blocks, splits, chunk;
 };
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys);
