@@ -56,7 +56,6 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 template <int CT, int D> struct Geo {
     static constexpr int NB = D / 32;            // 32-element blocks = matrix steps of Q K^T
@@ -78,59 +77,73 @@ template <int CT, int D> struct Tile {
     uint32_t vs[2 * G::NH];
 };
 
-template <int N> __device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *p)
+// N dwords (aligned to 4 N bytes, N = 3 to 4) at byte v + s of a buffer, v per
+// lane and s uniform; zeros past its end.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t *w, __amdgpu_buffer_rsrc_t b, int v, int s)
 {
     if constexpr (N == 4) {
-        const u4 x = *(const u4 *)p;
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(b, v, s, 0);
+        w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
     } else if constexpr (N == 3) {
-        const uint32_t *q = (const uint32_t *)p;
-        w[0] = q[0]; w[1] = q[1]; w[2] = q[2];
+        const auto x = __builtin_amdgcn_raw_buffer_load_b96(b, v, s, 0);
+        w[0] = x[0]; w[1] = x[1]; w[2] = x[2];
     } else if constexpr (N == 2) {
-        const u2 x = *(const u2 *)p;
-        w[0] = x.x; w[1] = x.y;
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(b, v, s, 0);
+        w[0] = x[0]; w[1] = x[1];
     } else {
-        w[0] = *(const uint32_t *)p;
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, v, s, 0);
     }
 }
 
-// The 16 keys at position pos (uniform) of the page whose chunks start at kc
-// and vc (uniform): uniform bases, one lane offset each.
+// The chunks of one page and head; of no bytes where there is no page, so
+// that its loads read zeros and move nothing.
+struct Chunks {
+    __amdgpu_buffer_rsrc_t k, v;
+};
+
+__device__ __forceinline__ Chunks chunks_at(const AttnArgs &a, int page, int h, int bytes)
+{
+    const int64_t at = ((int64_t)max(page, 0) * a.kv_heads + h) * bytes;
+    const int n = page < 0 ? 0 : bytes;
+    return Chunks{make_rsrc(a.kc + at, n), make_rsrc(a.vc + at, n)};
+}
+
+// The 16 keys at position pos (uniform) of a page.
 template <int CT, int D>
-__device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const uint8_t *kc, const uint8_t *vc,
-                                          int pos, int P, int lane)
+__device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
+                                          int lane)
 {
     using G = Geo<CT, D>;
     const int r = lane & 15, g = lane >> 4;
-    const uint8_t *kp = kc + pos * G::TB;
+    const int kl = r * G::TB + k_piece_off<CT, D>(0, g), ks = pos * G::TB;
     if constexpr (CT == TQ_Q8_0 && D % 64 != 0) {
 #pragma unroll
         for (int s = 0; s < G::NB; s++)
-            load_words<2>(raw.k + 2 * s, kp + (r * G::TB + k_piece_off<CT, D>(s, g)));
+            load_words<2>(raw.k + 2 * s, c.k, kl + 32 * s, ks);
     } else if constexpr (CT == TQ_Q4_0 && D % 128 != 0) {
-        load_words<G::KW>(raw.k, kp + (r * G::TB + k_piece_off<CT, D>(0, g)));
+        load_words<G::KW>(raw.k, c.k, kl, ks);
     } else {
-        constexpr int PER = CT == TQ_Q8_0 ? 2 : 4;           // blocks per 16 bytes
 #pragma unroll
-        for (int s = 0; s < G::NB; s += PER)
-            load_words<4>(raw.k + s * (4 / PER), kp + (r * G::TB + k_piece_off<CT, D>(s, g)));
+        for (int s = 0; s < G::KW; s += 4)       // 64 bytes of every key
+            load_words<4>(raw.k + s, c.k, kl + 16 * s, ks);
     }
-    const uint8_t *ks = kc + (P * G::TB + pos * (G::NB * 2)) + r * (G::NB * 2);
+    const int scales = P * G::TB;
     if constexpr (G::NB == 3) {
-        const uint16_t *q = (const uint16_t *)ks;
-        raw.ks[0] = q[0] | ((uint32_t)q[1] << 16);
-        raw.ks[1] = q[2];
+        raw.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6, scales + pos * 6, 0) |
+                    (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6 + 2,
+                                                                             scales + pos * 6, 0) << 16;
+        raw.ks[1] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6 + 4, scales + pos * 6, 0);
     } else {
-        load_words<G::NB / 2>(raw.ks, ks);
+        load_words<G::NB / 2>(raw.ks, c.k, r * (G::NB * 2), scales + pos * (G::NB * 2));
     }
-    const uint8_t *vp = vc + pos * G::TB;
-    const uint8_t *vs = vc + (P * G::TB + pos * 2);
+    const int vl = g * (4 * G::TB) + r * (G::VL * 4);
+    const int sl = ((G::CW * r / 32) * P + 4 * g) * 2;
 #pragma unroll
     for (int h = 0; h < G::NH; h++) {
-        load_words<G::VL>(raw.v + h * G::VL,
-                          vp + (g * (4 * G::TB) + (16 * h + r) * (G::VL * 4)));
-        const int block = (16 * G::CW * h + G::CW * r) / 32;
-        load_words<2>(raw.vs + 2 * h, vs + (block * P + 4 * g) * 2);
+        load_words<G::VL>(raw.v + h * G::VL, c.v, vl + h * (64 * G::VL), pos * G::TB);
+        // 16 * CW elements further: CW / 2 blocks of P scales
+        load_words<2>(raw.vs + 2 * h, c.v, sl, scales + pos * 2 + h * G::CW * P);
     }
 }
 
@@ -201,18 +214,20 @@ __device__ __forceinline__ void value_half(const Tile<CT, D> &raw, int t, h2 &a,
 template <int CT, int D>
 __device__ __forceinline__ void drop_values(Tile<CT, D> &raw, int key, bool there, int ctx, int L)
 {
+    const int left = there ? L - key : 0;        // tokens of the four that are there
     auto keep = [&](uint32_t w, int k) {
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const uint32_t half = 0xFFFFu << (16 * i), e = 0x7C00u << (16 * i);
-            const bool in = there && k + i < L;
-            w = !in || (k + i >= ctx && (w & e) == e) ? w & ~half : w;
+            const uint32_t e = 0x7C00u << (16 * i);
+            const int odd = (int)(key + k + i >= ctx) & (int)((w & e) == e);
+            m |= (int)(k + i < left) & (odd ^ 1) ? 0xFFFFu << (16 * i) : 0u;
         }
-        return w;
+        return w & m;
     };
 #pragma unroll
     for (int h = 0; h < 2 * Geo<CT, D>::NH; h++)
-        raw.vs[h] = keep(raw.vs[h], key + 2 * (h & 1));
+        raw.vs[h] = keep(raw.vs[h], 2 * (h & 1));
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -364,13 +379,29 @@ __device__ __forceinline__ void load_query(Query<D> &x, const AttnArgs &a, const
         x.o[t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
-// Whether new token n (counted from the cached ones) is seen by token node.
-__device__ __forceinline__ bool sees(const AttnArgs &a, const Rows &w, int node, int n)
+// Which of the keys key .. key + 3 token `node` sees, as 4 bits: all cached
+// ones, new ones by its mask row (or up to itself), none past the end or on a
+// page that is not there.
+__device__ __forceinline__ uint32_t seen4(const AttnArgs &a, const Rows &w, int node, int key,
+                                          bool there)
 {
-    if (!a.mask)
-        return n <= node;
-    return (n >> 5) < a.mask_words &&
-           ((a.mask[(w.tok0 + node) * a.mask_stride + (n >> 5)] >> (n & 31)) & 1u);
+    const int n = max(key - w.ctx, -4);
+    uint32_t bits;
+    if (a.mask) {
+        const uint32_t *row = a.mask + (w.tok0 + node) * a.mask_stride;
+        const int first = max(n, 0) >> 5, last = first + 1;
+        const uint32_t lo = row[min(first, a.mask_words - 1)];
+        const uint32_t hi = row[min(last, a.mask_words - 1)];
+        const uint64_t both = (first < a.mask_words ? (uint64_t)lo : 0) |
+                              (last < a.mask_words ? (uint64_t)hi << 32 : 0);
+        bits = (uint32_t)(both >> (max(n, 0) & 31));
+    } else {
+        bits = (1u << min(max(node - max(n, 0) + 1, 0), 4)) - 1;
+    }
+    const int before = max(-n, 0);               // keys of the four that are cached
+    bits = (bits << before) | ((1u << before) - 1);
+    const int left = min(max(w.L - key, 0), 4);
+    return there ? bits & ((1u << left) - 1) : 0;
 }
 
 // Scores of 32 keys from kb (some are new tokens, past the end, or on pages
@@ -379,17 +410,13 @@ template <int D>
 __device__ __forceinline__ void mask_scores(f4 (&s)[2], const Query<D> &x, const AttnArgs &a,
                                             const Rows &w, int kb, bool oka, bool okb, int g)
 {
+    const uint32_t b0 = seen4(a, w, x.node, kb + 4 * g, oka);
+    const uint32_t b1 = seen4(a, w, x.node, kb + 16 + 4 * g, okb);
 #pragma unroll
-    for (int T = 0; T < 2; T++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int key = kb + 16 * T + 4 * g + e, n = key - w.ctx;
-            bool see = key < w.L && (T ? okb : oka);
-            if (see && n >= 0)
-                see = sees(a, w, x.node, n);
-            if (!see)
-                s[T][e] = -__builtin_inff();
-        }
+    for (int e = 0; e < 4; e++) {
+        s[0][e] = (b0 >> e) & 1 ? s[0][e] : -__builtin_inff();
+        s[1][e] = (b1 >> e) & 1 ? s[1][e] : -__builtin_inff();
+    }
 }
 
 // Probabilities of 32 keys as the operand of the second product; the
@@ -530,13 +557,13 @@ struct Pages {
     int a, b;
 };
 
+// No branch: a load that may not happen would make every wait for the tile
+// loads in flight wait for all of them.
 __device__ __forceinline__ int page_at(const AttnArgs &a, const int32_t *table, int key, int end)
 {
     const int i = key >> a.log_page;
-    if (key >= end || i >= a.table_pages)
-        return -1;
-    const int page = load_uniform(table + i);
-    return (int64_t)(uint32_t)page < a.pages ? page : -1;
+    const int page = load_uniform(table + min(i, a.table_pages - 1));
+    return key < end && i < a.table_pages && (int64_t)(uint32_t)page < a.pages ? page : -1;
 }
 
 // Up to 32 rows: every wave has its own keys.
@@ -553,7 +580,7 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
     const Rows &w = k.w;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
     const int P = 1 << a.log_page;
-    const int64_t cb = chunk_bytes(CT, D, P);
+    const int cb = (int)chunk_bytes(CT, D, P);
     const int32_t *table = a.table + w.b * a.table_stride;
 
     Query<D> x[QT];
@@ -565,13 +592,8 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
         return Pages{page_at(a, table, kb, k.end), page_at(a, table, kb + 16, k.end)};
     };
     auto load = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
-        if (kb >= k.end)
-            return;
-        // a tile that is not there reads page 0; its keys are masked
-        const int64_t oa = ((int64_t)max(pg.a, 0) * a.kv_heads + w.h) * cb;
-        const int64_t ob = ((int64_t)max(pg.b, 0) * a.kv_heads + w.h) * cb;
-        load_tile<CT, D>(raw[0], a.kc + oa, a.vc + oa, kb & (P - 1), P, lane);
-        load_tile<CT, D>(raw[1], a.kc + ob, a.vc + ob, (kb + 16) & (P - 1), P, lane);
+        load_tile<CT, D>(raw[0], chunks_at(a, pg.a, w.h, cb), kb & (P - 1), P, lane);
+        load_tile<CT, D>(raw[1], chunks_at(a, pg.b, w.h, cb), (kb + 16) & (P - 1), P, lane);
     };
     auto compute = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
         f4 s[QT][2];
@@ -661,7 +683,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
     const int rg = wave / KG, kg = wave % KG;
     const int P = 1 << a.log_page;
-    const int64_t cb = chunk_bytes(CT, D, P);
+    const int cb = (int)chunk_bytes(CT, D, P);
     const int32_t *table = a.table + w.b * a.table_stride;
 
     Query<D> x[QT];
@@ -672,8 +694,6 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
     Tile<CT, D> raw;
     int page[WAVES];                             // of the tiles on their way
     auto load = [&](int kb) {
-        if (kb >= k.end)
-            return;
 #pragma unroll
         for (int n = 0; n < WAVES; n++)
             page[n] = page_at(a, table, kb + 16 * n, k.end);
@@ -681,8 +701,7 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
 #pragma unroll
         for (int n = 1; n < WAVES; n++)
             mine = wave == n ? page[n] : mine;
-        const int64_t o = ((int64_t)max(mine, 0) * a.kv_heads + w.h) * cb;
-        load_tile<CT, D>(raw, a.kc + o, a.vc + o, (kb + 16 * wave) & (P - 1), P, lane);
+        load_tile<CT, D>(raw, chunks_at(a, mine, w.h, cb), (kb + 16 * wave) & (P - 1), P, lane);
     };
     load(k.begin);
     for (int kb = k.begin; kb < k.end; kb += KEYS) {
