@@ -116,18 +116,10 @@ __device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int
 {
     using G = Geo<CT, D>;
     const int r = lane & 15, g = lane >> 4;
-    const int kl = r * G::TB + k_piece_off<CT, D>(0, g), ks = pos * G::TB;
-    if constexpr (CT == TQ_Q8_0 && D % 64 != 0) {
+    constexpr int B = k_piece<CT, D>();
 #pragma unroll
-        for (int s = 0; s < G::NB; s++)
-            load_words<2>(raw.k + 2 * s, c.k, kl + 32 * s, ks);
-    } else if constexpr (CT == TQ_Q4_0 && D % 128 != 0) {
-        load_words<G::KW>(raw.k, c.k, kl, ks);
-    } else {
-#pragma unroll
-        for (int s = 0; s < G::KW; s += 4)       // 64 bytes of every key
-            load_words<4>(raw.k + s, c.k, kl + 16 * s, ks);
-    }
+    for (int n = 0; n < G::KW * 4 / B; n++)
+        load_words<B / 4>(raw.k + n * (B / 4), c.k, lane * B + n * (64 * B), pos * G::TB);
     const int scales = P * G::TB;
     if constexpr (G::NB == 3) {
         raw.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6, scales + pos * 6, 0) |

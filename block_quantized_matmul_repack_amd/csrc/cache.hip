@@ -116,7 +116,7 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
     uint8_t *chunk = a.cache[which] + (page * a.heads + h) * chunk_bytes(CT, D, P);
     uint16_t *scales = (uint16_t *)(chunk + P * TB);
     if (which == 0) {
-        uint8_t *p = chunk + pos * TB + k_piece_off<CT, D>(s, c);
+        uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
         if constexpr (CT == TQ_Q8_0) {
             *(uint2 *)p = q;
         } else {
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(THREADS) void k_cache_read(ReadArgs a)
             f16_bits_to_f32(which == 0 ? scales[pos * (D / 32) + s] : scales[s * P + pos]);
         int code[8];
         if (which == 0) {
-            const uint8_t *p = chunk + pos * TB + k_piece_off<CT, D>(s, c);
+            const uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
             if constexpr (CT == TQ_Q8_0) {
                 const uint2 q = *(const uint2 *)p;
 #pragma unroll

@@ -8,10 +8,11 @@
 // instructions wants its operand, so that codes go from memory to the matrix
 // cores through registers alone:
 //
-//   K codes  [token][D]: lane group g (0..3) of an instruction holds elements
-//            8g..8g+7 of a 32-element block s.  Eight elements are one piece
-//            (8 bytes Q8_0, 4 bytes Q4_0), and the pieces one lane needs lie
-//            together in up to 16 bytes (k_piece_off).
+//   K codes  [token / 16][piece][lane group][token % 16]: lane group g (0..3)
+//            of an instruction holds elements 8g..8g+7 of a 32-element block.
+//            Eight elements are 8 bytes (Q8_0) or 4 (Q4_0); a piece is those of
+//            consecutive blocks, up to 16 bytes (k_piece).  A wave that loads
+//            a piece of 16 tokens reads consecutive bytes in lane order.
 //   K scales [token][D / 32].
 //   V codes  [token / 4][column][token % 4]: 4 tokens of one element (Q8_0:
 //            column = element) or of an element pair (Q4_0: column c holds
@@ -41,17 +42,22 @@ constexpr int64_t chunk_bytes(int ct, int64_t D, int64_t P)
     return P * (token_code_bytes(ct, D) + D / 16);
 }
 
-// Byte offset, within a token's K codes, of the piece of block s for lane
-// group g.  One lane's pieces of consecutive blocks are gathered into 16
-// bytes where D gives whole 16-byte groups, into D / 8 bytes (Q4_0) or
-// single 8-byte pieces (Q8_0, D = 96) otherwise.
-template <int CT, int D>
-__host__ __device__ constexpr int k_piece_off(int s, int g)
+// Bytes of a piece of K codes: 16 where D gives whole ones, else all of a
+// lane group's blocks (Q4_0) or one (Q8_0).
+template <int CT, int D> constexpr int k_piece()
 {
-    if constexpr (CT == TQ_Q8_0)
-        return D % 64 == 0 ? ((s >> 1) * 4 + g) * 16 + (s & 1) * 8 : s * 32 + g * 8;
-    else
-        return D % 128 == 0 ? ((s >> 2) * 4 + g) * 16 + (s & 3) * 4 : g * (D / 8) + s * 4;
+    if (CT == TQ_Q8_0)
+        return D % 64 == 0 ? 16 : 8;
+    return D % 128 == 0 ? 16 : D / 8;
+}
+
+// Byte offset, within a chunk, of the codes of lane group g of block s of the
+// token at position pos.
+template <int CT, int D> __host__ __device__ constexpr int k_offset(int pos, int s, int g)
+{
+    constexpr int TB = (int)token_code_bytes(CT, D), B = k_piece<CT, D>();
+    constexpr int one = CT == TQ_Q8_0 ? 8 : 4, per = B / one;
+    return (pos >> 4) * (16 * TB) + (s / per) * (64 * B) + (g * 16 + (pos & 15)) * B + s % per * one;
 }
 
 // Bit position of element i (0..7) in a Q4_0 K piece.
