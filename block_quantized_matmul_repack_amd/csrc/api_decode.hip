@@ -164,7 +164,7 @@ size_t tq_tree_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t k
         return 0;
     const tq::AttnPlan p = tq::attn_plan((int)D, batch, heads, kv_heads, max_nodes,
                                          max_ctx + max_nodes);
-    const size_t n = tq::attn_scratch_bytes(p, (int)D, batch, kv_heads);
+    const size_t n = tq::attn_scratch_bytes(p, (int)D);
     return n ? TQ_NOALLOC_SCRATCH_BYTES + n : 0;
 }
 
@@ -213,7 +213,7 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
                          mask, mask_stride, n_pages, tokens, (int)table_pages,
                          tq::log2_of(page_size), (int)batch, (int)kv_heads,
                          (int)(heads / kv_heads), (int)max_nodes, (int)mask_words, dtype, scale};
-    return launch_status(tq::launch_attention(type, (int)D, a, p, counters, scratch, stream));
+    return launch_status(tq::launch_attention(type, (int)D, a, p, scratch, stream));
 }
 
 size_t tq_verify_draft_workspace_bytes(int64_t batch, int64_t vocab)

@@ -13,9 +13,11 @@
 // the matrix cores and the vector work around them.
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
-// tile, so a cached byte serves all the query heads and tokens of its head;
-// the key ranges of a long cache go to several workgroups, whose sums
-// k_attn_combine joins.  Up to 32 rows (k_attn) the four waves of a workgroup
+// tile, so a cached byte serves all the query heads and tokens of its head.
+// Key steps of all sequences and heads are laid out in one line and cut into
+// equal spans, one for each resident workgroup, so that unlike lengths cost
+// nothing; where a cut falls inside a head's keys, k_attn_combine joins the
+// sums.  Up to 32 rows (k_attn) the four waves of a workgroup
 // hold the same rows and take every fourth group of 32 keys: keys and values
 // go from memory through registers into the matrix cores
 // (v_mfma_f32_16x16x32_f16), without LDS.  S^T = K Q^T leaves query columns in
@@ -47,10 +49,11 @@ constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -1e30f;
 constexpr int RED = 8;                           // fragments joined at a time
 #ifndef TG
-#define TG 1024
+#define TG 512
 #define MC 256
+#define OU 2048
 #endif
-constexpr int64_t TARGET_GROUPS = TG, MIN_CHUNK = MC;
+constexpr int64_t GROUPS = TG, MIN_KEYS = MC, OWN_UNITS = OU;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -224,6 +227,14 @@ __device__ __forceinline__ void drop_values(Tile<CT, D> &raw, int key, bool ther
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// x, which the compiler takes for a new value: what is derived from it is not
+// kept in registers from one turn of an outer loop to the next.
+__device__ __forceinline__ int fresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A read-only word at a uniform address, through the scalar cache: it does
 // not wait behind the tile loads in flight.
 __device__ __forceinline__ int load_uniform(const int32_t *p)
@@ -231,72 +242,206 @@ __device__ __forceinline__ int load_uniform(const int32_t *p)
     return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
 }
 
-// The rows of one workgroup: sequence b, key head h, row block rb; row r is
-// (token r / group, query head h * group + r % group).
+// One sequence, and key head h and row block rb of it; row r is (token
+// r / group, query head h * group + r % group).
 struct Rows {
     int b, h, rb, T, ctx, L;
     int64_t tok0;
 };
 
-__device__ __forceinline__ Rows rows_of(const AttnArgs &a, uint32_t row_blocks, uint32_t unit)
+// Lengths and starts are held inside the buffers whatever they say.
+__device__ __forceinline__ void set_lengths(Rows &w, const AttnArgs &a, int s0, int s1, int ctx)
 {
-    Rows w;
-    const uint32_t bh = unit / row_blocks;
-    w.rb = (int)(unit - bh * row_blocks);
-    w.b = (int)(bh / (uint32_t)a.kv_heads);
-    w.h = (int)(bh - w.b * (uint32_t)a.kv_heads);
-    // lengths and starts are held inside the buffers whatever they say
-    const int64_t s0 = min(max((int64_t)load_uniform(a.starts + w.b), (int64_t)0), a.tokens);
-    const int64_t s1 = min((int64_t)load_uniform(a.starts + w.b + 1), a.tokens);
-    w.tok0 = s0;
-    w.T = (int)min(max(s1 - s0, (int64_t)0), (int64_t)a.max_nodes);
-    w.ctx = max(load_uniform(a.ctx + w.b), 0);
+    const int64_t t0 = min(max((int64_t)s0, (int64_t)0), a.tokens);
+    const int64_t t1 = min((int64_t)s1, a.tokens);
+    w.tok0 = t0;
+    w.T = (int)min(max(t1 - t0, (int64_t)0), (int64_t)a.max_nodes);
+    w.ctx = max(ctx, 0);
     const int64_t most = (int64_t)a.table_pages << a.log_page;
     w.L = (int)min((int64_t)w.ctx + w.T, most);
+}
+
+__device__ __forceinline__ Rows rows_of(const AttnArgs &a, int b)
+{
+    Rows w;
+    w.b = b;
+    w.h = w.rb = 0;
+    set_lengths(w, a, load_uniform(a.starts + b), load_uniform(a.starts + b + 1),
+                load_uniform(a.ctx + b));
     return w;
 }
 
-// Ranges of keys that sequence w is cut into: range 0 always counts, the last
-// takes what the launch did not foresee.
-__device__ __forceinline__ int ranges_of(const Rows &w, int splits, int chunk)
+// Key steps of `keys` keys, and row blocks, of a sequence.  One that has new
+// tokens takes a step even if it sees no key: its outputs are zeros.
+__device__ __forceinline__ int steps_of(const Rows &w, int keys)
 {
-    return (int)max(1u, min((uint32_t)splits, ((uint32_t)w.L + chunk - 1) / (uint32_t)chunk));
+    return w.T == 0 ? 0 : max((w.L + keys - 1) / keys, 1);
 }
 
-// A workgroup's rows and keys; false: it has none.
-struct Work {
+__device__ __forceinline__ int blocks_of(const AttnArgs &a, const AttnPlan &p, const Rows &w)
+{
+    return (w.T * a.group + p.tiles * 16 - 1) / (p.tiles * 16);
+}
+
+// The line of key steps runs sequence by sequence, in it (head, row block) by
+// (head, row block).  Steps of sequence b in it.
+__device__ __forceinline__ int64_t line_steps(const AttnArgs &a, const AttnPlan &p, int keys, int b)
+{
     Rows w;
-    uint32_t unit;
-    int range, ranges, begin, end;               // keys begin .. end - 1
+    w.T = 0;
+    w.L = w.ctx = 0;
+    if (b < a.batch)
+        set_lengths(w, a, a.starts[b], a.starts[b + 1], a.ctx[b]);
+    return (int64_t)steps_of(w, keys) * blocks_of(a, p, w) * a.kv_heads;
+}
+
+__device__ __forceinline__ int64_t scan_lanes(int64_t v, int lane)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const int64_t o = __shfl_up(v, m);
+        v += lane >= m ? o : 0;
+    }
+    return v;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t x)
+{
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+}
+
+// Steps of the line for each workgroup (the line has less than 2048 * 2^24
+// steps, 512 workgroups share a long one); every wave computes it alike.
+__device__ __forceinline__ int span_of(const AttnArgs &a, const AttnPlan &p, int keys, int lane)
+{
+    int64_t sum = 0;
+    for (int b = lane; b < a.batch; b += 64)
+        sum += line_steps(a, p, keys, b);
+    if (a.batch > 1)
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1)
+            sum += __shfl_xor(sum, m);
+    sum = uniform64(sum);
+    return (int)max((sum + p.groups - 1) / p.groups, (int64_t)1);
+}
+
+// Sequence b that holds position `at` of the line, which becomes the position
+// in it; b = batch past the end.
+__device__ __forceinline__ int find_sequence(const AttnArgs &a, const AttnPlan &p, int keys,
+                                             int64_t &at, int lane)
+{
+    for (int base = 0; base < a.batch; base += 64) {
+        const int64_t n = line_steps(a, p, keys, base + lane), end = scan_lanes(n, lane);
+        const uint64_t hit = __ballot(at < end);
+        if (hit) {
+            const int k = __builtin_ctzll(hit);
+            at -= uniform64(__shfl(end - n, k));
+            return base + k;
+        }
+        at -= uniform64(__shfl(end, 63));
+    }
+    return a.batch;
+}
+
+// Position of sequence b's first step in the line.
+__device__ __forceinline__ int64_t line_start(const AttnArgs &a, const AttnPlan &p, int keys, int b,
+                                              int lane)
+{
+    int64_t sum = 0;
+    for (int c = lane; c < b; c += 64)
+        sum += line_steps(a, p, keys, c);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+        sum += __shfl_xor(sum, m);
+    return uniform64(sum);
+}
+
+// A workgroup's place in the line: its next steps are `step` .. of (head, row
+// block) `q` of the sequence in w, `left` steps remain.
+struct Cursor {
+    Rows w;
+    int q, steps, blocks, step, left;
 };
 
-__device__ __forceinline__ bool work_of(const AttnArgs &a, const AttnPlan &p, Work &k)
+__device__ __forceinline__ void set_sequence(Cursor &c, const AttnArgs &a, const AttnPlan &p,
+                                             int keys, int b)
 {
-    // consecutive workgroups go to the 8 dies in turn: the row blocks of one
-    // key range follow each other on one die, whose cache then serves them
-    const uint32_t keyed = (uint32_t)a.batch * a.kv_heads * p.splits;    // (b, h, range)
-    const uint32_t id = blockIdx.x, nrb = p.row_blocks, whole = keyed / 8 * 8;
-    uint32_t kr, rb;
-    if (id < whole * nrb) {
-        const uint32_t q = id >> 3, n = q / nrb;
-        kr = n * 8 + (id & 7);
-        rb = q - n * nrb;
-    } else {
-        const uint32_t left = id - whole * nrb, n = left / nrb;
-        kr = whole + n;
-        rb = left - n * nrb;
+    c.w = rows_of(a, b);
+    c.steps = steps_of(c.w, keys);
+    c.blocks = blocks_of(a, p, c.w);
+}
+
+__device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &p, int keys,
+                                             int lane)
+{
+    Cursor c;
+    c.left = 0;
+    if (p.groups == 0) {
+        // many heads: one workgroup for all the keys of each
+        const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
+        set_sequence(c, a, p, keys, (int)b);
+        const uint32_t q = blockIdx.x - b * per, h = q / p.row_blocks, rb = q - h * p.row_blocks;
+        c.q = (int)(h * c.blocks + rb);
+        c.step = 0;
+        if ((int)rb < c.blocks)
+            c.left = c.steps;
+        return c;
     }
-    const uint32_t bh = kr / (uint32_t)p.splits;
-    k.range = (int)(kr - bh * p.splits);
-    k.unit = bh * nrb + rb;
-    k.w = rows_of(a, nrb, k.unit);
-    if (k.w.rb * p.tiles * 16 >= k.w.T * a.group)
+    const int span = span_of(a, p, keys, lane);
+    int64_t at = (int64_t)blockIdx.x * span;
+    int b = 0;
+    if (a.batch > 1) {
+        b = uniform(find_sequence(a, p, keys, at, lane));
+        if (b >= a.batch)
+            return c;
+    }
+    set_sequence(c, a, p, keys, b);
+    const int64_t all = (int64_t)c.steps * c.blocks * a.kv_heads;
+    if (at >= all)
+        return c;
+    c.q = uniform((int)(at / max(c.steps, 1)));
+    c.step = uniform((int)(at - (int64_t)c.q * c.steps));
+    c.left = span;
+    return c;
+}
+
+// What a workgroup does next: keys begin .. end - 1 of the rows in w; `whole`
+// if those are all the rows have, else its sums go to slot `slot`.
+struct Work {
+    Rows w;
+    bool whole;
+    int slot, begin, end;
+};
+
+// false: nothing is left.
+__device__ __forceinline__ bool next_work(Cursor &c, Work &k, const AttnArgs &a, const AttnPlan &p,
+                                          int keys, bool first)
+{
+    if (!first) {
+        if (c.left <= 0 || p.groups == 0)
+            return false;
+        c.step = 0;
+        if (++c.q == c.blocks * a.kv_heads) {
+            c.q = 0;
+            int b = c.w.b;
+            do {
+                if (++b >= a.batch)
+                    return false;
+                set_sequence(c, a, p, keys, b);
+            } while (c.steps == 0);
+        }
+    }
+    if (c.left <= 0)
         return false;
-    k.ranges = ranges_of(k.w, p.splits, p.chunk);
-    if (k.range >= k.ranges)
-        return false;
-    k.begin = k.range * p.chunk;
-    k.end = k.range == k.ranges - 1 ? k.w.L : k.begin + p.chunk;
+    const int take = min(c.left, c.steps - c.step);
+    k.w = c.w;
+    k.w.h = c.q / c.blocks;
+    k.w.rb = c.q - k.w.h * c.blocks;
+    k.whole = take == c.steps;
+    k.slot = 2 * blockIdx.x + !first;
+    k.begin = c.step * keys;
+    k.end = min(c.w.L, (c.step + take) * keys);
+    c.left -= take;
     return true;
 }
 
@@ -451,11 +596,10 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
 }
 
 // Joins the KG waves that hold the same rows (rg, of RG groups) and stores
-// the outputs, or the range's sums where there are several.  red: RED
+// the outputs, or their sums where other workgroups have more of the keys.  red: RED
 // fragments of 64 lanes per wave.
 template <int CT, int D, int QT, int RG, int KG>
-__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const Work &k,
-                                       const AttnPlan &p, int rg, int kg, int lane, f4 *red,
+__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const Work &k, int rg, int kg, int lane, f4 *red,
                                        float *ml, float *__restrict__ part,
                                        float *__restrict__ part_ml)
 {
@@ -493,8 +637,8 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
             x[i].l = ll;
         }
     }
-    const int64_t slot = (int64_t)k.unit * p.splits + k.range;
-    if (k.ranges > 1 && kg == 0 && g == 0) {
+    const int64_t slot = k.slot;
+    if (!k.whole && kg == 0 && g == 0) {
 #pragma unroll
         for (int i = 0; i < QT; i++) {
             float2 *q = (float2 *)part_ml + slot * (TILES * 16) + (rg * QT + i) * 16 + col;
@@ -502,7 +646,7 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
         }
     }
     auto put = [&](int i, int t, f4 sum) {
-        if (k.ranges > 1) {
+        if (!k.whole) {
             const int ff = (rg * QT + i) * NT + t;
             *(f4 *)(part + ((slot * F + ff) * 64 + lane) * 4) = sum;
         } else {
@@ -544,266 +688,294 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
     }
 }
 
-// Page numbers of two neighbouring tiles; -1 where there is nothing to read.
-struct Pages {
-    int a, b;
-};
-
-// No branch: a load that may not happen would make every wait for the tile
+// The page table's entry for a key, and the page it means: -1 where there is
+// nothing to read.  Two calls, so that the entry can be asked for early; and
+// no branch: a load that may not happen would make every wait for the tile
 // loads in flight wait for all of them.
-__device__ __forceinline__ int page_at(const AttnArgs &a, const int32_t *table, int key, int end)
+__device__ __forceinline__ int entry_at(const AttnArgs &a, const int32_t *table, int key)
 {
-    const int i = key >> a.log_page;
-    const int page = load_uniform(table + min(i, a.table_pages - 1));
-    return key < end && i < a.table_pages && (int64_t)(uint32_t)page < a.pages ? page : -1;
+    return load_uniform(table + min(key >> a.log_page, a.table_pages - 1));
+}
+
+__device__ __forceinline__ int page_of(const AttnArgs &a, int entry, int key, int end)
+{
+    return key < end && (int64_t)(uint32_t)entry < a.pages ? entry : -1;
 }
 
 // Up to 32 rows: every wave has its own keys.
 template <int CT, int D, int QT>
-__global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(AttnArgs a, AttnPlan p, float *__restrict__ part,
-                                                  float *__restrict__ part_ml)
+__global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(
+    AttnArgs a, AttnPlan p, float *__restrict__ part, float *__restrict__ part_ml)
 {
     using G = Geo<CT, D>;
     __shared__ f4 red[WAVES * RED * 64];
     __shared__ float ml[WAVES * QT * 16 * 2];
-    Work k;
-    if (!work_of(a, p, k))
-        return;
-    const Rows &w = k.w;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
+    const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int P = 1 << a.log_page;
     const int cb = (int)chunk_bytes(CT, D, P);
-    const int32_t *table = a.table + w.b * a.table_stride;
-
-    Query<D> x[QT];
-#pragma unroll
-    for (int i = 0; i < QT; i++)
-        load_query<D>(x[i], a, w, QT, i, lane);
-
-    auto pages_at = [&](int kb) {
-        return Pages{page_at(a, table, kb, k.end), page_at(a, table, kb + 16, k.end)};
-    };
-    auto load = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
-        load_tile<CT, D>(raw[0], chunks_at(a, pg.a, w.h, cb), kb & (P - 1), P, lane);
-        load_tile<CT, D>(raw[1], chunks_at(a, pg.b, w.h, cb), (kb + 16) & (P - 1), P, lane);
-    };
-    auto compute = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
-        f4 s[QT][2];
-        auto scores = [&](const Tile<CT, D> &tile, int T) {
-#pragma unroll
-            for (int i = 0; i < QT; i++)
-                s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int b = 0; b < G::NB; b++) {
-                const h8 kf = key_frag<CT, D>(tile, b);
-#pragma unroll
-                for (int i = 0; i < QT; i++)
-                    s[i][T] = mfma(kf, x[i].q[b], s[i][T]);
-            }
+    Cursor cur = first_span(a, p, STRIDE, lane0);
+    Work k;
+    for (bool first = true; next_work(cur, k, a, p, STRIDE, first); first = false) {
+        const Rows &w = k.w;
+        const int32_t *table = a.table + w.b * a.table_stride;
+        const int lane = fresh(lane0), g = lane >> 4;
+        struct Pages {                           // of the two tiles of a step
+            int a, b;
         };
-        scores(raw[0], 0);
-        scores(raw[1], 1);
-        if (kb + STEP > w.ctx || pg.a < 0 || pg.b < 0) {
-#pragma unroll
-            for (int i = 0; i < QT; i++)
-                mask_scores<D>(s[i], x[i], a, w, kb, pg.a >= 0, pg.b >= 0, g);
-            drop_values<CT, D>(raw[0], kb + 4 * g, pg.a >= 0, w.ctx, w.L);
-            drop_values<CT, D>(raw[1], kb + 16 + 4 * g, pg.b >= 0, w.ctx, w.L);
-        }
-        h8 pr[QT];
-#pragma unroll
-        for (int i = 0; i < QT; i++)
-            pr[i] = softmax_step<D>(s[i], x[i]);
-#pragma unroll
-        for (int t = 0; t < G::NT; t++) {
-            Frag f;
-            value_half<CT, D>(raw[0], t, f.p[0], f.p[1]);
-            value_half<CT, D>(raw[1], t, f.p[2], f.p[3]);
-#pragma unroll
-            for (int i = 0; i < QT; i++)
-                x[i].o[t] = mfma(f.v, pr[i], x[i].o[t]);
-        }
-    };
-
-    // one step computed, the next one's codes on their way, and the page
-    // numbers of the one after that
-    int kb = k.begin + wave * STEP;
-    if (kb < k.end) {
-        Tile<CT, D> ra[2], rb[2];
-        Pages pa = pages_at(kb), pb = pages_at(kb + STRIDE);
-        load(ra, pa, kb);
-        for (;;) {
-            load(rb, pb, kb + STRIDE);
-            Pages pn = pages_at(kb + 2 * STRIDE);
-            compute(ra, pa, kb);
-            pa = pn;
-            kb += STRIDE;
-            if (kb >= k.end)
-                break;
-            load(ra, pa, kb + STRIDE);
-            pn = pages_at(kb + 2 * STRIDE);
-            compute(rb, pb, kb);
-            pb = pn;
-            kb += STRIDE;
-            if (kb >= k.end)
-                break;
-        }
-    }
-    finish<CT, D, QT, 1, WAVES>(x, a, k, p, 0, wave, lane, red, ml, part, part_ml);
-}
-
-// More rows: RG groups of waves with QT * 16 rows each, KG = 4 / RG waves per
-// group.  Every wave dequantizes one 16-key tile of 64 keys into LDS, in the
-// fragments of the matrix instructions, while the codes of the next 64 are on
-// their way; then each reads what its rows need (KG = 2: one 32-key half).
-template <int CT, int D, int QT, int RG>
-__global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p,
-                                                       float *__restrict__ part,
-                                                       float *__restrict__ part_ml)
-{
-    using G = Geo<CT, D>;
-    constexpr int KG = WAVES / RG, KEYS = 16 * WAVES;
-    constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
-    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
-    __shared__ h8 lds[STAGE > JOIN ? STAGE : JOIN];
-    __shared__ float ml[WAVES * QT * 16 * 2];
-    h8 *kf = lds, *vf = lds + K_FRAGS * 64;
-    Work k;
-    if (!work_of(a, p, k))
-        return;
-    const Rows &w = k.w;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
-    const int rg = wave / KG, kg = wave % KG;
-    const int P = 1 << a.log_page;
-    const int cb = (int)chunk_bytes(CT, D, P);
-    const int32_t *table = a.table + w.b * a.table_stride;
-
-    Query<D> x[QT];
-#pragma unroll
-    for (int i = 0; i < QT; i++)
-        load_query<D>(x[i], a, w, RG * QT, rg * QT + i, lane);
-
-    Tile<CT, D> raw;
-    int page[WAVES];                             // of the tiles on their way
-    auto load = [&](int kb) {
-#pragma unroll
-        for (int n = 0; n < WAVES; n++)
-            page[n] = page_at(a, table, kb + 16 * n, k.end);
-        int mine = page[0];
-#pragma unroll
-        for (int n = 1; n < WAVES; n++)
-            mine = wave == n ? page[n] : mine;
-        load_tile<CT, D>(raw, chunks_at(a, mine, w.h, cb), (kb + 16 * wave) & (P - 1), P, lane);
-    };
-    load(k.begin);
-    for (int kb = k.begin; kb < k.end; kb += KEYS) {
-        bool ok[WAVES];
-        bool all = kb + KEYS <= w.ctx;
-#pragma unroll
-        for (int n = 0; n < WAVES; n++) {
-            ok[n] = page[n] >= 0;
-            all = all && ok[n];
-        }
-        if (!all) {
-            bool mine = ok[0];
-#pragma unroll
-            for (int n = 1; n < WAVES; n++)
-                mine = wave == n ? ok[n] : mine;
-            drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, mine, w.ctx, w.L);
-        }
-        __syncthreads();                         // the last keys are used up
-#pragma unroll
-        for (int b = 0; b < G::NB; b++)
-            kf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
-#pragma unroll
-        for (int t = 0; t < G::NT; t++) {
-            union {
-                h2 h[2];
-                u2 u;
-            } v;
-            value_half<CT, D>(raw, t, v.h[0], v.h[1]);
-            ((u2 *)&vf[((wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
-        }
-        load(kb + KEYS);
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < 2; n++) {
-            if (KG == 2 && n != kg)
-                continue;
-            const int kp = kb + STEP * n;
-            if (kp >= k.end)
-                continue;
+        auto entries_at = [&](int kb) {
+            return Pages{entry_at(a, table, kb), entry_at(a, table, kb + 16)};
+        };
+        auto pages_of = [&](const Pages &e, int kb) {
+            return Pages{page_of(a, e.a, kb, k.end), page_of(a, e.b, kb + 16, k.end)};
+        };
+        auto load = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
+            load_tile<CT, D>(raw[0], chunks_at(a, pg.a, w.h, cb), kb & (P - 1), P, lane);
+            load_tile<CT, D>(raw[1], chunks_at(a, pg.b, w.h, cb), (kb + 16) & (P - 1), P, lane);
+        };
+        Query<D> x[QT];
+        auto compute = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
             f4 s[QT][2];
-#pragma unroll
-            for (int T = 0; T < 2; T++) {
+            auto scores = [&](const Tile<CT, D> &tile, int T) {
 #pragma unroll
                 for (int i = 0; i < QT; i++)
                     s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int b = 0; b < G::NB; b++) {
-                    const h8 kv = kf[((2 * n + T) * G::NB + b) * 64 + lane];
+                    const h8 kf = key_frag<CT, D>(tile, b);
 #pragma unroll
                     for (int i = 0; i < QT; i++)
-                        s[i][T] = mfma(kv, x[i].q[b], s[i][T]);
+                        s[i][T] = mfma(kf, x[i].q[b], s[i][T]);
                 }
-            }
-            if (!all)
+            };
+            scores(raw[0], 0);
+            scores(raw[1], 1);
+            if (kb + STEP > w.ctx || pg.a < 0 || pg.b < 0) {
 #pragma unroll
                 for (int i = 0; i < QT; i++)
-                    mask_scores<D>(s[i], x[i], a, w, kp, ok[2 * n], ok[2 * n + 1], g);
+                    mask_scores<D>(s[i], x[i], a, w, kb, pg.a >= 0, pg.b >= 0, g);
+                drop_values<CT, D>(raw[0], kb + 4 * g, pg.a >= 0, w.ctx, w.L);
+                drop_values<CT, D>(raw[1], kb + 16 + 4 * g, pg.b >= 0, w.ctx, w.L);
+            }
             h8 pr[QT];
 #pragma unroll
             for (int i = 0; i < QT; i++)
                 pr[i] = softmax_step<D>(s[i], x[i]);
 #pragma unroll
             for (int t = 0; t < G::NT; t++) {
-                const h8 vv = vf[(n * G::NT + t) * 64 + lane];
+                Frag f;
+                value_half<CT, D>(raw[0], t, f.p[0], f.p[1]);
+                value_half<CT, D>(raw[1], t, f.p[2], f.p[3]);
 #pragma unroll
                 for (int i = 0; i < QT; i++)
-                    x[i].o[t] = mfma(vv, pr[i], x[i].o[t]);
+                    x[i].o[t] = mfma(f.v, pr[i], x[i].o[t]);
             }
+        };
+
+        // one step computed, the next one's codes on their way, and the page
+        // numbers of the one after that
+        int kb = k.begin + wave * STEP;
+        Tile<CT, D> ra[2], rb[2];
+        Pages pa = pages_of(entries_at(kb), kb), pb, en = entries_at(kb + STRIDE);
+        load(ra, pa, kb);
+#pragma unroll
+        for (int i = 0; i < QT; i++)
+            load_query<D>(x[i], a, w, QT, i, lane);
+        while (kb < k.end) {
+            pb = pages_of(en, kb + STRIDE);
+            load(rb, pb, kb + STRIDE);
+            en = entries_at(kb + 2 * STRIDE);
+            compute(ra, pa, kb);
+            kb += STRIDE;
+            if (kb >= k.end)
+                break;
+            pa = pages_of(en, kb + STRIDE);
+            load(ra, pa, kb + STRIDE);
+            en = entries_at(kb + 2 * STRIDE);
+            compute(rb, pb, kb);
+            kb += STRIDE;
         }
+        finish<CT, D, QT, 1, WAVES>(x, a, k, 0, wave, lane, red, ml, part, part_ml);
     }
-    finish<CT, D, QT, RG, KG>(x, a, k, p, rg, kg, lane, (f4 *)lds, ml, part, part_ml);
 }
 
-// One workgroup per fragment: the ranges' sums, each rescaled to the largest
-// reference.  Wave n adds ranges n, n + 4, ... (four loads in flight), the
-// waves' sums are joined through LDS.
+// More rows: RG groups of waves with QT * 16 rows each, KG = 4 / RG waves per
+// group.  Every wave dequantizes one 16-key tile of 64 keys into LDS, in the
+// fragments of the matrix instructions, while the codes of the next 64 are on
+// their way; then each reads what its rows need (KG = 2: one 32-key half).
+constexpr int ROW_KEYS = 16 * WAVES;
+
+template <int CT, int D, int QT, int RG>
+__global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p,
+                                                          float *__restrict__ part,
+                                                          float *__restrict__ part_ml)
+{
+    using G = Geo<CT, D>;
+    constexpr int KG = WAVES / RG;
+    constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
+    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
+    __shared__ h8 lds[STAGE > JOIN ? STAGE : JOIN];
+    __shared__ float ml[WAVES * QT * 16 * 2];
+    h8 *kf = lds, *vf = lds + K_FRAGS * 64;
+    const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int rg = wave / KG, kg = wave % KG;
+    const int P = 1 << a.log_page;
+    const int cb = (int)chunk_bytes(CT, D, P);
+    Cursor cur = first_span(a, p, ROW_KEYS, lane0);
+    Work k;
+    for (bool first = true; next_work(cur, k, a, p, ROW_KEYS, first); first = false) {
+        const Rows &w = k.w;
+        const int32_t *table = a.table + w.b * a.table_stride;
+        const int lane = fresh(lane0), g = lane >> 4;
+        Tile<CT, D> raw;
+        int entry[WAVES], page[WAVES];           // of the 64 keys on their way
+        auto entries_at = [&](int kb) {
+#pragma unroll
+            for (int n = 0; n < WAVES; n++)
+                entry[n] = entry_at(a, table, kb + 16 * n);
+        };
+        auto load = [&](int kb) {
+#pragma unroll
+            for (int n = 0; n < WAVES; n++)
+                page[n] = page_of(a, entry[n], kb + 16 * n, k.end);
+            int mine = page[0];
+#pragma unroll
+            for (int n = 1; n < WAVES; n++)
+                mine = wave == n ? page[n] : mine;
+            load_tile<CT, D>(raw, chunks_at(a, mine, w.h, cb), (kb + 16 * wave) & (P - 1), P, lane);
+        };
+        entries_at(k.begin);
+        load(k.begin);
+        entries_at(k.begin + ROW_KEYS);
+        Query<D> x[QT];
+#pragma unroll
+        for (int i = 0; i < QT; i++)
+            load_query<D>(x[i], a, w, RG * QT, rg * QT + i, lane);
+        for (int kb = k.begin; kb < k.end; kb += ROW_KEYS) {
+            bool ok[WAVES];
+            bool all = kb + ROW_KEYS <= w.ctx;
+#pragma unroll
+            for (int n = 0; n < WAVES; n++) {
+                ok[n] = page[n] >= 0;
+                all = all && ok[n];
+            }
+            if (!all) {
+                bool mine = ok[0];
+#pragma unroll
+                for (int n = 1; n < WAVES; n++)
+                    mine = wave == n ? ok[n] : mine;
+                drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, mine, w.ctx, w.L);
+            }
+            __syncthreads();                     // the last keys are used up
+#pragma unroll
+            for (int b = 0; b < G::NB; b++)
+                kf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
+#pragma unroll
+            for (int t = 0; t < G::NT; t++) {
+                union {
+                    h2 h[2];
+                    u2 u;
+                } v;
+                value_half<CT, D>(raw, t, v.h[0], v.h[1]);
+                ((u2 *)&vf[((wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
+            }
+            load(kb + ROW_KEYS);
+            entries_at(kb + 2 * ROW_KEYS);
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                if (KG == 2 && n != kg)
+                    continue;
+                const int kp = kb + STEP * n;
+                if (kp >= k.end)
+                    continue;
+                // all of a step's keys are asked for before the first product,
+                // all of its values before the softmax: the reads' latency
+                // passes behind them
+                f4 s[QT][2];
+                h8 kv[2 * G::NB], vv[G::NT];
+#pragma unroll
+                for (int b = 0; b < 2 * G::NB; b++)
+                    kv[b] = kf[(2 * n * G::NB + b) * 64 + lane];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int T = 0; T < 2; T++) {
+#pragma unroll
+                    for (int i = 0; i < QT; i++)
+                        s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int b = 0; b < G::NB; b++)
+#pragma unroll
+                        for (int i = 0; i < QT; i++)
+                            s[i][T] = mfma(kv[T * G::NB + b], x[i].q[b], s[i][T]);
+                }
+#pragma unroll
+                for (int t = 0; t < G::NT; t++)
+                    vv[t] = vf[(n * G::NT + t) * 64 + lane];
+                __builtin_amdgcn_sched_barrier(0);
+                if (!all)
+#pragma unroll
+                    for (int i = 0; i < QT; i++)
+                        mask_scores<D>(s[i], x[i], a, w, kp, ok[2 * n], ok[2 * n + 1], g);
+                h8 pr[QT];
+#pragma unroll
+                for (int i = 0; i < QT; i++)
+                    pr[i] = softmax_step<D>(s[i], x[i]);
+#pragma unroll
+                for (int t = 0; t < G::NT; t++)
+#pragma unroll
+                    for (int i = 0; i < QT; i++)
+                        x[i].o[t] = mfma(vv[t], pr[i], x[i].o[t]);
+            }
+        }
+        finish<CT, D, QT, RG, KG>(x, a, k, rg, kg, lane, (f4 *)lds, ml, part, part_ml);
+    }
+}
+
+// Joins the sums of a head and row block whose steps several workgroups took,
+// one workgroup per fragment.  Wave n adds parts n, n + 4, ... (four loads in
+// flight), the waves' sums are joined through LDS.
 template <int CT, int D>
-__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p,
+__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p, int keys,
                                                           const float *__restrict__ part,
                                                           const float *__restrict__ part_ml)
 {
     constexpr int NT = D / 16;
     __shared__ f4 red[WAVES][64];
     __shared__ float redl[WAVES][64];
-    const uint32_t unit = blockIdx.x;
-    const Rows w = rows_of(a, p.row_blocks, unit);
-    if (w.rb * p.tiles * 16 >= w.T * a.group)
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
+    const uint32_t q = blockIdx.x - b * per;
+    Rows w = rows_of(a, (int)b);
+    w.h = (int)(q / p.row_blocks);
+    w.rb = (int)(q - w.h * p.row_blocks);
+    const int steps = steps_of(w, keys), blocks = blocks_of(a, p, w);
+    if (w.rb >= blocks)
         return;
-    const int ranges = ranges_of(w, p.splits, p.chunk);
-    if (ranges == 1)
+    const int64_t span = span_of(a, p, keys, lane);
+    const int64_t from = (b ? line_start(a, p, keys, (int)b, lane) : 0) +
+                         (int64_t)(w.h * blocks + w.rb) * steps;
+    const int first = uniform((int)(from / span)), last = uniform((int)((from + steps - 1) / span));
+    if (first == last)
         return;
+    const int late = uniform(from != first * span);     // it is not the first workgroup's first
     const int F = p.tiles * NT, ff = blockIdx.y, tile = ff / NT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t slot = (int64_t)unit * p.splits;
-    const float2 *mlp = (const float2 *)part_ml + slot * (p.tiles * 16) + tile * 16 + (lane & 15);
-    const int ms = p.tiles * 16;
+    const float2 *mlp = (const float2 *)part_ml + tile * 16 + (lane & 15);
+    const int ms = p.tiles * 16, n_parts = last - first + 1;
+    auto slot = [&](int n) { return (int64_t)(2 * (first + n) + (n == 0 ? late : 0)); };
     float mm = NO_REF;
-    for (int n = lane >> 4; n < ranges; n += 4)
-        mm = fmaxf(mm, mlp[n * ms].x);
+    for (int n = lane >> 4; n < n_parts; n += 4)
+        mm = fmaxf(mm, mlp[slot(n) * ms].x);
     mm = fmaxf(mm, __shfl_xor(mm, 16));
     mm = fmaxf(mm, __shfl_xor(mm, 32));
     float ll = 0.0f;
     f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float *q = part + ((slot * F + ff) * 64 + lane) * 4;
+    const float *o = part + (ff * 64 + lane) * 4;
 #pragma unroll 4
-    for (int n = wave; n < ranges; n += WAVES) {
-        const float2 t = mlp[n * ms];
+    for (int n = wave; n < n_parts; n += WAVES) {
+        const float2 t = mlp[slot(n) * ms];
         const float f = __builtin_amdgcn_exp2f(t.x - mm);
         ll += f * t.y;
-        sum += f * *(const f4 *)(q + (int64_t)n * F * 256);
+        sum += f * *(const f4 *)(o + slot(n) * F * 256);
     }
     red[wave][lane] = sum;
     redl[wave][lane] = ll;
@@ -824,12 +996,12 @@ template <int CT, int D>
 hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStream_t s)
 {
     const int64_t units = (int64_t)a.batch * a.kv_heads * p.row_blocks;
-    const int64_t blocks = units * p.splits;
+    const int64_t blocks = p.groups ? p.groups : units;
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
     const int F = p.tiles * (D / 16);
     float *part = (float *)scratch;
-    float *ml = part ? part + (size_t)units * p.splits * F * 256 : nullptr;
+    float *ml = part ? part + (size_t)2 * p.groups * F * 256 : nullptr;
     const dim3 grid((unsigned)blocks);
     constexpr int QT = rows_qt(D);
     if (p.row_groups == 4)
@@ -841,9 +1013,10 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     else if constexpr (D <= 128)
         k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p, part, ml);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1)
+    if (e != hipSuccess || p.groups <= 1)
         return e;
-    k_attn_combine<CT, D><<<dim3((unsigned)units, (unsigned)F), THREADS, 0, s>>>(a, p, part, ml);
+    k_attn_combine<CT, D><<<dim3((unsigned)units, (unsigned)F), THREADS, 0, s>>>(
+        a, p, p.row_groups > 1 ? ROW_KEYS : STRIDE, part, ml);
     return hipGetLastError();
 }
 
@@ -879,25 +1052,26 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     }
     p.row_blocks = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
     const int64_t units = batch * kv_heads * p.row_blocks;
-    const int64_t want = std::max<int64_t>(1, TARGET_GROUPS / std::max<int64_t>(units, 1));
-    const int64_t most = std::max<int64_t>(1, (max_keys + MIN_CHUNK - 1) / MIN_CHUNK);
-    const int64_t s = std::min(want, most);
-    const int64_t chunk = ((max_keys + s - 1) / s + STRIDE - 1) / STRIDE * STRIDE;
-    p.chunk = (int)std::max<int64_t>(chunk, STRIDE);
-    p.splits = (int)std::max<int64_t>(1, (max_keys + p.chunk - 1) / p.chunk);
+    // two workgroups are resident on each of the 256 compute units; a span
+    // is at least MIN_KEYS keys, and where the heads alone fill the chip
+    // several times over each has a workgroup of its own
+    const int keys = p.row_groups > 1 ? ROW_KEYS : STRIDE;
+    const int64_t steps = units * ((max_keys + keys - 1) / keys);
+    p.groups = units >= OWN_UNITS
+                   ? 0
+                   : (int)std::min<int64_t>(GROUPS, std::max<int64_t>(1, steps / (MIN_KEYS / keys)));
     return p;
 }
 
-size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads)
+size_t attn_scratch_bytes(const AttnPlan &p, int D)
 {
-    if (p.splits == 1)
-        return 0;
-    const size_t units = (size_t)batch * kv_heads * p.row_blocks * p.splits;
-    return units * p.tiles * ((size_t)(D / 16) * 256 + 32) * sizeof(float);
+    // sums of one workgroup: at most its first and its last rows are shared
+    return p.groups <= 1 ? 0
+                         : (size_t)2 * p.groups * p.tiles * ((size_t)(D / 16) * 256 + 32) * sizeof(float);
 }
 
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
-                            uint32_t *, void *scratch, hipStream_t s)
+                            void *scratch, hipStream_t s)
 {
     return cache_type == TQ_Q8_0 ? launch_c<TQ_Q8_0>(D, a, p, scratch, s)
                                  : launch_c<TQ_Q4_0>(D, a, p, scratch, s);

@@ -424,15 +424,16 @@ struct AttnArgs {
     float scale;
 };
 // Launch geometry, from host sizes alone: 16-row tiles per workgroup (in
-// row_groups groups of waves), row blocks of them, key ranges of `chunk`.
+// row_groups groups of waves), row blocks of them, and how many workgroups
+// share the key steps (0: each head and row block has its own).
 struct AttnPlan {
-    int tiles, row_groups, row_blocks, splits, chunk;
+    int tiles, row_groups, row_blocks, groups;
 };
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys);
-size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads);
+size_t attn_scratch_bytes(const AttnPlan &p, int D);
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
-                            uint32_t *counters, void *scratch, hipStream_t s);
+                            void *scratch, hipStream_t s);
 
 // Verification of drafted tokens.
 struct VerifyArgs {
