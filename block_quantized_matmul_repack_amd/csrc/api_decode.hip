@@ -164,7 +164,7 @@ size_t tq_tree_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t k
         return 0;
     const tq::AttnPlan p = tq::attn_plan((int)D, batch, heads, kv_heads, max_nodes,
                                          max_ctx + max_nodes);
-    const size_t n = tq::attn_scratch_bytes(p, (int)D);
+    const size_t n = tq::attn_scratch_bytes(p, (int)D, batch, kv_heads);
     return n ? TQ_NOALLOC_SCRATCH_BYTES + n : 0;
 }
 

@@ -57,8 +57,10 @@ constexpr int64_t GROUPS = TG, MIN_KEYS = MC, OWN_UNITS = OU;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef int i4 __attribute__((ext_vector_type(4)));
 
 template <int CT, int D> struct Geo {
     static constexpr int NB = D / 32;            // 32-element blocks = matrix steps of Q K^T
@@ -112,13 +114,13 @@ __device__ __forceinline__ Chunks chunks_at(const AttnArgs &a, int page, int h, 
     return Chunks{make_rsrc(a.kc + at, n), make_rsrc(a.vc + at, n)};
 }
 
-// The 16 keys at position pos (uniform) of a page.
+// The 16 keys at position pos (uniform) of a page, and their values.
 template <int CT, int D>
-__device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
+__device__ __forceinline__ void load_keys(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
                                           int lane)
 {
     using G = Geo<CT, D>;
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 15;
     constexpr int B = k_piece<CT, D>();
 #pragma unroll
     for (int n = 0; n < G::KW * 4 / B; n++)
@@ -132,6 +134,14 @@ __device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int
     } else {
         load_words<G::NB / 2>(raw.ks, c.k, r * (G::NB * 2), scales + pos * (G::NB * 2));
     }
+}
+
+template <int CT, int D>
+__device__ __forceinline__ void load_values(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
+                                            int lane)
+{
+    using G = Geo<CT, D>;
+    const int r = lane & 15, g = lane >> 4, scales = P * G::TB;
     const int vl = g * (4 * G::TB) + r * (G::VL * 4);
     const int sl = ((G::CW * r / 32) * P + 4 * g) * 2;
 #pragma unroll
@@ -140,6 +150,14 @@ __device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int
         // 16 * CW elements further: CW / 2 blocks of P scales
         load_words<2>(raw.vs + 2 * h, c.v, sl, scales + pos * 2 + h * G::CW * P);
     }
+}
+
+template <int CT, int D>
+__device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
+                                          int lane)
+{
+    load_keys<CT, D>(raw, c, pos, P, lane);
+    load_values<CT, D>(raw, c, pos, P, lane);
 }
 
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
@@ -343,24 +361,11 @@ __device__ __forceinline__ int find_sequence(const AttnArgs &a, const AttnPlan &
     return a.batch;
 }
 
-// Position of sequence b's first step in the line.
-__device__ __forceinline__ int64_t line_start(const AttnArgs &a, const AttnPlan &p, int keys, int b,
-                                              int lane)
-{
-    int64_t sum = 0;
-    for (int c = lane; c < b; c += 64)
-        sum += line_steps(a, p, keys, c);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        sum += __shfl_xor(sum, m);
-    return uniform64(sum);
-}
-
 // A workgroup's place in the line: its next steps are `step` .. of (head, row
 // block) `q` of the sequence in w, `left` steps remain.
 struct Cursor {
     Rows w;
-    int q, steps, blocks, step, left;
+    int q, steps, blocks, step, left, span;
 };
 
 __device__ __forceinline__ void set_sequence(Cursor &c, const AttnArgs &a, const AttnPlan &p,
@@ -401,16 +406,18 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
         return c;
     c.q = uniform((int)(at / max(c.steps, 1)));
     c.step = uniform((int)(at - (int64_t)c.q * c.steps));
-    c.left = span;
+    c.left = c.span = span;
     return c;
 }
 
-// What a workgroup does next: keys begin .. end - 1 of the rows in w; `whole`
-// if those are all the rows have, else its sums go to slot `slot`.
+// What a workgroup does next: keys begin .. end - 1 of the rows in w, the
+// first of `parts` parts if begin is 0; `whole` if those are all the rows
+// have, else its sums go to slot `slot`: two a workgroup, the even one for its
+// first rows (part n > 0 of any rows), the odd one for its last.
 struct Work {
     Rows w;
     bool whole;
-    int slot, begin, end;
+    int slot, parts, begin, end;
 };
 
 // false: nothing is left.
@@ -438,6 +445,7 @@ __device__ __forceinline__ bool next_work(Cursor &c, Work &k, const AttnArgs &a,
     k.w.h = c.q / c.blocks;
     k.w.rb = c.q - k.w.h * c.blocks;
     k.whole = take == c.steps;
+    k.parts = k.whole ? 1 : 1 + (c.steps - take + c.span - 1) / c.span;
     k.slot = 2 * blockIdx.x + !first;
     k.begin = c.step * keys;
     k.end = min(c.w.L, (c.step + take) * keys);
@@ -468,9 +476,9 @@ __device__ __forceinline__ void store_frag(const AttnArgs &a, const Rows &w, int
 // = what a score is times, and the running sums.
 template <int D> struct Query {
     h8 q[D / 32];
-    float c, m, l;
+    float c, m;
     int node;
-    f4 o[D / 16];
+    f4 l, o[D / 16];                             // l: the sum in each element
 };
 
 template <int D>
@@ -510,7 +518,7 @@ __device__ __forceinline__ void load_query(Query<D> &x, const AttnArgs &a, const
             x.q[s][e] = (_Float16)(v[s][e] * up);
     x.c = a.scale * 1.44269504088896f * down;
     x.m = NO_REF;
-    x.l = 0.0f;
+    x.l = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < D / 16; t++)
         x.o[t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -556,8 +564,15 @@ __device__ __forceinline__ void mask_scores(f4 (&s)[2], const Query<D> &x, const
     }
 }
 
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 // Probabilities of 32 keys as the operand of the second product; the
-// reference, sum and outputs follow where a score passes it.
+// reference, sum and outputs follow where a score passes it.  The sum is one
+// more product, with a row of ones: it then adds the rounded probabilities,
+// the same ones that weigh the values.
 template <int D>
 __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
 {
@@ -576,40 +591,42 @@ __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
             x.o[t] *= f;
     }
     const float ref = BIAS - x.m;
-    h8 p;
-    float sum = 0.0f;
+    Frag p;
 #pragma unroll
-    for (int T = 0; T < 2; T++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float y = __builtin_amdgcn_exp2f(fmaf(s[T][e], x.c, ref));
-            sum += y;
-            p[4 * T + e] = (_Float16)y;
-        }
-    x.l += sum;
-    return p;
+    for (int i = 0; i < 4; i++) {
+        const int T = i >> 1, e = 2 * (i & 1);
+        const f2 y = {__builtin_amdgcn_exp2f(fmaf(s[T][e], x.c, ref)),
+                      __builtin_amdgcn_exp2f(fmaf(s[T][e + 1], x.c, ref))};
+        p.p[i] = __builtin_convertvector(y, h2);
+    }
+    const _Float16 one = (_Float16)1.0f;
+    x.l = mfma(h8{one, one, one, one, one, one, one, one}, p.v, x.l);
+    return p.v;
 }
 
-__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
+// Sums of cut rows: outputs (fragments of a slot), reference and sum of each
+// row, and for each sequence, key head and row block its first slot and how
+// many parts it has.
+struct Parts {
+    f4 *sum;
+    float2 *ml;
+    int2 *list;
+};
 
 // Joins the KG waves that hold the same rows (rg, of RG groups) and stores
 // the outputs, or their sums where other workgroups have more of the keys.  red: RED
 // fragments of 64 lanes per wave.
 template <int CT, int D, int QT, int RG, int KG>
-__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const Work &k, int rg, int kg, int lane, f4 *red,
-                                       float *ml, float *__restrict__ part,
-                                       float *__restrict__ part_ml)
+__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const AttnPlan &p, const Work &k, int rg, int kg, int lane, f4 *red,
+                                       float *ml, const Parts &parts)
 {
+    lane = fresh(lane);
     constexpr int NT = D / 16, TILES = RG * QT, F = TILES * NT, MINE = QT * NT;
     const int col = lane & 15, g = lane >> 4;
-    float f[QT];
+    float f[QT], l[QT];
 #pragma unroll
     for (int i = 0; i < QT; i++) {
-        x[i].l += __shfl_xor(x[i].l, 16);
-        x[i].l += __shfl_xor(x[i].l, 32);
+        l[i] = x[i].l[0];
         f[i] = 1.0f;
     }
     if constexpr (KG > 1) {
@@ -619,7 +636,7 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
 #pragma unroll
             for (int i = 0; i < QT; i++) {
                 ml[mine + i * 32] = x[i].m;
-                ml[mine + i * 32 + 1] = x[i].l;
+                ml[mine + i * 32 + 1] = l[i];
             }
         __syncthreads();
 #pragma unroll
@@ -634,25 +651,27 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
                 ll += q[n * QT * 32 + 1] * __builtin_amdgcn_exp2f(q[n * QT * 32] - mm);
             f[i] = __builtin_amdgcn_exp2f(x[i].m - mm);
             x[i].m = mm;
-            x[i].l = ll;
+            l[i] = ll;
         }
     }
     const int64_t slot = k.slot;
+    if (parts.list && k.begin == 0 && threadIdx.x == 0)
+        parts.list[(k.w.b * a.kv_heads + k.w.h) * p.row_blocks + k.w.rb] = make_int2(k.slot, k.parts);
     if (!k.whole && kg == 0 && g == 0) {
 #pragma unroll
         for (int i = 0; i < QT; i++) {
-            float2 *q = (float2 *)part_ml + slot * (TILES * 16) + (rg * QT + i) * 16 + col;
-            *q = make_float2(x[i].m, x[i].l);
+            float2 *q = parts.ml + slot * (TILES * 16) + (rg * QT + i) * 16 + col;
+            *q = make_float2(x[i].m, l[i]);
         }
     }
     auto put = [&](int i, int t, f4 sum) {
         if (!k.whole) {
             const int ff = (rg * QT + i) * NT + t;
-            *(f4 *)(part + ((slot * F + ff) * 64 + lane) * 4) = sum;
+            parts.sum[(slot * F + ff) * 64 + lane] = sum;
         } else {
             // nothing seen: zeros
             store_frag<CT, D>(a, k.w, TILES, rg * QT + i, t, lane,
-                              x[i].l == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / x[i].l));
+                              l[i] == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / l[i]));
         }
     };
     if constexpr (KG == 1) {
@@ -705,7 +724,7 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, int entry, int key, in
 // Up to 32 rows: every wave has its own keys.
 template <int CT, int D, int QT>
 __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(
-    AttnArgs a, AttnPlan p, float *__restrict__ part, float *__restrict__ part_ml)
+    AttnArgs a, AttnPlan p, Parts parts)
 {
     using G = Geo<CT, D>;
     __shared__ f4 red[WAVES * RED * 64];
@@ -780,42 +799,38 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
 #pragma unroll
         for (int i = 0; i < QT; i++)
             load_query<D>(x[i], a, w, QT, i, lane);
-        while (kb < k.end) {
+        for (; kb < k.end; kb += 2 * STRIDE) {
             pb = pages_of(en, kb + STRIDE);
             load(rb, pb, kb + STRIDE);
             en = entries_at(kb + 2 * STRIDE);
             compute(ra, pa, kb);
-            kb += STRIDE;
-            if (kb >= k.end)
-                break;
-            pa = pages_of(en, kb + STRIDE);
-            load(ra, pa, kb + STRIDE);
-            en = entries_at(kb + 2 * STRIDE);
-            compute(rb, pb, kb);
-            kb += STRIDE;
+            pa = pages_of(en, kb + 2 * STRIDE);
+            load(ra, pa, kb + 2 * STRIDE);
+            en = entries_at(kb + 3 * STRIDE);
+            compute(rb, pb, kb + STRIDE);        // past the end: no key is seen
         }
-        finish<CT, D, QT, 1, WAVES>(x, a, k, 0, wave, lane, red, ml, part, part_ml);
+        finish<CT, D, QT, 1, WAVES>(x, a, p, k, 0, wave, lane, red, ml, parts);
     }
 }
 
 // More rows: RG groups of waves with QT * 16 rows each, KG = 4 / RG waves per
-// group.  Every wave dequantizes one 16-key tile of 64 keys into LDS, in the
-// fragments of the matrix instructions, while the codes of the next 64 are on
-// their way; then each reads what its rows need (KG = 2: one 32-key half).
+// group.  64 keys at a time lie dequantized in LDS, as the fragments of the
+// matrix instructions; each wave reads what its rows need (KG = 2: one 32-key
+// half) and meanwhile dequantizes a 16-key tile of the next 64 into a second
+// buffer, between its matrix instructions, so that one barrier a step is
+// enough; the codes after those are on their way.
 constexpr int ROW_KEYS = 16 * WAVES;
 
 template <int CT, int D, int QT, int RG>
-__global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p,
-                                                          float *__restrict__ part,
-                                                          float *__restrict__ part_ml)
+__global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
+    AttnArgs a, AttnPlan p, Parts parts)
 {
     using G = Geo<CT, D>;
     constexpr int KG = WAVES / RG;
     constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
     constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
-    __shared__ h8 lds[STAGE > JOIN ? STAGE : JOIN];
+    __shared__ h8 lds[2 * STAGE > JOIN ? 2 * STAGE : JOIN];
     __shared__ float ml[WAVES * QT * 16 * 2];
-    h8 *kf = lds, *vf = lds + K_FRAGS * 64;
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int rg = wave / KG, kg = wave % KG;
     const int P = 1 << a.log_page;
@@ -826,60 +841,66 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
         const Rows &w = k.w;
         const int32_t *table = a.table + w.b * a.table_stride;
         const int lane = fresh(lane0), g = lane >> 4;
-        Tile<CT, D> raw;
-        int entry[WAVES], page[WAVES];           // of the 64 keys on their way
+        // of the four tiles of 64 keys
         auto entries_at = [&](int kb) {
-#pragma unroll
-            for (int n = 0; n < WAVES; n++)
-                entry[n] = entry_at(a, table, kb + 16 * n);
+            return i4{entry_at(a, table, kb), entry_at(a, table, kb + 16),
+                      entry_at(a, table, kb + 32), entry_at(a, table, kb + 48)};
         };
-        auto load = [&](int kb) {
-#pragma unroll
-            for (int n = 0; n < WAVES; n++)
-                page[n] = page_of(a, entry[n], kb + 16 * n, k.end);
-            int mine = page[0];
-#pragma unroll
-            for (int n = 1; n < WAVES; n++)
-                mine = wave == n ? page[n] : mine;
-            load_tile<CT, D>(raw, chunks_at(a, mine, w.h, cb), (kb + 16 * wave) & (P - 1), P, lane);
+        auto pages_of = [&](i4 e, int kb) {
+            return i4{page_of(a, e.x, kb, k.end), page_of(a, e.y, kb + 16, k.end),
+                      page_of(a, e.z, kb + 32, k.end), page_of(a, e.w, kb + 48, k.end)};
         };
-        entries_at(k.begin);
-        load(k.begin);
-        entries_at(k.begin + ROW_KEYS);
+        auto own = [&](i4 f) { return wave < 2 ? (wave ? f.y : f.x) : (wave == 2 ? f.z : f.w); };
+        auto all_cached = [&](i4 f, int kb) {
+            return kb + ROW_KEYS <= w.ctx && min(min(f.x, f.y), min(f.z, f.w)) >= 0;
+        };
+        Tile<CT, D> raw;
+        auto keep_values = [&](i4 f, int kb) {
+            if (!all_cached(f, kb))
+                drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, own(f) >= 0, w.ctx, w.L);
+        };
+        auto stage_key = [&](h8 *buf, int b) {
+            buf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
+        };
+        auto stage_value = [&](h8 *buf, int t) {
+            union {
+                h2 h[2];
+                u2 u;
+            } v;
+            value_half<CT, D>(raw, t, v.h[0], v.h[1]);
+            ((u2 *)&buf[(K_FRAGS + (wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
+        };
+
+        i4 now = pages_of(entries_at(k.begin), k.begin);
+        i4 en = entries_at(k.begin + ROW_KEYS);
+        load_tile<CT, D>(raw, chunks_at(a, own(now), w.h, cb), (k.begin + 16 * wave) & (P - 1), P,
+                         lane);
         Query<D> x[QT];
 #pragma unroll
         for (int i = 0; i < QT; i++)
             load_query<D>(x[i], a, w, RG * QT, rg * QT + i, lane);
-        for (int kb = k.begin; kb < k.end; kb += ROW_KEYS) {
-            bool ok[WAVES];
-            bool all = kb + ROW_KEYS <= w.ctx;
+        keep_values(now, k.begin);
+        __syncthreads();                         // the last rows' fragments are used up
 #pragma unroll
-            for (int n = 0; n < WAVES; n++) {
-                ok[n] = page[n] >= 0;
-                all = all && ok[n];
-            }
-            if (!all) {
-                bool mine = ok[0];
+        for (int b = 0; b < G::NB; b++)
+            stage_key(lds, b);
 #pragma unroll
-                for (int n = 1; n < WAVES; n++)
-                    mine = wave == n ? ok[n] : mine;
-                drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, mine, w.ctx, w.L);
-            }
-            __syncthreads();                     // the last keys are used up
-#pragma unroll
-            for (int b = 0; b < G::NB; b++)
-                kf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
-#pragma unroll
-            for (int t = 0; t < G::NT; t++) {
-                union {
-                    h2 h[2];
-                    u2 u;
-                } v;
-                value_half<CT, D>(raw, t, v.h[0], v.h[1]);
-                ((u2 *)&vf[((wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
-            }
-            load(kb + ROW_KEYS);
-            entries_at(kb + 2 * ROW_KEYS);
+        for (int t = 0; t < G::NT; t++)
+            stage_value(lds, t);
+        i4 next = pages_of(en, k.begin + ROW_KEYS);
+        load_tile<CT, D>(raw, chunks_at(a, own(next), w.h, cb),
+                         (k.begin + ROW_KEYS + 16 * wave) & (P - 1), P, lane);
+        en = entries_at(k.begin + 2 * ROW_KEYS);
+        int turn = 0;
+        for (int kb = k.begin; kb < k.end; kb += ROW_KEYS, turn ^= 1) {
+            const h8 *kf = lds + turn * STAGE, *vf = kf + K_FRAGS * 64;
+            h8 *put = lds + (turn ^ 1) * STAGE;
+            const bool all = all_cached(now, kb);
+            const i4 after = pages_of(en, kb + 2 * ROW_KEYS);
+            const Chunks ch = chunks_at(a, own(after), w.h, cb);
+            const int pos = (kb + 2 * ROW_KEYS + 16 * wave) & (P - 1);
+            en = entries_at(kb + 3 * ROW_KEYS);
+            keep_values(next, kb + ROW_KEYS);
             __syncthreads();
 #pragma unroll
             for (int n = 0; n < 2; n++) {
@@ -887,7 +908,8 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
                     continue;
                 const int kp = kb + STEP * n;
                 if (kp >= k.end)
-                    continue;
+                    continue;                    // then nothing is to be staged either
+                const bool stage = KG == 2 || n == 0;
                 // all of a step's keys are asked for before the first product,
                 // all of its values before the softmax: the reads' latency
                 // passes behind them
@@ -903,11 +925,16 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
                     for (int i = 0; i < QT; i++)
                         s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int b = 0; b < G::NB; b++)
+                    for (int b = 0; b < G::NB; b++) {
 #pragma unroll
                         for (int i = 0; i < QT; i++)
                             s[i][T] = mfma(kv[T * G::NB + b], x[i].q[b], s[i][T]);
+                        if (stage && T == b % 2)
+                            stage_key(put, b);
+                    }
                 }
+                if (stage)
+                    load_keys<CT, D>(raw, ch, pos, P, lane);
 #pragma unroll
                 for (int t = 0; t < G::NT; t++)
                     vv[t] = vf[(n * G::NT + t) * 64 + lane];
@@ -915,29 +942,36 @@ __global__ __launch_bounds__(THREADS, 2) void k_attn_rows(AttnArgs a, AttnPlan p
                 if (!all)
 #pragma unroll
                     for (int i = 0; i < QT; i++)
-                        mask_scores<D>(s[i], x[i], a, w, kp, ok[2 * n], ok[2 * n + 1], g);
+                        mask_scores<D>(s[i], x[i], a, w, kp, (n ? now.z : now.x) >= 0,
+                                       (n ? now.w : now.y) >= 0, g);
                 h8 pr[QT];
 #pragma unroll
                 for (int i = 0; i < QT; i++)
                     pr[i] = softmax_step<D>(s[i], x[i]);
 #pragma unroll
-                for (int t = 0; t < G::NT; t++)
+                for (int t = 0; t < G::NT; t++) {
 #pragma unroll
                     for (int i = 0; i < QT; i++)
                         x[i].o[t] = mfma(vv[t], pr[i], x[i].o[t]);
+                    if (stage)
+                        stage_value(put, t);
+                }
+                if (stage)
+                    load_values<CT, D>(raw, ch, pos, P, lane);
             }
+            now = next;
+            next = after;
         }
-        finish<CT, D, QT, RG, KG>(x, a, k, rg, kg, lane, (f4 *)lds, ml, part, part_ml);
+        finish<CT, D, QT, RG, KG>(x, a, p, k, rg, kg, lane, (f4 *)lds, ml, parts);
     }
 }
 
-// Joins the sums of a head and row block whose steps several workgroups took,
-// one workgroup per fragment.  Wave n adds parts n, n + 4, ... (four loads in
-// flight), the waves' sums are joined through LDS.
-template <int CT, int D>
-__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p, int keys,
-                                                          const float *__restrict__ part,
-                                                          const float *__restrict__ part_ml)
+// Joins the parts of a head and row block, each rescaled to the largest
+// reference.  A wave adds one fragment's parts in order (the next ones' loads
+// in flight); with many parts (SHARED) the four waves of a workgroup take
+// every fourth part of one fragment, and their sums are joined through LDS.
+template <int CT, int D, bool SHARED>
+__global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p, Parts parts)
 {
     constexpr int NT = D / 16;
     __shared__ f4 red[WAVES][64];
@@ -945,23 +979,19 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
     const uint32_t q = blockIdx.x - b * per;
+    const int32_t *list = (const int32_t *)(parts.list + blockIdx.x);
+    const int slot0 = load_uniform(list), n_parts = load_uniform(list + 1);
     Rows w = rows_of(a, (int)b);
     w.h = (int)(q / p.row_blocks);
     w.rb = (int)(q - w.h * p.row_blocks);
-    const int steps = steps_of(w, keys), blocks = blocks_of(a, p, w);
-    if (w.rb >= blocks)
+    const int F = p.tiles * NT, ff = SHARED ? blockIdx.y : blockIdx.y * WAVES + wave;
+    // rows that do not exist have no entry in the list
+    if (w.rb >= blocks_of(a, p, w) || n_parts <= 1 || ff >= F)
         return;
-    const int64_t span = span_of(a, p, keys, lane);
-    const int64_t from = (b ? line_start(a, p, keys, (int)b, lane) : 0) +
-                         (int64_t)(w.h * blocks + w.rb) * steps;
-    const int first = uniform((int)(from / span)), last = uniform((int)((from + steps - 1) / span));
-    if (first == last)
-        return;
-    const int late = uniform(from != first * span);     // it is not the first workgroup's first
-    const int F = p.tiles * NT, ff = blockIdx.y, tile = ff / NT;
-    const float2 *mlp = (const float2 *)part_ml + tile * 16 + (lane & 15);
-    const int ms = p.tiles * 16, n_parts = last - first + 1;
-    auto slot = [&](int n) { return (int64_t)(2 * (first + n) + (n == 0 ? late : 0)); };
+    const int tile = ff / NT, ms = p.tiles * 16;
+    const float2 *mlp = parts.ml + tile * 16 + (lane & 15);
+    const f4 *o = parts.sum + ff * 64 + lane;
+    auto slot = [&](int n) { return (int64_t)(n ? (slot0 | 1) - 1 + 2 * n : slot0); };
     float mm = NO_REF;
     for (int n = lane >> 4; n < n_parts; n += 4)
         mm = fmaxf(mm, mlp[slot(n) * ms].x);
@@ -969,21 +999,22 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
     mm = fmaxf(mm, __shfl_xor(mm, 32));
     float ll = 0.0f;
     f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float *o = part + (ff * 64 + lane) * 4;
 #pragma unroll 4
-    for (int n = wave; n < n_parts; n += WAVES) {
+    for (int n = SHARED ? wave : 0; n < n_parts; n += SHARED ? WAVES : 1) {
         const float2 t = mlp[slot(n) * ms];
         const float f = __builtin_amdgcn_exp2f(t.x - mm);
         ll += f * t.y;
-        sum += f * *(const f4 *)(o + slot(n) * F * 256);
+        sum += f * o[slot(n) * F * 64];
     }
-    red[wave][lane] = sum;
-    redl[wave][lane] = ll;
-    __syncthreads();
-    if (wave)
-        return;
-    sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-    ll = (redl[0][lane] + redl[1][lane]) + (redl[2][lane] + redl[3][lane]);
+    if constexpr (SHARED) {
+        red[wave][lane] = sum;
+        redl[wave][lane] = ll;
+        __syncthreads();
+        if (wave)
+            return;
+        sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        ll = (redl[0][lane] + redl[1][lane]) + (redl[2][lane] + redl[3][lane]);
+    }
     store_frag<CT, D>(a, w, p.tiles, tile, ff % NT, lane,
                       ll == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / ll));
 }
@@ -1000,23 +1031,30 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
     const int F = p.tiles * (D / 16);
-    float *part = (float *)scratch;
-    float *ml = part ? part + (size_t)2 * p.groups * F * 256 : nullptr;
+    Parts parts{nullptr, nullptr, nullptr};
+    if (p.groups > 1) {
+        parts.sum = (f4 *)scratch;
+        parts.ml = (float2 *)(parts.sum + (size_t)2 * p.groups * F * 64);
+        parts.list = (int2 *)(parts.ml + (size_t)2 * p.groups * p.tiles * 16);
+    }
     const dim3 grid((unsigned)blocks);
     constexpr int QT = rows_qt(D);
     if (p.row_groups == 4)
-        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(a, p, parts);
     else if (p.row_groups == 2)
-        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(a, p, parts);
     else if (p.tiles == 1)
-        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(a, p, parts);
     else if constexpr (D <= 128)
-        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p, part, ml);
+        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p, parts);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.groups <= 1)
         return e;
-    k_attn_combine<CT, D><<<dim3((unsigned)units, (unsigned)F), THREADS, 0, s>>>(
-        a, p, p.row_groups > 1 ? ROW_KEYS : STRIDE, part, ml);
+    if (p.groups >= 16 * units)
+        k_attn_combine<CT, D, true><<<dim3((unsigned)units, (unsigned)F), THREADS, 0, s>>>(a, p, parts);
+    else
+        k_attn_combine<CT, D, false><<<dim3((unsigned)units, (unsigned)((F + WAVES - 1) / WAVES)),
+                                       THREADS, 0, s>>>(a, p, parts);
     return hipGetLastError();
 }
 
@@ -1063,11 +1101,12 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     return p;
 }
 
-size_t attn_scratch_bytes(const AttnPlan &p, int D)
+size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads)
 {
-    // sums of one workgroup: at most its first and its last rows are shared
-    return p.groups <= 1 ? 0
-                         : (size_t)2 * p.groups * p.tiles * ((size_t)(D / 16) * 256 + 32) * sizeof(float);
+    if (p.groups <= 1)
+        return 0;
+    return (size_t)2 * p.groups * p.tiles * ((size_t)(D / 16) * 1024 + 16 * sizeof(float2)) +
+           (size_t)batch * kv_heads * p.row_blocks * sizeof(int2);
 }
 
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,

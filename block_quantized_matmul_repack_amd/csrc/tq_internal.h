@@ -431,7 +431,7 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys);
-size_t attn_scratch_bytes(const AttnPlan &p, int D);
+size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads);
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
                             void *scratch, hipStream_t s);
 
