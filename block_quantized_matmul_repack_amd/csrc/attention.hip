@@ -60,7 +60,6 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef int i4 __attribute__((ext_vector_type(4)));
 
 template <int CT, int D> struct Geo {
     static constexpr int NB = D / 32;            // 32-element blocks = matrix steps of Q K^T
@@ -83,39 +82,79 @@ template <int CT, int D> struct Tile {
 };
 
 // N dwords (aligned to 4 N bytes, N = 3 to 4) at byte v + s of a buffer, v per
-// lane and s uniform; zeros past its end.
-template <int N>
+// lane and s uniform; zeros past its end.  AUX: BUF_NT where no other
+// workgroup reads the same keys (one row block): 64 sequences of one token
+// 262 -> 241 us; with two row blocks the caches serve the second.
+template <int N, int AUX>
 __device__ __forceinline__ void load_words(uint32_t *w, __amdgpu_buffer_rsrc_t b, int v, int s)
 {
     if constexpr (N == 4) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b128(b, v, s, 0);
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(b, v, s, AUX);
         w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
     } else if constexpr (N == 3) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b96(b, v, s, 0);
+        const auto x = __builtin_amdgcn_raw_buffer_load_b96(b, v, s, AUX);
         w[0] = x[0]; w[1] = x[1]; w[2] = x[2];
     } else if constexpr (N == 2) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b64(b, v, s, 0);
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(b, v, s, AUX);
         w[0] = x[0]; w[1] = x[1];
     } else {
-        w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, v, s, 0);
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, v, s, AUX);
     }
 }
 
-// The chunks of one page and head; of no bytes where there is no page, so
-// that its loads read zeros and move nothing.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// A read-only word at a uniform address, through the scalar cache: it does
+// not wait behind the tile loads in flight.
+__device__ __forceinline__ int load_uniform(const int32_t *p)
+{
+    return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+}
+
+// Where the keys of one sequence and key head lie (all uniform).
+struct Place {
+    const int32_t *table;
+    uint64_t k, v;                   // of page 0's chunk
+    uint32_t stride, pages;          // bytes from page to page
+    int bytes, log_page, last, end;  // of a chunk; the table's last entry; keys end before `end`
+    int plain;                       // keys before it are cached ones of the range
+};
+
+// The page table's entry for a key.  No branch: a load that may not happen
+// would make every wait for the tile loads in flight wait for all of them.
+__device__ __forceinline__ int entry_at(const Place &c, int key)
+{
+    return load_uniform(c.table + min(key >> c.log_page, c.last));
+}
+
+__device__ __forceinline__ bool mapped(const Place &c, int entry, int key)
+{
+    return key < c.end && (uint32_t)entry < c.pages;
+}
+
+// The chunks of one page; of no bytes where there is none or the keys have
+// ended, so that its loads read zeros and move nothing.
 struct Chunks {
     __amdgpu_buffer_rsrc_t k, v;
 };
 
-__device__ __forceinline__ Chunks chunks_at(const AttnArgs &a, int page, int h, int bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(uint64_t at, int n)
 {
-    const int64_t at = ((int64_t)max(page, 0) * a.kv_heads + h) * bytes;
-    const int n = page < 0 ? 0 : bytes;
-    return Chunks{make_rsrc(a.kc + at, n), make_rsrc(a.vc + at, n)};
+    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)at), hi = (uint32_t)uniform((int)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0,
+                                             uniform(n), 0x00020000);
+}
+
+__device__ __forceinline__ Chunks chunks_at(const Place &c, int entry, int key)
+{
+    const bool there = mapped(c, entry, key);
+    const int n = there ? c.bytes : 0;
+    const uint64_t at = (uint64_t)(there ? (uint32_t)entry : 0) * c.stride;
+    return Chunks{chunk_rsrc(c.k + at, n), chunk_rsrc(c.v + at, n)};
 }
 
 // The 16 keys at position pos (uniform) of a page, and their values.
-template <int CT, int D>
+template <int CT, int D, int AUX>
 __device__ __forceinline__ void load_keys(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
                                           int lane)
 {
@@ -124,19 +163,19 @@ __device__ __forceinline__ void load_keys(Tile<CT, D> &raw, const Chunks &c, int
     constexpr int B = k_piece<CT, D>();
 #pragma unroll
     for (int n = 0; n < G::KW * 4 / B; n++)
-        load_words<B / 4>(raw.k + n * (B / 4), c.k, lane * B + n * (64 * B), pos * G::TB);
+        load_words<B / 4, AUX>(raw.k + n * (B / 4), c.k, lane * B + n * (64 * B), pos * G::TB);
     const int scales = P * G::TB;
     if constexpr (G::NB == 3) {
-        raw.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6, scales + pos * 6, 0) |
+        raw.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6, scales + pos * 6, AUX) |
                     (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6 + 2,
-                                                                             scales + pos * 6, 0) << 16;
-        raw.ks[1] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6 + 4, scales + pos * 6, 0);
+                                                                             scales + pos * 6, AUX) << 16;
+        raw.ks[1] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(c.k, r * 6 + 4, scales + pos * 6, AUX);
     } else {
-        load_words<G::NB / 2>(raw.ks, c.k, r * (G::NB * 2), scales + pos * (G::NB * 2));
+        load_words<G::NB / 2, AUX>(raw.ks, c.k, r * (G::NB * 2), scales + pos * (G::NB * 2));
     }
 }
 
-template <int CT, int D>
+template <int CT, int D, int AUX>
 __device__ __forceinline__ void load_values(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
                                             int lane)
 {
@@ -146,18 +185,18 @@ __device__ __forceinline__ void load_values(Tile<CT, D> &raw, const Chunks &c, i
     const int sl = ((G::CW * r / 32) * P + 4 * g) * 2;
 #pragma unroll
     for (int h = 0; h < G::NH; h++) {
-        load_words<G::VL>(raw.v + h * G::VL, c.v, vl + h * (64 * G::VL), pos * G::TB);
+        load_words<G::VL, AUX>(raw.v + h * G::VL, c.v, vl + h * (64 * G::VL), pos * G::TB);
         // 16 * CW elements further: CW / 2 blocks of P scales
-        load_words<2>(raw.vs + 2 * h, c.v, sl, scales + pos * 2 + h * G::CW * P);
+        load_words<2, AUX>(raw.vs + 2 * h, c.v, sl, scales + pos * 2 + h * G::CW * P);
     }
 }
 
-template <int CT, int D>
+template <int CT, int D, int AUX>
 __device__ __forceinline__ void load_tile(Tile<CT, D> &raw, const Chunks &c, int pos, int P,
                                           int lane)
 {
-    load_keys<CT, D>(raw, c, pos, P, lane);
-    load_values<CT, D>(raw, c, pos, P, lane);
+    load_keys<CT, D, AUX>(raw, c, pos, P, lane);
+    load_values<CT, D, AUX>(raw, c, pos, P, lane);
 }
 
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
@@ -243,8 +282,6 @@ __device__ __forceinline__ void drop_values(Tile<CT, D> &raw, int key, bool ther
         raw.vs[h] = keep(raw.vs[h], 2 * (h & 1));
 }
 
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // x, which the compiler takes for a new value: what is derived from it is not
 // kept in registers from one turn of an outer loop to the next.
 __device__ __forceinline__ int fresh(int x)
@@ -253,11 +290,28 @@ __device__ __forceinline__ int fresh(int x)
     return x;
 }
 
-// A read-only word at a uniform address, through the scalar cache: it does
-// not wait behind the tile loads in flight.
-__device__ __forceinline__ int load_uniform(const int32_t *p)
+// Sums of cut rows: outputs (fragments of a slot), reference and sum of each
+// row, and for each sequence, key head and row block its first slot and how
+// many parts it has.
+struct Parts {
+    f4 *sum;
+    float2 *ml;
+    int2 *list;
+};
+
+struct Launch {
+    AttnArgs a;
+    AttnPlan p;
+    Parts parts;
+};
+
+// The kernel's argument, read anew: what one phase of a kernel has loaded of
+// it is not kept in scalar registers through the others.
+__device__ __forceinline__ const Launch &arguments()
 {
-    return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();     // in the constant address space
+    asm volatile("" : "+s"(p));
+    return *(const Launch *)p;
 }
 
 // One sequence, and key head h and row block rb of it; row r is (token
@@ -421,9 +475,11 @@ struct Work {
 };
 
 // false: nothing is left.
-__device__ __forceinline__ bool next_work(Cursor &c, Work &k, const AttnArgs &a, const AttnPlan &p,
-                                          int keys, bool first)
+__device__ __forceinline__ bool next_work(Cursor &c, Work &k, const Launch &launch, int keys,
+                                          bool first)
 {
+    const AttnArgs &a = launch.a;
+    const AttnPlan &p = launch.p;
     if (!first) {
         if (c.left <= 0 || p.groups == 0)
             return false;
@@ -604,22 +660,16 @@ __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
     return p.v;
 }
 
-// Sums of cut rows: outputs (fragments of a slot), reference and sum of each
-// row, and for each sequence, key head and row block its first slot and how
-// many parts it has.
-struct Parts {
-    f4 *sum;
-    float2 *ml;
-    int2 *list;
-};
-
 // Joins the KG waves that hold the same rows (rg, of RG groups) and stores
 // the outputs, or their sums where other workgroups have more of the keys.  red: RED
 // fragments of 64 lanes per wave.
 template <int CT, int D, int QT, int RG, int KG>
-__device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, const AttnPlan &p, const Work &k, int rg, int kg, int lane, f4 *red,
-                                       float *ml, const Parts &parts)
+__device__ __forceinline__ void finish(Query<D> (&x)[QT], const Launch &launch, const Work &k,
+                                       int rg, int kg, int lane, f4 *red, float *ml)
 {
+    const AttnArgs &a = launch.a;
+    const AttnPlan &p = launch.p;
+    const Parts &parts = launch.parts;
     lane = fresh(lane);
     constexpr int NT = D / 16, TILES = RG * QT, F = TILES * NT, MINE = QT * NT;
     const int col = lane & 15, g = lane >> 4;
@@ -707,52 +757,60 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const AttnArgs &a, con
     }
 }
 
-// The page table's entry for a key, and the page it means: -1 where there is
-// nothing to read.  Two calls, so that the entry can be asked for early; and
-// no branch: a load that may not happen would make every wait for the tile
-// loads in flight wait for all of them.
-__device__ __forceinline__ int entry_at(const AttnArgs &a, const int32_t *table, int key)
+template <int CT, int D>
+__device__ __forceinline__ Place place_of(const AttnArgs &a, const Work &k)
 {
-    return load_uniform(table + min(key >> a.log_page, a.table_pages - 1));
+    Place c;
+    c.table = a.table + k.w.b * a.table_stride;
+    c.bytes = (int)chunk_bytes(CT, D, 1 << a.log_page);
+    c.stride = (uint32_t)a.kv_heads * c.bytes;
+    c.k = (uint64_t)a.kc + (uint32_t)(k.w.h * c.bytes);
+    c.v = (uint64_t)a.vc + (uint32_t)(k.w.h * c.bytes);
+    c.pages = (uint32_t)a.pages;
+    c.log_page = a.log_page;
+    c.last = a.table_pages - 1;
+    c.end = k.end;
+    c.plain = min(k.w.ctx, k.end);
+    return c;
 }
 
-__device__ __forceinline__ int page_of(const AttnArgs &a, int entry, int key, int end)
+// Whether all pages of keys begin .. end - 1 are there.
+__device__ __forceinline__ bool all_mapped(const Place &c, int begin, int lane)
 {
-    return key < end && (int64_t)(uint32_t)entry < a.pages ? entry : -1;
+    bool bad = false;
+    for (int i = (begin >> c.log_page) + lane; i <= (c.end - 1) >> c.log_page; i += 64)
+        bad = bad || (uint32_t)c.table[i] >= c.pages;
+    return !__any(bad);
 }
 
 // Up to 32 rows: every wave has its own keys.
 template <int CT, int D, int QT>
 __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(
-    AttnArgs a, AttnPlan p, Parts parts)
+    Launch launch)
 {
     using G = Geo<CT, D>;
     __shared__ f4 red[WAVES * RED * 64];
     __shared__ float ml[WAVES * QT * 16 * 2];
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int P = 1 << a.log_page;
-    const int cb = (int)chunk_bytes(CT, D, P);
-    Cursor cur = first_span(a, p, STRIDE, lane0);
+    const int P = 1 << launch.a.log_page;
+    Cursor cur = first_span(launch.a, launch.p, STRIDE, lane0);
     Work k;
-    for (bool first = true; next_work(cur, k, a, p, STRIDE, first); first = false) {
+    for (bool first = true; next_work(cur, k, arguments(), STRIDE, first); first = false) {
         const Rows &w = k.w;
-        const int32_t *table = a.table + w.b * a.table_stride;
+        const AttnArgs &a = arguments().a;
         const int lane = fresh(lane0), g = lane >> 4;
-        struct Pages {                           // of the two tiles of a step
+        const Place pl = place_of<CT, D>(a, k);
+        struct Two {                             // entries of the two tiles of a step
             int a, b;
         };
-        auto entries_at = [&](int kb) {
-            return Pages{entry_at(a, table, kb), entry_at(a, table, kb + 16)};
-        };
-        auto pages_of = [&](const Pages &e, int kb) {
-            return Pages{page_of(a, e.a, kb, k.end), page_of(a, e.b, kb + 16, k.end)};
-        };
-        auto load = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
-            load_tile<CT, D>(raw[0], chunks_at(a, pg.a, w.h, cb), kb & (P - 1), P, lane);
-            load_tile<CT, D>(raw[1], chunks_at(a, pg.b, w.h, cb), (kb + 16) & (P - 1), P, lane);
+        auto entries_at = [&](int kb) { return Two{entry_at(pl, kb), entry_at(pl, kb + 16)}; };
+        auto load = [&](Tile<CT, D> (&raw)[2], const Two &e, int kb) {
+            load_tile<CT, D, BUF_NT>(raw[0], chunks_at(pl, e.a, kb), kb & (P - 1), P, lane);
+            load_tile<CT, D, BUF_NT>(raw[1], chunks_at(pl, e.b, kb + 16), (kb + 16) & (P - 1), P, lane);
         };
         Query<D> x[QT];
-        auto compute = [&](Tile<CT, D> (&raw)[2], const Pages &pg, int kb) {
+        bool whole_pages;
+        auto compute = [&](Tile<CT, D> (&raw)[2], int kb) {
             f4 s[QT][2];
             auto scores = [&](const Tile<CT, D> &tile, int T) {
 #pragma unroll
@@ -768,12 +826,15 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
             };
             scores(raw[0], 0);
             scores(raw[1], 1);
-            if (kb + STEP > w.ctx || pg.a < 0 || pg.b < 0) {
+            if (kb + STEP > pl.plain || !whole_pages) {
+                // some keys are new tokens, past the end or on no page
+                const bool oka = mapped(pl, entry_at(pl, kb), kb);
+                const bool okb = mapped(pl, entry_at(pl, kb + 16), kb + 16);
 #pragma unroll
                 for (int i = 0; i < QT; i++)
-                    mask_scores<D>(s[i], x[i], a, w, kb, pg.a >= 0, pg.b >= 0, g);
-                drop_values<CT, D>(raw[0], kb + 4 * g, pg.a >= 0, w.ctx, w.L);
-                drop_values<CT, D>(raw[1], kb + 16 + 4 * g, pg.b >= 0, w.ctx, w.L);
+                    mask_scores<D>(s[i], x[i], arguments().a, w, kb, oka, okb, g);
+                drop_values<CT, D>(raw[0], kb + 4 * g, oka, w.ctx, w.L);
+                drop_values<CT, D>(raw[1], kb + 16 + 4 * g, okb, w.ctx, w.L);
             }
             h8 pr[QT];
 #pragma unroll
@@ -794,22 +855,21 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
         // numbers of the one after that
         int kb = k.begin + wave * STEP;
         Tile<CT, D> ra[2], rb[2];
-        Pages pa = pages_of(entries_at(kb), kb), pb, en = entries_at(kb + STRIDE);
-        load(ra, pa, kb);
+        load(ra, entries_at(kb), kb);
+        Two en = entries_at(kb + STRIDE);
+        whole_pages = all_mapped(pl, k.begin, lane);
 #pragma unroll
         for (int i = 0; i < QT; i++)
             load_query<D>(x[i], a, w, QT, i, lane);
         for (; kb < k.end; kb += 2 * STRIDE) {
-            pb = pages_of(en, kb + STRIDE);
-            load(rb, pb, kb + STRIDE);
+            load(rb, en, kb + STRIDE);
             en = entries_at(kb + 2 * STRIDE);
-            compute(ra, pa, kb);
-            pa = pages_of(en, kb + 2 * STRIDE);
-            load(ra, pa, kb + 2 * STRIDE);
+            compute(ra, kb);
+            load(ra, en, kb + 2 * STRIDE);
             en = entries_at(kb + 3 * STRIDE);
-            compute(rb, pb, kb + STRIDE);        // past the end: no key is seen
+            compute(rb, kb + STRIDE);            // past the end no key is seen
         }
-        finish<CT, D, QT, 1, WAVES>(x, a, p, k, 0, wave, lane, red, ml, parts);
+        finish<CT, D, QT, 1, WAVES>(x, arguments(), k, 0, wave, lane, red, ml);
     }
 }
 
@@ -823,41 +883,34 @@ constexpr int ROW_KEYS = 16 * WAVES;
 
 template <int CT, int D, int QT, int RG>
 __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
-    AttnArgs a, AttnPlan p, Parts parts)
+    Launch launch)
 {
     using G = Geo<CT, D>;
-    constexpr int KG = WAVES / RG;
+    constexpr int KG = WAVES / RG, AUX = RG == 2 ? BUF_NT : 0;
     constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
     constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
     __shared__ h8 lds[2 * STAGE > JOIN ? 2 * STAGE : JOIN];
     __shared__ float ml[WAVES * QT * 16 * 2];
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int rg = wave / KG, kg = wave % KG;
-    const int P = 1 << a.log_page;
-    const int cb = (int)chunk_bytes(CT, D, P);
-    Cursor cur = first_span(a, p, ROW_KEYS, lane0);
+    const int P = 1 << launch.a.log_page;
+    Cursor cur = first_span(launch.a, launch.p, ROW_KEYS, lane0);
     Work k;
-    for (bool first = true; next_work(cur, k, a, p, ROW_KEYS, first); first = false) {
+    for (bool first = true; next_work(cur, k, arguments(), ROW_KEYS, first); first = false) {
         const Rows &w = k.w;
-        const int32_t *table = a.table + w.b * a.table_stride;
+        const AttnArgs &a = arguments().a;
         const int lane = fresh(lane0), g = lane >> 4;
-        // of the four tiles of 64 keys
-        auto entries_at = [&](int kb) {
-            return i4{entry_at(a, table, kb), entry_at(a, table, kb + 16),
-                      entry_at(a, table, kb + 32), entry_at(a, table, kb + 48)};
-        };
-        auto pages_of = [&](i4 e, int kb) {
-            return i4{page_of(a, e.x, kb, k.end), page_of(a, e.y, kb + 16, k.end),
-                      page_of(a, e.z, kb + 32, k.end), page_of(a, e.w, kb + 48, k.end)};
-        };
-        auto own = [&](i4 f) { return wave < 2 ? (wave ? f.y : f.x) : (wave == 2 ? f.z : f.w); };
-        auto all_cached = [&](i4 f, int kb) {
-            return kb + ROW_KEYS <= w.ctx && min(min(f.x, f.y), min(f.z, f.w)) >= 0;
-        };
+        const Place pl = place_of<CT, D>(a, k);
         Tile<CT, D> raw;
-        auto keep_values = [&](i4 f, int kb) {
-            if (!all_cached(f, kb))
-                drop_values<CT, D>(raw, kb + 16 * wave + 4 * g, own(f) >= 0, w.ctx, w.L);
+        // the wave's tile of the 64 keys from kb
+        auto chunks = [&](int entry, int kb) { return chunks_at(pl, entry, kb + 16 * wave); };
+        auto entry = [&](int kb) { return entry_at(pl, kb + 16 * wave); };
+        bool whole_pages;
+        auto keep_values = [&](int kb) {
+            if (kb + ROW_KEYS > pl.plain || !whole_pages) {
+                const int key = kb + 16 * wave;
+                drop_values<CT, D>(raw, key + 4 * g, mapped(pl, entry_at(pl, key), key), w.ctx, w.L);
+            }
         };
         auto stage_key = [&](h8 *buf, int b) {
             buf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
@@ -871,15 +924,15 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
             ((u2 *)&buf[(K_FRAGS + (wave >> 1) * G::NT + t) * 64 + lane])[wave & 1] = v.u;
         };
 
-        i4 now = pages_of(entries_at(k.begin), k.begin);
-        i4 en = entries_at(k.begin + ROW_KEYS);
-        load_tile<CT, D>(raw, chunks_at(a, own(now), w.h, cb), (k.begin + 16 * wave) & (P - 1), P,
+        load_tile<CT, D, AUX>(raw, chunks(entry(k.begin), k.begin), (k.begin + 16 * wave) & (P - 1), P,
                          lane);
+        int en = entry(k.begin + ROW_KEYS);
+        whole_pages = all_mapped(pl, k.begin, lane);
         Query<D> x[QT];
 #pragma unroll
         for (int i = 0; i < QT; i++)
             load_query<D>(x[i], a, w, RG * QT, rg * QT + i, lane);
-        keep_values(now, k.begin);
+        keep_values(k.begin);
         __syncthreads();                         // the last rows' fragments are used up
 #pragma unroll
         for (int b = 0; b < G::NB; b++)
@@ -887,20 +940,17 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
 #pragma unroll
         for (int t = 0; t < G::NT; t++)
             stage_value(lds, t);
-        i4 next = pages_of(en, k.begin + ROW_KEYS);
-        load_tile<CT, D>(raw, chunks_at(a, own(next), w.h, cb),
+        load_tile<CT, D, AUX>(raw, chunks(en, k.begin + ROW_KEYS),
                          (k.begin + ROW_KEYS + 16 * wave) & (P - 1), P, lane);
-        en = entries_at(k.begin + 2 * ROW_KEYS);
+        en = entry(k.begin + 2 * ROW_KEYS);
         int turn = 0;
         for (int kb = k.begin; kb < k.end; kb += ROW_KEYS, turn ^= 1) {
             const h8 *kf = lds + turn * STAGE, *vf = kf + K_FRAGS * 64;
             h8 *put = lds + (turn ^ 1) * STAGE;
-            const bool all = all_cached(now, kb);
-            const i4 after = pages_of(en, kb + 2 * ROW_KEYS);
-            const Chunks ch = chunks_at(a, own(after), w.h, cb);
+            const Chunks ch = chunks(en, kb + 2 * ROW_KEYS);
             const int pos = (kb + 2 * ROW_KEYS + 16 * wave) & (P - 1);
-            en = entries_at(kb + 3 * ROW_KEYS);
-            keep_values(next, kb + ROW_KEYS);
+            en = entry(kb + 3 * ROW_KEYS);
+            keep_values(kb + ROW_KEYS);
             __syncthreads();
 #pragma unroll
             for (int n = 0; n < 2; n++) {
@@ -934,16 +984,18 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
                     }
                 }
                 if (stage)
-                    load_keys<CT, D>(raw, ch, pos, P, lane);
+                    load_keys<CT, D, AUX>(raw, ch, pos, P, lane);
 #pragma unroll
                 for (int t = 0; t < G::NT; t++)
                     vv[t] = vf[(n * G::NT + t) * 64 + lane];
                 __builtin_amdgcn_sched_barrier(0);
-                if (!all)
+                if (kp + STEP > pl.plain || !whole_pages) {
+                    const bool oka = mapped(pl, entry_at(pl, kp), kp);
+                    const bool okb = mapped(pl, entry_at(pl, kp + 16), kp + 16);
 #pragma unroll
                     for (int i = 0; i < QT; i++)
-                        mask_scores<D>(s[i], x[i], a, w, kp, (n ? now.z : now.x) >= 0,
-                                       (n ? now.w : now.y) >= 0, g);
+                        mask_scores<D>(s[i], x[i], arguments().a, w, kp, oka, okb, g);
+                }
                 h8 pr[QT];
 #pragma unroll
                 for (int i = 0; i < QT; i++)
@@ -957,12 +1009,10 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
                         stage_value(put, t);
                 }
                 if (stage)
-                    load_values<CT, D>(raw, ch, pos, P, lane);
+                    load_values<CT, D, AUX>(raw, ch, pos, P, lane);
             }
-            now = next;
-            next = after;
         }
-        finish<CT, D, QT, RG, KG>(x, a, p, k, rg, kg, lane, (f4 *)lds, ml, parts);
+        finish<CT, D, QT, RG, KG>(x, arguments(), k, rg, kg, lane, (f4 *)lds, ml);
     }
 }
 
@@ -1040,13 +1090,13 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     const dim3 grid((unsigned)blocks);
     constexpr int QT = rows_qt(D);
     if (p.row_groups == 4)
-        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(a, p, parts);
+        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
     else if (p.row_groups == 2)
-        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(a, p, parts);
+        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
     else if (p.tiles == 1)
-        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(a, p, parts);
+        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
     else if constexpr (D <= 128)
-        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(a, p, parts);
+        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.groups <= 1)
         return e;
