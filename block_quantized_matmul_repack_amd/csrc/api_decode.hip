@@ -34,7 +34,9 @@ bool apart(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t D)
 {
     if (!valid_strides(ts, hs))
         return false;
-    const bool one_head = heads <= 1, one_token = tokens <= 1;
+    if (heads == 0)
+        return true;
+    const bool one_head = heads == 1, one_token = tokens <= 1;
     if (one_head && one_token)
         return true;
     if (one_head)

@@ -13,20 +13,31 @@
 // scalars a, b, so no row is ever written.  Everything is fp64: an index then
 // depends on the order of a sum with a probability of about 1e-13.
 //
-// Bound: the rows the last token is drawn from are read once (HBM; for one
-// sequence, latency: tokens -> their probabilities -> the row).  A sequence's
-// row is cut into tiles of TILE elements, one workgroup each; every workgroup
-// walks the drafted nodes itself (a few values in LDS), sums its tile, and
-// the last one to finish finds the tile that holds the threshold and the
-// element in it.  Trees drafted with probabilities need whole-row sums during
-// the walk and run as one workgroup per sequence instead.
+// Bound: the rows the last token is drawn from are read once; for few
+// sequences, latency (starts -> nodes -> their probabilities -> the row -> the
+// tile).  A sequence's row is cut into tiles of TILE elements, one a wave;
+// the first wave of every workgroup of 16 walks the drafted nodes, 64 at a
+// time in its lanes (a ballot finds the children: a turn per child tried, not
+// per node), the waves sum their tiles, and the last workgroup of the
+// sequence finds the tile that holds the threshold and the element in it.
+// Reductions are DPP adds, not LDS permutes; one device-scope count per
+// workgroup, on a cache line of its sequence's own, since such atomics on one
+// line follow each other (with one per wave on a shared line 32 trees took 44
+// us).  One sequence of
+// 5 nodes over 128001 tokens: CHAIN_US us; 32 trees of up to 31: TREES_US us.
+// Trees drafted with probabilities need whole-row sums during the walk and
+// run as one workgroup per sequence instead.
+#include <algorithm>
+
 #include "tq_internal.h"
 
 namespace tq {
 namespace {
 
-constexpr int TILE = 2048;
-constexpr int MAX_NODES = 1024;
+constexpr int TILE = 512;                        // 8 elements a lane
+constexpr int PER = TILE / 64;
+constexpr int WAVES = 16, THREADS = 64 * WAVES;
+constexpr int MOST_TILES = 64;                   // of one workgroup
 
 template <int DT> __device__ __forceinline__ double prob(const void *p, int64_t i)
 {
@@ -40,19 +51,38 @@ template <int DT> __device__ __forceinline__ double prob(const void *p, int64_t 
 
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }
 
-// What the walk needs of each node, and its result.
-struct Walk {
-    int parent[MAX_NODES], token[MAX_NODES];
-    float u[MAX_NODES];
-    double p[MAX_NODES], q[MAX_NODES];
-    int path[MAX_NODES];                         // accepted nodes, then the rejected ones
-};
+// Lane k's value, k uniform.
+__device__ __forceinline__ int lane_of(int x, int k) { return __builtin_amdgcn_readlane(x, k); }
 
-struct Found {
-    int taken, rejected, node;                   // path[0..taken), then `rejected` more
-    double a, b;                                 // last token from max(a p - b q, 0), ...
-    double a0, b0;                               // ... or, where that is all zero, this one
-};
+__device__ __forceinline__ double lane_of(double x, int k)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)lane_of((int)(uint32_t)b, k), hi = (uint32_t)lane_of((int)(b >> 32), k);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive running sum over the lanes: shifts by 1, 2, 4, 8 in each row of
+// 16, then the last lane of a row added to the rows behind it.
+__device__ __forceinline__ double scan_wave(double v)
+{
+    v += dpp<0x111, 0xF>(v);
+    v += dpp<0x112, 0xF>(v);
+    v += dpp<0x114, 0xF>(v);
+    v += dpp<0x118, 0xF>(v);
+    v += dpp<0x142, 0xA>(v);                     // row 0 -> 1, 2 -> 3
+    v += dpp<0x143, 0xC>(v);                     // rows 0, 1 -> 2, 3
+    return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) { return lane_of(scan_wave(v), 63); }
 
 struct Seq {
     int64_t n0;
@@ -66,375 +96,339 @@ __device__ __forceinline__ Seq seq_of(const VerifyArgs &a, int b)
     return {s0, (int)min(max(s1 - s0, (int64_t)0), (int64_t)a.width)};
 }
 
-template <int DT>
-__device__ __forceinline__ void load_nodes(const VerifyArgs &a, const Seq &s, Walk &w, int tid,
-                                           int threads)
+// Result of a walk.  took: the accepted nodes, a bit each; gone: the tokens
+// refused at the last node (no draft probabilities only).
+struct Found {
+    int taken, rejected, node;
+    double a, b;                                 // last token from max(a p - b q, 0), ...
+    double a0, b0;                               // ... or, where that is all zero, this one
+};
+
+struct Record {
+    uint64_t *took;                              // [width / 64 rounded up], LDS
+    int *gone;                                   // [width], LDS
+};
+
+__host__ __device__ constexpr size_t record_bytes(int width)
 {
-    for (int i = tid; i < s.T; i += threads) {
-        const int par = a.parents ? a.parents[s.n0 + i] : i - 1;
-        const int64_t x = a.tokens[s.n0 + i];
-        // a child after its parent and inside the vocabulary, or never accepted
-        const bool ok = i > 0 && par >= 0 && par < i && x >= 0 && x < a.vocab;
-        w.parent[i] = i > 0 && par >= 0 && par < i ? par : -1;
-        w.token[i] = (int)(ok ? x : -1);
-        w.u[i] = a.u[s.n0 + i];
-        w.p[i] = ok ? positive(prob<DT>(a.target, (s.n0 + par) * a.target_stride + x)) : 0.0;
-        w.q[i] = ok && a.draft ? prob<DT>(a.draft, (s.n0 + par) * a.draft_stride + x) : 0.0;
-    }
+    return (size_t)((width + 63) / 64) * 8 + (size_t)((width + 1) / 2) * 8;
 }
 
-// The walk.  row_sum(node, a, b): sum of max(a p - b q, 0), called only for a
-// sibling after a rejection with draft probabilities given.  Without those one
-// thread walks (`writer`) and reads path[] back; with them path[] is only
-// written, so a whole workgroup may walk alike and join in row_sum.
-template <typename F>
-__device__ __forceinline__ Found walk(const VerifyArgs &a, const Seq &s, Walk &w, bool writer,
+extern __shared__ uint64_t record_lds[];
+
+__device__ __forceinline__ Record record_of(int width)
+{
+    return {record_lds, (int *)(record_lds + (width + 63) / 64)};
+}
+
+// The walk, by a whole wave: one pass over the nodes, since children come
+// after their parents.  row_sum(node, a, b): sum of max(a p - b q, 0), called
+// only for a sibling after a rejection with draft probabilities given.  Waves
+// that walk alike to join in it share the record: they write the same words,
+// and `gone` is not used then.
+template <int DT, typename F>
+__device__ __forceinline__ Found walk(const VerifyArgs &a, const Seq &s, const Record &rec,
                                       F row_sum)
 {
     Found f{0, 0, 0, 1.0, 0.0, 1.0, 0.0};
+    const int lane = threadIdx.x & 63;
     double left = 1.0;
     bool pending = false;                        // the last rejection's sum is not taken yet
-    for (int i = 1; i < s.T; i++) {
-        if (w.parent[i] != f.node)
-            continue;
-        if (w.token[i] < 0)
-            continue;
-        bool good;
-        double p = w.p[i];
-        if (a.draft) {
-            if (pending) {
-                const double z = row_sum(f.node, f.a, f.b);
-                if (z > 0.0) {
-                    f.a /= z;
-                    f.b /= z;
-                } else {
-                    f.a = f.a0;
-                    f.b = f.b0;
+    for (int base = 0; base < s.T; base += 64) {
+        const int i = base + lane;
+        const bool in = i > 0 && i < s.T;
+        const int64_t at = s.n0 + (in ? i : 0);
+        int parent = a.parents ? a.parents[at] : i - 1;
+        int x = a.tokens[at];
+        const float ul = a.u[at];
+        // a child after its parent and inside the vocabulary, or never accepted
+        const bool ok = in && parent >= 0 && parent < i && x >= 0 && x < a.vocab;
+        parent = ok ? parent : -1;
+        x = ok ? x : 0;
+        const int64_t row = s.n0 + max(parent, 0);
+        const double pl = positive(prob<DT>(a.target, row * a.target_stride + x));
+        const double ql = a.draft ? prob<DT>(a.draft, row * a.draft_stride + x) : 0.0;
+        uint64_t took = 0, children = __ballot(parent == f.node);
+        while (children) {
+            const int c = __builtin_ctzll(children);
+            children &= children - 1;
+            const int token = lane_of(x, c);
+            double p = lane_of(pl, c);
+            const double q = lane_of(ql, c);
+            const double u = (double)__builtin_bit_cast(float, lane_of(__builtin_bit_cast(int, ul), c));
+            bool good;
+            if (a.draft) {
+                if (pending) {
+                    const double z = row_sum(f.node, f.a, f.b);
+                    if (z > 0.0) {
+                        f.a /= z;
+                        f.b /= z;
+                    } else {
+                        f.a = f.a0;
+                        f.b = f.b0;
+                    }
+                    pending = false;
                 }
-                pending = false;
+                good = u * q < positive(f.a * p - f.b * q);
+            } else {
+                // a sibling with the same token has taken its probability along
+                for (int k = 0; k < f.rejected; k += 64)
+                    if (__any(k + lane < f.rejected && rec.gone[k + lane] == token))
+                        p = 0.0;
+                good = p > 0.0 && u * left < p;
             }
-            good = (double)w.u[i] * w.q[i] < positive(f.a * p - f.b * w.q[i]);
-        } else {
-            // a sibling with the same token has taken its probability along
-            for (int k = 0; k < f.rejected; k++)
-                if (w.token[w.path[f.taken + k]] == w.token[i])
-                    p = 0.0;
-            good = p > 0.0 && (double)w.u[i] * left < p;
+            if (good) {
+                f.node = base + c;
+                took |= uint64_t(1) << c;
+                f.taken++;
+                f.rejected = 0;
+                f.a = f.a0 = 1.0;
+                f.b = f.b0 = 0.0;
+                left = 1.0;
+                pending = false;
+                children = __ballot(parent == f.node);
+            } else if (a.draft) {
+                f.a0 = f.a;
+                f.b0 = f.b;
+                f.b += 1.0;
+                pending = true;
+            } else {
+                if (lane == 0)
+                    rec.gone[f.rejected] = token;
+                f.rejected++;
+                left -= p;
+            }
         }
-        if (good) {
-            f.node = i;
-            if (writer)
-                w.path[f.taken] = i;
-            f.taken++;
-            f.rejected = 0;
-            f.a = f.a0 = 1.0;
-            f.b = f.b0 = 0.0;
-            left = 1.0;
-        } else if (a.draft) {
-            f.a0 = f.a;
-            f.b0 = f.b;
-            f.b += 1.0;
-            pending = true;
-        } else {
-            if (writer)
-                w.path[f.taken + f.rejected] = i;
-            f.rejected++;
-            left -= p;
-        }
+        if (lane == 0)
+            rec.took[base >> 6] = took;
     }
     return f;
 }
 
 // Weight of vocabulary entry x at node row `row`, and the fallback's.
+struct Sums {
+    double now, before;
+};
+
 template <int DT>
-__device__ __forceinline__ void weights(const VerifyArgs &a, const Walk &w, const Found &f,
-                                        int64_t row, int64_t x, double &now, double &before)
+__device__ __forceinline__ Sums weights(const VerifyArgs &a, const Record &rec, const Found &f,
+                                        int64_t row, int64_t x)
 {
     const double p = prob<DT>(a.target, row * a.target_stride + x);
     if (a.draft) {
         const double q = prob<DT>(a.draft, row * a.draft_stride + x);
-        now = positive(f.a * p - f.b * q);
-        before = positive(f.a0 * p - f.b0 * q);
-    } else {
-        now = positive(p);
-        for (int k = 0; k < f.rejected; k++)
-            if (w.token[w.path[f.taken + k]] == x)
-                now = 0.0;
-        before = 0.0;
+        return {positive(f.a * p - f.b * q), positive(f.a0 * p - f.b0 * q)};
     }
+    double now = positive(p);
+    for (int k = 0; k < f.rejected; k++)
+        if (rec.gone[k] == x)
+            now = 0.0;
+    return {now, 0.0};
 }
 
-__device__ __forceinline__ double wave_sum(double v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        v += __shfl_xor(v, m);
-    return v;
-}
-
-// The tile whose running sum passes the threshold, and the sum before it.
-struct Place {
-    int tile;
-    double before;
-};
-
-// Looks for the element in tile `place.tile` (the first 256 threads) and
-// writes the sequence's outputs.
+// One wave: a tile's sums.
 template <int DT>
-__device__ __forceinline__ void finish(const VerifyArgs &a, int b, const Seq &s, const Walk &w,
-                                       const Found &f, bool use_before, const Place &place,
-                                       double thr, double total, int *pick)
+__device__ __forceinline__ Sums tile_sums(const VerifyArgs &a, const Seq &s, const Record &rec,
+                                          const Found &f, int tile)
 {
-    __shared__ double part[4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int PER = TILE / 256;
-    double v[PER], sum = 0.0;
-    const int64_t x0 = (int64_t)place.tile * TILE + tid * PER;
-    if (tid == 0) {
-        pick[0] = 0x7fffffff;                    // first element past the threshold
-        pick[1] = -1;                            // last element of positive weight
-    }
+    const int lane = threadIdx.x & 63;
+    Sums t{0.0, 0.0};
 #pragma unroll
     for (int e = 0; e < PER; e++) {
-        double now = 0.0, before = 0.0;
-        if (s.T > 0 && tid < 256 && x0 + e < a.vocab)
-            weights<DT>(a, w, f, s.n0 + f.node, x0 + e, now, before);
-        v[e] = use_before ? before : now;
-        sum += v[e];
+        const int64_t x = (int64_t)tile * TILE + e * 64 + lane;
+        if (x < a.vocab) {
+            const Sums w = weights<DT>(a, rec, f, s.n0 + f.node, x);
+            t.now += w.now;
+            t.before += w.before;
+        }
     }
-    double run = sum;                            // inclusive over the wave's threads
+    return {wave_sum(t.now), a.draft ? wave_sum(t.before) : 0.0};
+}
+
+// One wave: from the tile sums that sums(i) gives, which of the two weights
+// counts and the tile where the running sum passes r times the total; then the
+// element in it; and the sequence's outputs.
+template <int DT, typename F>
+__device__ __forceinline__ void finish(const VerifyArgs &a, int b, const Seq &s, const Record &rec,
+                                       const Found &f, int tiles, F sums)
+{
+    const int lane = threadIdx.x & 63;
+    int next = -1;
+    if (s.T > 0) {
+        const Sums mine = lane < tiles ? sums(lane) : Sums{0.0, 0.0};   // the first 64 stay here
+        Sums t = mine;
+        for (int i = 64 + lane; i < tiles; i += 64) {
+            const Sums v = sums(i);
+            t.now += v.now;
+            t.before += v.before;
+        }
+        t.now = wave_sum(t.now);
+        t.before = wave_sum(t.before);
+        const bool use_before = !(t.now > 0.0);
+        const double total = use_before ? t.before : t.now, thr = (double)a.r[b] * total;
+        int tile = -1;                           // else the last tile of positive sum
+        double from = 0.0, before = 0.0;
+        for (int base = 0; base < tiles; base += 64) {
+            Sums v = mine;
+            if (base)
+                v = base + lane < tiles ? sums(base + lane) : Sums{0.0, 0.0};
+            const double w = use_before ? v.before : v.now;
+            const double run = scan_wave(w), prev = before + (run - w);
+            const uint64_t hit = __ballot(w > 0.0 && before + run > thr), some = __ballot(w > 0.0);
+            if (hit | some) {
+                const int k = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
+                tile = base + k;
+                from = lane_of(prev, k);
+                if (hit)
+                    break;
+            }
+            before += lane_of(run, 63);
+        }
+        if (tile >= 0) {
+            double v[PER], sum = 0.0;
+            const int64_t x0 = (int64_t)tile * TILE + lane * PER;
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(run, m);
-        if (lane >= m)
-            run += o;
-    }
-    if (tid < 256 && lane == 63)
-        part[wave] = run;
-    __syncthreads();
-    if (tid < 256 && total > 0.0) {
-        double at = place.before + (run - sum);
-        for (int k = 0; k < wave; k++)
-            at += part[k];
-        int hit = 0x7fffffff, last = -1;
+            for (int e = 0; e < PER; e++) {
+                Sums w{0.0, 0.0};
+                if (x0 + e < a.vocab)
+                    w = weights<DT>(a, rec, f, s.n0 + f.node, x0 + e);
+                v[e] = use_before ? w.before : w.now;
+                sum += v[e];
+            }
+            double at = from + (scan_wave(sum) - sum);
+            int hit = -1, last = -1;
 #pragma unroll
-        for (int e = 0; e < PER; e++) {
-            at += v[e];
-            if (v[e] > 0.0) {
-                last = (int)(x0 + e);
-                if (at > thr && hit == 0x7fffffff)
-                    hit = last;
+            for (int e = 0; e < PER; e++) {
+                at += v[e];
+                if (v[e] > 0.0) {
+                    last = e;
+                    if (at > thr && hit < 0)
+                        hit = e;
+                }
+            }
+            const uint64_t hits = __ballot(hit >= 0), some = __ballot(last >= 0);
+            if (hits) {
+                const int k = __builtin_ctzll(hits);
+                next = tile * TILE + k * PER + lane_of(hit, k);
+            } else if (some) {
+                const int k = 63 - __builtin_clzll(some);
+                next = tile * TILE + k * PER + lane_of(last, k);
             }
         }
-        if (hit != 0x7fffffff)
-            atomicMin(&pick[0], hit);
-        if (last >= 0)
-            atomicMax(&pick[1], last);
     }
-    __syncthreads();
-    const int next = pick[0] != 0x7fffffff ? pick[0] : pick[1];
-    for (int i = tid; i < a.width; i += blockDim.x) {
-        const bool in = i < f.taken;
-        a.out_nodes[(int64_t)b * a.width + i] = in ? w.path[i] : -1;
-        a.out_tokens[(int64_t)b * a.width + i] =
-            in ? w.token[w.path[i]] : (i == f.taken && s.T > 0 ? next : -1);
+    int32_t *tokens = a.out_tokens + (int64_t)b * a.width, *nodes = a.out_nodes + (int64_t)b * a.width;
+    int done = 0;
+    for (int base = 0; base < s.T; base += 64) {
+        const uint64_t took = rec.took[base >> 6];
+        if ((took >> lane) & 1) {
+            const int at = done + __builtin_popcountll(took & ((uint64_t(1) << lane) - 1));
+            nodes[at] = base + lane;
+            tokens[at] = a.tokens[s.n0 + base + lane];
+        }
+        done += __builtin_popcountll(took);
     }
-    if (tid == 0)
+    for (int i = f.taken + lane; i < a.width; i += 64) {
+        nodes[i] = -1;
+        tokens[i] = i == f.taken ? next : -1;
+    }
+    if (lane == 0)
         a.count[b] = f.taken;
 }
 
-// Running search over tile sums by one wave: lane k of a round holds tile
-// base + k.  sums(i) gives tile i's sum.
-template <typename F>
-__device__ __forceinline__ Place find_tile(int tiles, double thr, F sums)
-{
-    const int lane = threadIdx.x & 63;
-    double before = 0.0, last_before = 0.0;
-    int last = 0;                                // last tile of positive sum
-    for (int base = 0; base < tiles; base += 64) {
-        const double v = base + lane < tiles ? sums(base + lane) : 0.0;
-        double run = v;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const double o = __shfl_up(run, m);
-            if (lane >= m)
-                run += o;
-        }
-        const double prev = before + (run - v);
-        const uint64_t hit = __ballot(v > 0.0 && before + run > thr);
-        if (hit) {
-            const int k = __builtin_ctzll(hit);
-            return {base + k, __shfl(prev, k)};
-        }
-        const uint64_t some = __ballot(v > 0.0);
-        if (some) {
-            const int k = 63 - __builtin_clzll(some);
-            last = base + k;
-            last_before = __shfl(prev, k);
-        }
-        before += __shfl(run, 63);
-    }
-    return {last, last_before};
-}
-
-// Chains, and trees without draft probabilities: one workgroup per (tile,
-// sequence).
+// Chains, and trees without draft probabilities: `per` tiles a wave.
 template <int DT>
-__global__ __launch_bounds__(256) void k_verify(VerifyArgs a, int tiles, uint32_t *counters,
-                                                double *sums)
+__global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, int tiles, int per,
+                                                    uint32_t *counters, int counter_stride,
+                                                    double *sums)
 {
-    __shared__ Walk w;
-    __shared__ double red[2][4];
-    __shared__ int pick[2], last_flag;
     __shared__ Found found;
-    __shared__ Place place;
-    __shared__ double total_s;
-    __shared__ int before_s;
-    const int tile = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    __shared__ double mine[MOST_TILES * 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int b = blockIdx.y, own = WAVES * per, first = blockIdx.x * own;
+    const Record rec = record_of(a.width);
     const Seq s = seq_of(a, b);
-    load_nodes<DT>(a, s, w, tid, 256);
-    __syncthreads();
-    if (tid == 0)
-        found = walk(a, s, w, true, [](int, double, double) { return 1.0; });
+    if (wave == 0) {
+        const Found f = walk<DT>(a, s, rec, [](int, double, double) { return 1.0; });
+        if (lane == 0)
+            found = f;
+    }
     __syncthreads();
     const Found f = found;
-
-    double now = 0.0, before = 0.0;
-    if (s.T > 0)
-        for (int e = 0; e < TILE / 256; e++) {
-            const int64_t x = (int64_t)tile * TILE + e * 256 + tid;
-            if (x < a.vocab) {
-                double n, o;
-                weights<DT>(a, w, f, s.n0 + f.node, x, n, o);
-                now += n;
-                before += o;
-            }
-        }
-    now = wave_sum(now);
-    before = wave_sum(before);
-    if ((tid & 63) == 0) {
-        red[0][tid >> 6] = now;
-        red[1][tid >> 6] = before;
+    for (int i = wave; i < own; i += WAVES) {
+        Sums t{0.0, 0.0};
+        if (s.T > 0 && first + i < tiles)
+            t = tile_sums<DT>(a, s, rec, f, first + i);
+        if (lane < 2)
+            mine[2 * i + lane] = lane ? t.before : t.now;
     }
     __syncthreads();
-    double *mine = sums + (int64_t)b * tiles * 2;
-    if (tid == 0) {
-        __hip_atomic_store(mine + 2 * tile, (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(mine + 2 * tile + 1, (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint32_t done = __hip_atomic_fetch_add(counters + b, 1u, __ATOMIC_ACQ_REL,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-        last_flag = done == (uint32_t)tiles - 1;
-    }
-    __syncthreads();
-    if (!last_flag)
+    if (wave)
         return;
-    auto sum_of = [&](int use, int i) {
-        return __hip_atomic_load(mine + 2 * i + use, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    };
-    if (tid < 64) {
-        double t0 = 0.0, t1 = 0.0;
-        for (int i = tid; i < tiles; i += 64) {
-            t0 += sum_of(0, i);
-            t1 += sum_of(1, i);
-        }
-        t0 = wave_sum(t0);
-        t1 = wave_sum(t1);
-        const int use = t0 > 0.0 ? 0 : 1;
-        const double total = use ? t1 : t0;
-        const double thr = (double)a.r[b] * total;
-        const Place at = find_tile(tiles, thr, [&](int i) { return sum_of(use, i); });
-        if (tid == 0) {
-            place = at;
-            total_s = total;
-            before_s = use;
-            // zero again for the next call on this workspace
-            __hip_atomic_store(counters + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-    }
-    __syncthreads();
-    finish<DT>(a, b, s, w, f, before_s != 0, place, (double)a.r[b] * total_s, total_s, pick);
+    // The sums are exchanged into memory (device-scope atomics act there, past
+    // the dies' caches) and have come back before the count rises, so whoever
+    // sees the last count reads them whole.  A release at device scope would
+    // do as well, but it writes back and drops a die's whole L2 (32 trees: 58
+    // us instead of 35, everything else alike).
+    uint64_t *all = (uint64_t *)(sums + (int64_t)b * tiles * 2);
+    const int n = 2 * min(own, tiles - first);
+    uint64_t was = 0;
+    for (int i = lane; i < n; i += 64)
+        was |= __hip_atomic_exchange(all + 2 * first + i, __builtin_bit_cast(uint64_t, mine[i]),
+                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" : : "v"(was) : "memory");
+    uint32_t *count = counters + (int64_t)b * counter_stride;
+    uint32_t done = 0;
+    if (lane == 0)
+        done = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane_of((int)done, 0) != (int)gridDim.x - 1)
+        return;
+    finish<DT>(a, b, s, rec, f, tiles, [&](int i) {
+        const double *p = (const double *)all + 2 * i;
+        return Sums{__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                    __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+    });
+    if (lane == 0)                               // zero again for the next call
+        __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Trees with draft probabilities: one workgroup per sequence.
-constexpr int TREE_THREADS = 1024;
-
+// Trees with draft probabilities: one workgroup per sequence, its waves walk
+// alike and share the row sums.
 template <int DT>
-__global__ __launch_bounds__(TREE_THREADS) void k_verify_tree(VerifyArgs a, int tiles,
-                                                              double *sums)
+__global__ __launch_bounds__(THREADS) void k_verify_tree(VerifyArgs a, int tiles, double *sums)
 {
-    __shared__ Walk w;
-    __shared__ double red[2][TREE_THREADS / 64];
-    __shared__ int pick[2];
-    __shared__ Place place;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ double red[WAVES];
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Record rec = record_of(a.width);
     const Seq s = seq_of(a, b);
-    load_nodes<DT>(a, s, w, tid, TREE_THREADS);
-    __syncthreads();
-    auto row_sum = [&](int node, double fa, double fb) {
+    const Found f = walk<DT>(a, s, rec, [&](int node, double fa, double fb) {
         double v = 0.0;
         const int64_t row = s.n0 + node;
-        for (int64_t x = tid; x < a.vocab; x += TREE_THREADS)
+#pragma unroll 8
+        for (int64_t x = tid; x < a.vocab; x += THREADS)
             v += positive(fa * prob<DT>(a.target, row * a.target_stride + x) -
                           fb * prob<DT>(a.draft, row * a.draft_stride + x));
         v = wave_sum(v);
-        __syncthreads();
+        __syncthreads();                         // red is free
         if (lane == 0)
-            red[0][wave] = v;
+            red[wave] = v;
         __syncthreads();
         double z = 0.0;
-        for (int k = 0; k < TREE_THREADS / 64; k++)
-            z += red[0][k];
+        for (int k = 0; k < WAVES; k++)
+            z += red[k];
         return z;
-    };
-    const Found f = walk(a, s, w, tid == 0, row_sum);
-    __syncthreads();
-
+    });
     double *mine = sums + (int64_t)b * tiles * 2;
-    double t0 = 0.0, t1 = 0.0;                   // the same in every lane of a wave
-    for (int tile = wave; tile < tiles; tile += TREE_THREADS / 64) {
-        double now = 0.0, before = 0.0;
+    for (int tile = wave; tile < tiles; tile += WAVES) {
+        Sums t{0.0, 0.0};
         if (s.T > 0)
-            for (int e = 0; e < TILE / 64; e++) {
-                const int64_t x = (int64_t)tile * TILE + e * 64 + lane;
-                if (x < a.vocab) {
-                    double n, o;
-                    weights<DT>(a, w, f, s.n0 + f.node, x, n, o);
-                    now += n;
-                    before += o;
-                }
-            }
-        now = wave_sum(now);
-        before = wave_sum(before);
-        if (lane == 0) {
-            mine[2 * tile] = now;
-            mine[2 * tile + 1] = before;
-        }
-        t0 += now;
-        t1 += before;
+            t = tile_sums<DT>(a, s, rec, f, tile);
+        if (lane < 2)
+            mine[2 * tile + lane] = lane ? t.before : t.now;
     }
     __syncthreads();
-    if (lane == 0) {
-        red[0][wave] = t0;
-        red[1][wave] = t1;
-    }
-    __syncthreads();
-    t0 = t1 = 0.0;
-    for (int k = 0; k < TREE_THREADS / 64; k++) {
-        t0 += red[0][k];
-        t1 += red[1][k];
-    }
-    const int use = t0 > 0.0 ? 0 : 1;
-    const double total = use ? t1 : t0;
-    const double thr = (double)a.r[b] * total;
-    if (tid < 64) {
-        const Place at = find_tile(tiles, thr, [&](int i) { return mine[2 * i + use]; });
-        if (tid == 0)
-            place = at;
-    }
-    __syncthreads();
-    finish<DT>(a, b, s, w, f, use != 0, place, thr, total, pick);
+    if (wave == 0)
+        finish<DT>(a, b, s, rec, f, tiles, [&](int i) { return Sums{mine[2 * i], mine[2 * i + 1]}; });
 }
 
 int tiles_of(int64_t vocab) { return (int)((vocab + TILE - 1) / TILE); }
@@ -443,11 +437,20 @@ template <int DT>
 hipError_t launch_dt(const VerifyArgs &a, uint32_t *counters, double *sums, hipStream_t s)
 {
     const int tiles = tiles_of(a.vocab);
+    const size_t rec = record_bytes(a.width);
     if (a.parents && a.draft) {
-        k_verify_tree<DT><<<dim3((unsigned)a.batch), TREE_THREADS, 0, s>>>(a, tiles, sums);
-    } else {
-        k_verify<DT><<<dim3((unsigned)tiles, (unsigned)a.batch), 256, 0, s>>>(a, tiles, counters, sums);
+        k_verify_tree<DT><<<dim3((unsigned)a.batch), THREADS, rec, s>>>(a, tiles, sums);
+        return hipGetLastError();
     }
+    // one tile a wave, or up to four where that gives more workgroups than
+    // the chip holds (256 compute units, two each)
+    const int64_t groups = (int64_t)a.batch * ((tiles + WAVES - 1) / WAVES);
+    const int per = (int)std::min<int64_t>(MOST_TILES / WAVES, (groups + 511) / 512);
+    const int x = (tiles + WAVES * per - 1) / (WAVES * per);
+    // counts 256 bytes apart, closer where TQ_NOALLOC_SCRATCH_BYTES asks for it
+    const int stride = (int)std::min<int64_t>(64, TQ_NOALLOC_SCRATCH_BYTES / 4 / a.batch);
+    k_verify<DT><<<dim3((unsigned)x, (unsigned)a.batch), THREADS, rec, s>>>(a, tiles, per, counters,
+                                                                           stride, sums);
     return hipGetLastError();
 }
 

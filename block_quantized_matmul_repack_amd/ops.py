@@ -417,31 +417,52 @@ def block_dots(qtype, tiles, K, N, q, lut=None, path=PATH_GEMV, out=None):
     return out
 
 
-def _need_int32(name, what, t, n, dims=1):
-    if t.dtype != torch.int32 or t.dim() != dims or t.numel() < n:
-        raise TiledqError(f"{name}: {what} must be int32 with {dims} dimension(s) and at least "
-                          f"{n} elements, got {t.dtype} {tuple(t.shape)}")
+# The decode-step operators run once or more per layer and token, so their
+# checks are written for few Python operations: one condition per tensor,
+# details only once it has failed.
 
-
-def _check_rows(name, what, t, heads=None, D=None, dtypes=_DTYPES):
-    """t is [tokens, heads, D] on the GPU with contiguous rows of D; returns
-    (token stride, head stride)."""
-    if t.dim() != 3 or t.dtype not in dtypes or (heads is not None and t.shape[1] != heads) or \
-            (D is not None and t.shape[2] != D):
-        want = f"[tokens, {'heads' if heads is None else heads}, {'D' if D is None else D}]"
-        raise TiledqError(f"{name}: {what} must be {want} of {[str(d) for d in dtypes]}, got "
-                          f"{t.dtype} {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise TiledqError(f"{name}: {what} must have contiguous rows")
+def _refuse(name, what, want, t):
     if not t.is_cuda:
         raise TiledqError("tiledq operates on GPU tensors only")
-    return t.stride(0), t.stride(1)
+    raise TiledqError(f"{name}: {what} must be {want}, got {t.dtype} {tuple(t.shape)} with strides "
+                      f"{t.stride()} on {t.device}")
 
 
-def _same_device(name, *ts):
-    devices = {t.device for t in ts if t is not None}
-    if len(devices) > 1:
-        raise TiledqError(f"{name}: tensors on several devices: {sorted(map(str, devices))}")
+def _check_index(name, what, t, n, dev):
+    """t is a contiguous int32 vector of at least n elements on device dev."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] < n or t.get_device() != dev or \
+            not t.is_contiguous():
+        _refuse(name, what, f"contiguous int32, 1-D, >= {n} elements, on device {dev}", t)
+
+
+def _check_heads(name, what, t, shape, dtype, dev):
+    """t is `shape` of dtype on device dev with contiguous rows; returns its
+    token and head strides."""
+    ts, hs, es = t.stride()
+    if t.shape != shape or t.dtype is not dtype or (es != 1 and shape[2] > 1) or \
+            t.get_device() != dev:
+        _refuse(name, what, f"{dtype} {tuple(shape)} with contiguous rows on device {dev}", t)
+    return ts, hs
+
+
+def _heads_of(name, what, t, dtypes):
+    """Shape, strides, device of t [tokens, heads, D] on the GPU."""
+    code = dtypes.get(t.dtype)
+    dev = t.get_device()
+    if t.dim() != 3 or code is None or dev < 0:
+        _refuse(name, what, f"[tokens, heads, D] of {[str(d) for d in dtypes]}", t)
+    shape = t.shape
+    ts, hs, es = t.stride()
+    if es != 1 and shape[2] > 1:
+        _refuse(name, what, "[tokens, heads, D] with contiguous rows", t)
+    return shape, ts, hs, dev, code
+
+
+def _stream_of(dev):
+    """The current HIP stream of GPU number dev, as an int handle."""
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
@@ -452,35 +473,49 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     positions [T] (int32) * inv_freq (fp32): pairs (i, i + half), or
     neighbours if interleaved.  q_out, k_out may be q, k.  Returns both."""
     name = "tq_qk_norm_rope"
-    qs = _check_rows(name, "q", q)
-    T, Hq, D = q.shape
-    ks = _check_rows(name, "k", k, D=D, dtypes=(q.dtype,))
-    if k.shape[0] != T:
-        raise TiledqError(f"{name}: q has {T} tokens, k {k.shape[0]}")
+    qshape, q_ts, q_hs, dev, code = _heads_of(name, "q", q, _DTYPES)
+    T, Hq, D = qshape
+    dtype = q.dtype
+    if k.dim() != 3:
+        _refuse(name, "k", f"[{T}, heads, {D}]", k)
     Hk = k.shape[1]
-    _need_int32(name, "positions", positions, T)
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
-        raise TiledqError(f"{name}: inv_freq must be 1-D float32")
-    wdt = q.dtype
-    for w in (q_weight, k_weight):
+    kshape = (T, Hk, D)
+    k_ts, k_hs = _check_heads(name, "k", k, kshape, dtype, dev)
+    _check_index(name, "positions", positions, T, dev)
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or \
+            inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+        _refuse(name, "inv_freq", f"contiguous float32, 1-D, on device {dev}", inv_freq)
+    wcode = code
+    qw = kw = None
+    for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            wdt = w.dtype
-            if w.dtype not in _DTYPES or w.dim() != 1 or w.shape[0] != D:
-                raise TiledqError(f"{name}: norm weights must be [{D}] fp32, bf16 or fp16")
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TiledqError(f"{name}: q_weight and k_weight must share a type")
-    _need_cuda(positions, inv_freq, q_weight, k_weight)
-    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device) if k_out is None else k_out
-    qo = _check_rows(name, "q_out", q_out, Hq, D, dtypes=(q.dtype,))
-    ko = _check_rows(name, "k_out", k_out, Hk, D, dtypes=(q.dtype,))
-    if q_out.shape[0] != T or k_out.shape[0] != T:
-        raise TiledqError(f"{name}: outputs must have {T} tokens")
-    _same_device(name, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    check(lib().tq_qk_norm_rope(
-        _DTYPES[q.dtype], _ptr(q), *qs, Hq, _ptr(k), *ks, Hk, T, D, 2 * inv_freq.shape[0],
-        int(interleaved), _DTYPES[wdt], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions),
-        _ptr(inv_freq), _ptr(q_out), *qo, _ptr(k_out), *ko, _stream(q)), name)
+            wcode = _DTYPES.get(w.dtype)
+            if wcode is None or w.dim() != 1 or w.shape[0] != D or w.get_device() != dev or \
+                    not w.is_contiguous():
+                _refuse(name, what, f"contiguous fp32, bf16 or fp16 [{D}] on device {dev}", w)
+    if q_weight is not None:
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if q_weight is not None and q_weight.dtype is not k_weight.dtype:
+            raise TiledqError(f"{name}: q_weight and k_weight must share a type")
+        kw = k_weight.data_ptr()
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        qo_ts, qo_hs, _ = q_out.stride()
+    else:
+        qo_ts, qo_hs = _check_heads(name, "q_out", q_out, qshape, dtype, dev)
+    if k_out is None:
+        k_out = torch.empty_like(k)
+        ko_ts, ko_hs, _ = k_out.stride()
+    else:
+        ko_ts, ko_hs = _check_heads(name, "k_out", k_out, kshape, dtype, dev)
+    status = lib().tq_qk_norm_rope(
+        code, q.data_ptr(), q_ts, q_hs, Hq, k.data_ptr(), k_ts, k_hs, Hk, T, D,
+        2 * inv_freq.shape[0], 1 if interleaved else 0, wcode, qw, kw, eps, positions.data_ptr(),
+        inv_freq.data_ptr(), q_out.data_ptr(), qo_ts, qo_hs, k_out.data_ptr(), ko_ts, ko_hs,
+        _stream_of(dev))
+    if status:
+        check(status, name)
     return q_out, k_out
 
 
@@ -489,16 +524,18 @@ def cache_bytes(ctype, n_pages, page_size, kv_heads, D):
     return lib().tq_cache_bytes(ctype, n_pages, page_size, kv_heads, D)
 
 
-def _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D):
+def _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D, dev):
     """Pages of a cache, from its buffers' size."""
     page = _size_query("tq_cache_bytes", ctype, 1, page_size, kv_heads, D)
     if page == 0:
         raise TiledqError(f"{name}: no cache of type {ctype} with {kv_heads} heads of {D} and "
                           f"pages of {page_size}")
-    _need_cuda(k_cache, v_cache)
-    n = _nbytes(k_cache)
-    if n != _nbytes(v_cache) or n == 0 or n % page:
-        raise TiledqError(f"{name}: caches hold {n} and {_nbytes(v_cache)} bytes, not the same "
+    for what, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dtype is not torch.uint8 or c.get_device() != dev or not c.is_contiguous():
+            _refuse(name, what, f"contiguous uint8 on device {dev}", c)
+    n = k_cache.numel()
+    if n != v_cache.numel() or n == 0 or n % page:
+        raise TiledqError(f"{name}: caches hold {n} and {v_cache.numel()} bytes, not the same "
                           f"whole number of pages of {page}")
     return n // page
 
@@ -508,42 +545,45 @@ def cache_write(ctype, k, v, k_cache, v_cache, slots, page_size):
     page * page_size + position; one outside the cache is skipped) of a paged
     Q8_0 or Q4_0 cache (uint8 buffers of cache_bytes)."""
     name = "tq_cache_write"
-    ks = _check_rows(name, "k", k)
-    T, H, D = k.shape
-    vs = _check_rows(name, "v", v, H, D, dtypes=(k.dtype,))
-    if v.shape[0] != T:
-        raise TiledqError(f"{name}: k has {T} tokens, v {v.shape[0]}")
-    _need_int32(name, "slots", slots, T)
-    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, H, D)
-    _need_cuda(slots)
-    _same_device(name, k, v, k_cache, v_cache, slots)
-    check(lib().tq_cache_write(ctype, _DTYPES[k.dtype], _ptr(k), *ks, _ptr(v), *vs, T, H, D,
-                               _ptr(slots), _ptr(k_cache), _ptr(v_cache), n_pages, page_size,
-                               _stream(k)), name)
+    shape, k_ts, k_hs, dev, code = _heads_of(name, "k", k, _DTYPES)
+    T, H, D = shape
+    if v.dim() != 3:
+        _refuse(name, "v", f"{tuple(shape)}", v)
+    v_ts, v_hs = _check_heads(name, "v", v, shape, k.dtype, dev)
+    _check_index(name, "slots", slots, T, dev)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, H, D, dev)
+    status = lib().tq_cache_write(
+        ctype, code, k.data_ptr(), k_ts, k_hs, v.data_ptr(), v_ts, v_hs, T, H, D,
+        slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page_size,
+        _stream_of(dev))
+    if status:
+        check(status, name)
 
 
 def cache_read(ctype, k_cache, v_cache, slots, kv_heads, D, page_size, dtype=torch.float32):
     """The values of cache slots [T]: (k, v) [T, kv_heads, D] of dtype; a slot
     outside the cache reads as zeros."""
     name = "tq_cache_read"
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TiledqError(f"{name}: dtype must be float32, bfloat16 or float16")
-    if slots.dim() != 1:
-        raise TiledqError(f"{name}: slots must have one dimension")
+    dev = slots.get_device()
+    if dev < 0 or slots.dim() != 1:
+        _refuse(name, "slots", "int32, 1-D", slots)
     T = slots.shape[0]
-    _need_int32(name, "slots", slots, T)
-    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D)
-    _need_cuda(slots)
-    _same_device(name, k_cache, v_cache, slots)
-    k = torch.empty((T, kv_heads, D), dtype=dtype, device=k_cache.device)
+    _check_index(name, "slots", slots, T, dev)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D, dev)
+    k = torch.empty((T, kv_heads, D), dtype=dtype, device=slots.device)
     v = torch.empty_like(k)
-    check(lib().tq_cache_read(ctype, _DTYPES[dtype], _ptr(k_cache), _ptr(v_cache), n_pages,
-                              page_size, kv_heads, D, _ptr(slots), T, _ptr(k), _ptr(v),
-                              _stream(k_cache)), name)
+    status = lib().tq_cache_read(
+        ctype, code, k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page_size, kv_heads, D,
+        slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _stream_of(dev))
+    if status:
+        check(status, name)
     return k, v
 
 
-_ATTN_DTYPES = (torch.bfloat16, torch.float16)
+_ATTN_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
 def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_heads, page_size,
@@ -556,40 +596,45 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
     max_ctx bound the new and the cached tokens of a sequence; they default
     to all rows of q and all of the table.  scale defaults to D ** -0.5."""
     name = "tq_tree_attention"
-    qs = _check_rows(name, "q", q, dtypes=_ATTN_DTYPES)
-    T, Hq, D = q.shape
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise TiledqError(f"{name}: page_table must be int32 [batch, pages], rows contiguous")
+    shape, q_ts, q_hs, dev, code = _heads_of(name, "q", q, _ATTN_DTYPES)
+    T, Hq, D = shape
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or \
+            page_table.get_device() != dev or (page_table.shape[1] > 1 and
+                                               page_table.stride(1) != 1):
+        _refuse(name, "page_table", f"int32 [batch, pages], rows contiguous, on device {dev}",
+                page_table)
     B, width = page_table.shape
-    _need_int32(name, "ctx_lens", ctx_lens, B)
-    _need_int32(name, "starts", starts, B + 1)
-    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D)
-    _need_cuda(ctx_lens, starts)
-    if not page_table.is_cuda or (mask is not None and not mask.is_cuda):
-        raise TiledqError("tiledq operates on GPU tensors only")
+    _check_index(name, "ctx_lens", ctx_lens, B, dev)
+    _check_index(name, "starts", starts, B + 1, dev)
+    n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D, dev)
     words = stride = 0
+    mp = None
     if mask is not None:
-        if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] < T or \
-                (mask.shape[1] > 1 and mask.stride(1) != 1):
-            raise TiledqError(f"{name}: mask must be int32 [{T}, words], rows contiguous")
-        words, stride = mask.shape[1], mask.stride(0)
-    max_nodes = max(T, 1) if max_nodes is None else max_nodes
-    max_ctx = width * page_size if max_ctx is None else max_ctx
+        if mask.dim() != 2 or mask.dtype is not torch.int32 or mask.shape[0] < T or \
+                mask.get_device() != dev or (mask.shape[1] > 1 and mask.stride(1) != 1):
+            _refuse(name, "mask", f"int32 [{T}, words], rows contiguous, on device {dev}", mask)
+        words, stride, mp = mask.shape[1], mask.stride(0), mask.data_ptr()
+    if max_nodes is None:
+        max_nodes = max(T, 1)
+    if max_ctx is None:
+        max_ctx = width * page_size
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    os = _check_rows(name, "out", out, Hq, D, dtypes=(q.dtype,))
-    if out.shape[0] < T:
-        raise TiledqError(f"{name}: out has {out.shape[0]} tokens, needs {T}")
-    _same_device(name, q, k_cache, v_cache, page_table, ctx_lens, starts, mask, out)
-    st = _stream(q)
+        out = torch.empty_like(q)
+        o_ts, o_hs, _ = out.stride()
+    else:
+        if out.dim() != 3 or out.shape[0] < T:
+            _refuse(name, "out", f"[>= {T}, {Hq}, {D}]", out)
+        o_ts, o_hs = _check_heads(name, "out", out, (out.shape[0], Hq, D), q.dtype, dev)
+    st = _stream_of(dev)
     need = _size_query("tq_tree_attention_workspace_bytes", B, Hq, kv_heads, D, max_nodes, max_ctx)
-    ws = workspace(q.device, st, need) if need else None
-    check(lib().tq_tree_attention(
-        ctype, _DTYPES[q.dtype], _ptr(q), *qs, T, Hq, kv_heads, D, _ptr(k_cache), _ptr(v_cache),
-        n_pages, page_size, _ptr(page_table), page_table.stride(0), width, B, _ptr(ctx_lens),
-        _ptr(starts), _ptr(mask), stride, words, max_nodes, max_ctx,
-        D ** -0.5 if scale is None else scale, _ptr(out), *os, _ptr(ws), need, st), name)
+    ws = workspace(q.device, st, need).data_ptr() if need else None
+    status = lib().tq_tree_attention(
+        ctype, code, q.data_ptr(), q_ts, q_hs, T, Hq, kv_heads, D, k_cache.data_ptr(),
+        v_cache.data_ptr(), n_pages, page_size, page_table.data_ptr(), page_table.stride(0), width,
+        B, ctx_lens.data_ptr(), starts.data_ptr(), mp, stride, words, max_nodes, max_ctx,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), o_ts, o_hs, ws, need, st)
+    if status:
+        check(status, name)
     return out
 
 
@@ -605,40 +650,46 @@ def verify_draft(target, tokens, starts, uniforms, final_uniforms, draft=None, p
     max_nodes]: the accepted nodes, -1s).  max_nodes bounds the nodes of a
     sequence; it defaults to all of them."""
     name = "tq_verify_draft"
-    for what, t in (("target", target), ("draft", draft)):
-        if t is None:
-            continue
-        if t.dim() != 2 or t.dtype not in _DTYPES or t.dtype != target.dtype or \
-                t.shape != target.shape or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise TiledqError(f"{name}: {what} must be [nodes, vocab] fp32, bf16 or fp16 with "
-                              f"contiguous rows, got {t.dtype} {tuple(t.shape)}")
-        if not t.is_cuda:
-            raise TiledqError("tiledq operates on GPU tensors only")
+    code = _DTYPES.get(target.dtype)
+    dev = target.get_device()
+    if target.dim() != 2 or code is None or dev < 0 or \
+            (target.shape[1] > 1 and target.stride(1) != 1):
+        _refuse(name, "target", "[nodes, vocab] fp32, bf16 or fp16 with contiguous rows", target)
     N, V = target.shape
-    _need_int32(name, "tokens", tokens, N)
+    dp = parp = None
+    d_stride = 0
+    if draft is not None:
+        if draft.shape != target.shape or draft.dtype is not target.dtype or \
+                draft.get_device() != dev or (V > 1 and draft.stride(1) != 1):
+            _refuse(name, "draft", f"{target.dtype} {tuple(target.shape)} with contiguous rows on "
+                                   f"device {dev}", draft)
+        dp, d_stride = draft.data_ptr(), draft.stride(0)
+    _check_index(name, "tokens", tokens, N, dev)
     if parents is not None:
-        _need_int32(name, "parents", parents, N)
-    _need_int32(name, "starts", starts, 1)
+        _check_index(name, "parents", parents, N, dev)
+        parp = parents.data_ptr()
+    _check_index(name, "starts", starts, 1, dev)
     B = starts.shape[0] - 1
     for what, t, n in (("uniforms", uniforms, N), ("final_uniforms", final_uniforms, B)):
-        if t.dtype != torch.float32 or t.dim() != 1 or t.numel() < n:
-            raise TiledqError(f"{name}: {what} must be float32 with at least {n} elements")
-    _need_cuda(tokens, parents, starts, uniforms, final_uniforms)
-    _same_device(name, target, draft, tokens, parents, starts, uniforms, final_uniforms)
+        if t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] < n or \
+                t.get_device() != dev or not t.is_contiguous():
+            _refuse(name, what, f"contiguous float32, 1-D, >= {n} elements, on device {dev}", t)
     width = max(N, 1) if max_nodes is None else max_nodes
     if width < 1:
         raise TiledqError(f"{name}: max_nodes must be at least 1")
-    accepted = torch.empty(B, dtype=torch.int32, device=target.device)
-    out_tokens = torch.empty((B, width), dtype=torch.int32, device=target.device)
+    device = target.device
+    accepted = torch.empty(B, dtype=torch.int32, device=device)
+    out_tokens = torch.empty((B, width), dtype=torch.int32, device=device)
     nodes = torch.empty_like(out_tokens)
-    st = _stream(target)
+    st = _stream_of(dev)
     need = _size_query("tq_verify_draft_workspace_bytes", B, V)
-    ws = workspace(target.device, st, need) if need else None
-    check(lib().tq_verify_draft(
-        _DTYPES[target.dtype], _ptr(target), target.stride(0), _ptr(draft),
-        draft.stride(0) if draft is not None else 0, N, V, _ptr(tokens), _ptr(parents),
-        _ptr(starts), B, _ptr(uniforms), _ptr(final_uniforms), width, _ptr(accepted),
-        _ptr(out_tokens), _ptr(nodes), _ptr(ws), need, st), name)
+    ws = workspace(device, st, need).data_ptr() if need else None
+    status = lib().tq_verify_draft(
+        code, target.data_ptr(), target.stride(0), dp, d_stride, N, V, tokens.data_ptr(), parp,
+        starts.data_ptr(), B, uniforms.data_ptr(), final_uniforms.data_ptr(), width,
+        accepted.data_ptr(), out_tokens.data_ptr(), nodes.data_ptr(), ws, need, st)
+    if status:
+        check(status, name)
     return accepted, out_tokens, nodes
 
 
