@@ -4,7 +4,11 @@
 //
 // Both kernels only move data (about 3 bytes of traffic per bf16 element
 // stored, one pass).  A quad of lanes holds one 32-element block, 8 elements
-// per lane, as in the activation quantization.
+// per lane, as in the activation quantization, of four tokens in a row: where
+// those fill one group of four positions (a prompt's do), the values' bytes of
+// four tokens leave and enter as whole dwords, 32 bytes a lane; else one by
+// one.  8192 tokens of 8 heads of 128 in bf16: WRITE_US us written (byte by
+// byte 33), READ_US us read (24).
 #include <type_traits>
 
 #include "cache_layout.h"
@@ -88,61 +92,138 @@ struct WriteArgs {
     int heads, log_page;
 };
 
-// One unit (8 elements) per lane; blockIdx.y picks keys or values.
+// Four tokens in a row: those of one group of four positions if the slots run
+// on from the first call's first slot.
+struct Group {
+    int64_t t0;                      // first token, may lie before 0
+    int64_t slot[4];                 // -1: no such token or slot
+    bool whole;                      // slots 4n, 4n + 1, 4n + 2, 4n + 3
+};
+
+__device__ __forceinline__ Group group_at(const int32_t *slots, int64_t tokens, int64_t slots_total,
+                                          int64_t n)
+{
+    Group q;
+    q.t0 = 4 * n - (slots[0] & 3);
+    q.whole = true;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int64_t t = q.t0 + i;
+        const int64_t s = t >= 0 && t < tokens ? (int64_t)slots[t] : -1;
+        q.slot[i] = s >= 0 && s < slots_total ? s : -1;
+        q.whole = q.whole && q.slot[i] >= 0 && q.slot[i] == (q.slot[0] & ~int64_t(3)) + i;
+    }
+    return q;
+}
+
+// Which (group, head, unit of 8 elements) a lane has.
+template <int D> struct Unit {
+    int64_t group;
+    int h, uu;
+    bool live;
+    __device__ __forceinline__ Unit(int64_t tokens, int heads)
+    {
+        constexpr uint32_t UPH = D / 8;
+        const uint32_t u = blockIdx.x * (uint32_t)THREADS + threadIdx.x, per = heads * UPH;
+        const uint32_t g = u / per, rest = u - g * per;
+        group = g;
+        h = (int)(rest / UPH);
+        uu = (int)(rest % UPH);
+        live = group < (tokens + 6) / 4;
+    }
+};
+
+// blockIdx.y picks keys or values.
 template <int CT, int DT, int D>
 __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
 {
-    constexpr int UPH = D / 8;                   // units per head
     const int which = blockIdx.y;
-    const int64_t u = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    const int64_t th = u / UPH;
-    const int uu = (int)(u - th * UPH), s = uu >> 2, c = uu & 3;
-    const int64_t t = th / a.heads;
-    const int h = (int)(th - t * a.heads);
-    if (t >= a.tokens)
+    const Unit<D> u(a.tokens, a.heads);
+    if (!u.live)
         return;                                  // uniform across the quad of a block
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.slots_total)
-        return;
-    float v[8];
-    load_x8<DT>(v, a.x[which], t * a.ts[which] + h * a.hs[which] + 8 * uu);
-    uint16_t db;
-    const uint2 q = quantize_lane<CT>(v, c, db);
-
+    const int s = u.uu >> 2, c = u.uu & 3;
+    const Group q = group_at(a.slots, a.tokens, a.slots_total, u.group);
     const int P = 1 << a.log_page;
-    const int64_t page = slot >> a.log_page;
-    const int pos = (int)(slot & (P - 1));
     constexpr int TB = (int)token_code_bytes(CT, D);
-    uint8_t *chunk = a.cache[which] + (page * a.heads + h) * chunk_bytes(CT, D, P);
-    uint16_t *scales = (uint16_t *)(chunk + P * TB);
-    if (which == 0) {
-        uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
-        if constexpr (CT == TQ_Q8_0) {
-            *(uint2 *)p = q;
+    uint2 code[4];
+    uint16_t db[4];
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        if (q.slot[i] >= 0)
+            load_x8<DT>(v[i], a.x[which], (q.t0 + i) * a.ts[which] + u.h * a.hs[which] + 8 * u.uu);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (q.slot[i] < 0)
+            continue;
+        code[i] = quantize_lane<CT>(v[i], c, db[i]);
+        if (which && q.whole)
+            continue;
+        const int64_t page = q.slot[i] >> a.log_page;
+        const int pos = (int)(q.slot[i] & (P - 1));
+        uint8_t *chunk = a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+        uint16_t *scales = (uint16_t *)(chunk + P * TB);
+        if (which == 0) {
+            uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
+            if constexpr (CT == TQ_Q8_0) {
+                *(uint2 *)p = code[i];
+            } else {
+                uint32_t w = 0;
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    w |= ((code[i].x >> (4 * e)) & 15u) << k4_shift(e);
+                *(uint32_t *)p = w;
+            }
+            if (c == 0)
+                scales[pos * (D / 32) + s] = db[i];
         } else {
-            uint32_t w = 0;
+            if constexpr (CT == TQ_Q8_0) {
+                uint8_t *p = chunk + ((pos >> 2) * D + 8 * u.uu) * 4 + (pos & 3);
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                w |= ((q.x >> (4 * e)) & 15u) << k4_shift(e);
-            *(uint32_t *)p = w;
+                for (int e = 0; e < 8; e++)
+                    p[4 * e] = (uint8_t)((e < 4 ? code[i].x : code[i].y) >> (8 * (e & 3)));
+            } else {
+                uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * u.uu) * 4 + v4_byte(pos & 3);
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    p[4 * e] = (uint8_t)(code[i].x >> (8 * e));
+            }
+            if (c == 0)
+                scales[s * P + pos] = db[i];
         }
-        if (c == 0)
-            scales[pos * (D / 32) + s] = db;
-    } else {
-        if constexpr (CT == TQ_Q8_0) {
-            uint8_t *p = chunk + ((pos >> 2) * D + 8 * uu) * 4 + (pos & 3);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                p[4 * e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
-        } else {
-            uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * uu) * 4 + v4_byte(pos & 3);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                p[4 * e] = (uint8_t)(q.x >> (8 * e));
-        }
-        if (c == 0)
-            scales[s * P + pos] = db;
     }
+    if (which == 0 || !q.whole)
+        return;
+    const int64_t page = q.slot[0] >> a.log_page;
+    const int pos = (int)(q.slot[0] & (P - 1));
+    uint8_t *chunk = a.cache[1] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+    // byte b of the four tokens' dwords, in the order the layout asks for
+    auto column = [&](uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, int b) {
+        const uint32_t pick = (uint32_t)(0x0C0C0400 + 0x0101 * b);
+        const uint32_t lo = __builtin_amdgcn_perm(t1, t0, pick), hi = __builtin_amdgcn_perm(t3, t2, pick);
+        return lo | (hi << 16);
+    };
+    if constexpr (CT == TQ_Q8_0) {
+        uint4 *p = (uint4 *)(chunk + ((pos >> 2) * D + 8 * u.uu) * 4);
+        p[0] = make_uint4(column(code[0].x, code[1].x, code[2].x, code[3].x, 0),
+                          column(code[0].x, code[1].x, code[2].x, code[3].x, 1),
+                          column(code[0].x, code[1].x, code[2].x, code[3].x, 2),
+                          column(code[0].x, code[1].x, code[2].x, code[3].x, 3));
+        p[1] = make_uint4(column(code[0].y, code[1].y, code[2].y, code[3].y, 0),
+                          column(code[0].y, code[1].y, code[2].y, code[3].y, 1),
+                          column(code[0].y, code[1].y, code[2].y, code[3].y, 2),
+                          column(code[0].y, code[1].y, code[2].y, code[3].y, 3));
+    } else {
+        // tokens 0, 2, 1, 3 (v4_byte)
+        uint4 *p = (uint4 *)(chunk + ((pos >> 2) * (D / 2) + 4 * u.uu) * 4);
+        p[0] = make_uint4(column(code[0].x, code[2].x, code[1].x, code[3].x, 0),
+                          column(code[0].x, code[2].x, code[1].x, code[3].x, 1),
+                          column(code[0].x, code[2].x, code[1].x, code[3].x, 2),
+                          column(code[0].x, code[2].x, code[1].x, code[3].x, 3));
+    }
+    if (c == 0)
+        *(uint2 *)((uint16_t *)(chunk + P * TB) + s * P + pos) =
+            make_uint2(db[0] | ((uint32_t)db[1] << 16), db[2] | ((uint32_t)db[3] << 16));
 }
 
 struct ReadArgs {
@@ -157,56 +238,88 @@ struct ReadArgs {
 template <int CT, int DT, int D>
 __global__ __launch_bounds__(THREADS) void k_cache_read(ReadArgs a)
 {
-    constexpr int UPH = D / 8;
     const int which = blockIdx.y;
-    const int64_t u = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    const int64_t th = u / UPH;
-    const int uu = (int)(u - th * UPH), s = uu >> 2, c = uu & 3;
-    const int64_t t = th / a.heads;
-    const int h = (int)(th - t * a.heads);
-    if (t >= a.tokens)
+    const Unit<D> u(a.tokens, a.heads);
+    if (!u.live)
         return;
-    const int64_t slot = a.slots[t];
-    float v[8] = {};
-    if (slot >= 0 && slot < a.slots_total) {
-        const int P = 1 << a.log_page;
-        const int64_t page = slot >> a.log_page;
-        const int pos = (int)(slot & (P - 1));
-        constexpr int TB = (int)token_code_bytes(CT, D);
-        const uint8_t *chunk = a.cache[which] + (page * a.heads + h) * chunk_bytes(CT, D, P);
-        const uint16_t *scales = (const uint16_t *)(chunk + P * TB);
-        const float d =
-            f16_bits_to_f32(which == 0 ? scales[pos * (D / 32) + s] : scales[s * P + pos]);
-        int code[8];
-        if (which == 0) {
-            const uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
-            if constexpr (CT == TQ_Q8_0) {
-                const uint2 q = *(const uint2 *)p;
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    code[e] = (int)(((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 255u) - 128;
-            } else {
-                const uint32_t w = *(const uint32_t *)p;
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    code[e] = (int)((w >> k4_shift(e)) & 15u) - 8;
-            }
-        } else if constexpr (CT == TQ_Q8_0) {
-            const uint8_t *p = chunk + ((pos >> 2) * D + 8 * uu) * 4 + (pos & 3);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                code[e] = (int)p[4 * e] - 128;
-        } else {
-            const uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * uu) * 4 + v4_byte(pos & 3);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                code[e] = (int)((p[4 * (e >> 1)] >> (4 * (e & 1))) & 15u) - 8;
+    const int s = u.uu >> 2, c = u.uu & 3;
+    const Group q = group_at(a.slots, a.tokens, a.slots_total, u.group);
+    const int P = 1 << a.log_page;
+    constexpr int TB = (int)token_code_bytes(CT, D);
+    float v[4][8] = {};
+    if (which && q.whole) {
+        const int64_t page = q.slot[0] >> a.log_page;
+        const int pos = (int)(q.slot[0] & (P - 1));
+        const uint8_t *chunk = a.cache[1] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+        const uint2 sc = *(const uint2 *)((const uint16_t *)(chunk + P * TB) + s * P + pos);
+        uint32_t w[8];
+        const uint4 *p = (const uint4 *)(chunk + (pos >> 2) * (4 * TB) + u.uu * (CT == TQ_Q8_0 ? 32 : 16));
+        const uint4 x = p[0];
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        if constexpr (CT == TQ_Q8_0) {
+            const uint4 y = p[1];
+            w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
         }
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            v[e] = d * (float)code[e];           // 19 bits at most: exact in fp32
+        for (int i = 0; i < 4; i++) {
+            const float d = f16_bits_to_f32((uint16_t)((i < 2 ? sc.x : sc.y) >> (16 * (i & 1))));
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                int code;
+                if constexpr (CT == TQ_Q8_0)
+                    code = (int)((w[e] >> (8 * i)) & 255u) - 128;
+                else
+                    code = (int)((w[e >> 1] >> (8 * v4_byte(i) + 4 * (e & 1))) & 15u) - 8;
+                v[i][e] = d * (float)code;       // 19 bits at most: exact in fp32
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (q.slot[i] < 0)
+                continue;
+            const int64_t page = q.slot[i] >> a.log_page;
+            const int pos = (int)(q.slot[i] & (P - 1));
+            const uint8_t *chunk = a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+            const uint16_t *scales = (const uint16_t *)(chunk + P * TB);
+            const float d =
+                f16_bits_to_f32(which == 0 ? scales[pos * (D / 32) + s] : scales[s * P + pos]);
+            int code[8];
+            if (which == 0) {
+                const uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
+                if constexpr (CT == TQ_Q8_0) {
+                    const uint2 x = *(const uint2 *)p;
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        code[e] = (int)(((e < 4 ? x.x : x.y) >> (8 * (e & 3))) & 255u) - 128;
+                } else {
+                    const uint32_t x = *(const uint32_t *)p;
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        code[e] = (int)((x >> k4_shift(e)) & 15u) - 8;
+                }
+            } else if constexpr (CT == TQ_Q8_0) {
+                const uint8_t *p = chunk + ((pos >> 2) * D + 8 * u.uu) * 4 + (pos & 3);
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    code[e] = (int)p[4 * e] - 128;
+            } else {
+                const uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * u.uu) * 4 + v4_byte(pos & 3);
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    code[e] = (int)((p[4 * (e >> 1)] >> (4 * (e & 1))) & 15u) - 8;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                v[i][e] = d * (float)code[e];
+        }
     }
-    store_x8<DT>(a.y[which], th * D + 8 * uu, v);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int64_t t = q.t0 + i;
+        if (t >= 0 && t < a.tokens)
+            store_x8<DT>(a.y[which], (t * a.heads + u.h) * D + 8 * u.uu, v[i]);
+    }
 }
 
 template <int CT, int DT>
@@ -254,6 +367,12 @@ hipError_t by_dtype(int dtype, int D, dim3 grid, const A &a, hipStream_t s)
     return hipErrorInvalidValue;
 }
 
+// Groups of four tokens, the first of which may begin up to three before.
+int64_t blocks_of(int64_t tokens, const CacheShape &c)
+{
+    return ((tokens + 6) / 4 * c.heads * (c.D / 8) + THREADS - 1) / THREADS;
+}
+
 }  // namespace
 
 hipError_t launch_cache_write(const CacheShape &c, int dtype, const void *k, int64_t k_ts,
@@ -261,7 +380,7 @@ hipError_t launch_cache_write(const CacheShape &c, int dtype, const void *k, int
                               int64_t tokens, const int32_t *slots, void *k_cache, void *v_cache,
                               hipStream_t s)
 {
-    const int64_t blocks = (tokens * c.heads * (c.D / 8) + THREADS - 1) / THREADS;
+    const int64_t blocks = blocks_of(tokens, c);
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
     WriteArgs a{{k, v}, {k_ts, v_ts}, {k_hs, v_hs}, {(uint8_t *)k_cache, (uint8_t *)v_cache},
@@ -275,7 +394,7 @@ hipError_t launch_cache_read(const CacheShape &c, int dtype, const void *k_cache
                              const void *v_cache, const int32_t *slots, int64_t tokens, void *k,
                              void *v, hipStream_t s)
 {
-    const int64_t blocks = (tokens * c.heads * (c.D / 8) + THREADS - 1) / THREADS;
+    const int64_t blocks = blocks_of(tokens, c);
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
     ReadArgs a{{(const uint8_t *)k_cache, (const uint8_t *)v_cache}, {k, v}, slots, tokens,
