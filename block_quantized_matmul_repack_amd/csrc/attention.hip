@@ -50,7 +50,7 @@ constexpr float NO_REF = -1e30f;
 constexpr int RED = 8;                           // fragments joined at a time
 #ifndef TG
 #define TG 512
-#define MC 256
+#define MC 512
 #define OU 2048
 #endif
 constexpr int64_t GROUPS = TG, MIN_KEYS = MC, OWN_UNITS = OU;
@@ -214,7 +214,12 @@ __device__ __forceinline__ void codes8(uint32_t w, h2 &a, h2 &b)
 __device__ __forceinline__ h2 codes4(uint32_t w)
 {
     const h2 off = {(_Float16)1032.0f, (_Float16)1032.0f};
-    return as_h2((w & 0x000f000fu) | 0x64006400u) - off;
+    // one three-input operation: the mask in a vector register, the bits in a
+    // scalar one (two literals would be two operations)
+    uint32_t mask = 0x000f000fu, bits = 0x64006400u;
+    asm("" : "+v"(mask));
+    asm("" : "+s"(bits));
+    return as_h2((w & mask) | bits) - off;
 }
 
 union Frag {
@@ -382,19 +387,26 @@ __device__ __forceinline__ int64_t uniform64(int64_t x)
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
 }
 
-// Steps of the line for each workgroup (the line has less than 2048 * 2^24
-// steps, 512 workgroups share a long one); every wave computes it alike.
+// Steps for each workgroup of a line of `all` (it has less than 2048 * 2^24
+// steps, and 512 workgroups share a long one).
+__device__ __forceinline__ int span_for(int64_t all, const AttnPlan &p)
+{
+    const uint32_t groups = p.groups;
+    return (int)max(all < (int64_t(1) << 31) ? (uint32_t)((uint32_t)all + groups - 1) / groups
+                                             : (uint32_t)((all + groups - 1) / groups),
+                    1u);
+}
+
+// The same, from all sequences; every wave computes it alike.
 __device__ __forceinline__ int span_of(const AttnArgs &a, const AttnPlan &p, int keys, int lane)
 {
     int64_t sum = 0;
     for (int b = lane; b < a.batch; b += 64)
         sum += line_steps(a, p, keys, b);
-    if (a.batch > 1)
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1)
-            sum += __shfl_xor(sum, m);
-    sum = uniform64(sum);
-    return (int)max((sum + p.groups - 1) / p.groups, (int64_t)1);
+    for (int m = 1; m < 64; m <<= 1)
+        sum += __shfl_xor(sum, m);
+    return span_for(uniform64(sum), p);
 }
 
 // Sequence b that holds position `at` of the line, which becomes the position
@@ -446,20 +458,27 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
             c.left = c.steps;
         return c;
     }
-    const int span = span_of(a, p, keys, lane);
-    int64_t at = (int64_t)blockIdx.x * span;
-    int b = 0;
-    if (a.batch > 1) {
+    int span, b = 0;
+    int64_t at;
+    if (a.batch == 1) {
+        set_sequence(c, a, p, keys, 0);
+        const int64_t all = (int64_t)c.steps * c.blocks * a.kv_heads;
+        span = span_for(all, p);
+        at = (int64_t)blockIdx.x * span;
+        if (at >= all)
+            return c;
+    } else {
+        span = span_of(a, p, keys, lane);
+        at = (int64_t)blockIdx.x * span;
         b = uniform(find_sequence(a, p, keys, at, lane));
         if (b >= a.batch)
             return c;
+        set_sequence(c, a, p, keys, b);
     }
-    set_sequence(c, a, p, keys, b);
-    const int64_t all = (int64_t)c.steps * c.blocks * a.kv_heads;
-    if (at >= all)
-        return c;
-    c.q = uniform((int)(at / max(c.steps, 1)));
-    c.step = uniform((int)(at - (int64_t)c.q * c.steps));
+    // positions inside a sequence pass 31 bits only past 2^31 steps of it
+    c.q = at < (int64_t(1) << 31) ? (int)((uint32_t)at / (uint32_t)max(c.steps, 1))
+                                  : (int)(at / max(c.steps, 1));
+    c.step = (int)(at - (int64_t)c.q * c.steps);
     c.left = c.span = span;
     return c;
 }
@@ -632,8 +651,13 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
 template <int D>
 __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
 {
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    // the median with +inf: a maximum without fmaxf's extra operation on each
+    // product of the matrix cores (a NaN score shows in p, not here)
+    float inf = __builtin_inff();
+    asm("" : "+s"(inf));
+    auto larger = [&](float a, float b) { return __builtin_amdgcn_fmed3f(a, b, inf); };
+    float top = larger(larger(larger(s[0][0], s[0][1]), larger(s[0][2], s[0][3])),
+                       larger(larger(s[1][0], s[1][1]), larger(s[1][2], s[1][3])));
     top *= x.c;
     if (__any(top > x.m + RAISE)) {
         top = fmaxf(top, __shfl_xor(top, 16));
