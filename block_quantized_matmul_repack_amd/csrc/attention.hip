@@ -361,30 +361,52 @@ __device__ __forceinline__ int blocks_of(const AttnArgs &a, const AttnPlan &p, c
 }
 
 // The line of key steps runs sequence by sequence, in it (head, row block) by
-// (head, row block).  Steps of sequence b in it.
-__device__ __forceinline__ int64_t line_steps(const AttnArgs &a, const AttnPlan &p, int keys, int b)
+// (head, row block).  A lane's sequence (none past the batch), and its steps.
+struct Entry {
+    int s0, s1, ctx;
+    int64_t steps;
+};
+
+__device__ __forceinline__ Entry line_entry(const AttnArgs &a, const AttnPlan &p, int keys, int b)
 {
+    Entry e{0, 0, 0, 0};
+    if (b < a.batch) {
+        e.s0 = a.starts[b];
+        e.s1 = a.starts[b + 1];
+        e.ctx = a.ctx[b];
+    }
     Rows w;
-    w.T = 0;
-    w.L = w.ctx = 0;
-    if (b < a.batch)
-        set_lengths(w, a, a.starts[b], a.starts[b + 1], a.ctx[b]);
-    return (int64_t)steps_of(w, keys) * blocks_of(a, p, w) * a.kv_heads;
+    set_lengths(w, a, e.s0, e.s1, e.ctx);
+    e.steps = b < a.batch ? (int64_t)steps_of(w, keys) * blocks_of(a, p, w) * a.kv_heads : 0;
+    return e;
 }
 
-__device__ __forceinline__ int64_t scan_lanes(int64_t v, int lane)
+template <int CTRL, int ROWS> __device__ __forceinline__ int64_t dpp64(int64_t x)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const int64_t o = __shfl_up(v, m);
-        v += lane >= m ? o : 0;
-    }
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, true);
+    return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// Running sum over the lanes: shifts by 1, 2, 4, 8 in each row of 16, then
+// the last lane of a row added to the rows behind it.
+__device__ __forceinline__ int64_t scan_lanes(int64_t v)
+{
+    v += dpp64<0x111, 0xF>(v);
+    v += dpp64<0x112, 0xF>(v);
+    v += dpp64<0x114, 0xF>(v);
+    v += dpp64<0x118, 0xF>(v);
+    v += dpp64<0x142, 0xA>(v);
+    v += dpp64<0x143, 0xC>(v);
     return v;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t x)
+__device__ __forceinline__ int lane_of(int x, int k) { return __builtin_amdgcn_readlane(x, k); }
+
+__device__ __forceinline__ int64_t lane_of(int64_t x, int k)
 {
-    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+    return (int64_t)(((uint64_t)(uint32_t)lane_of((int)(x >> 32), k) << 32) |
+                     (uint32_t)lane_of((int)x, k));
 }
 
 // Steps for each workgroup of a line of `all` (it has less than 2048 * 2^24
@@ -397,36 +419,6 @@ __device__ __forceinline__ int span_for(int64_t all, const AttnPlan &p)
                     1u);
 }
 
-// The same, from all sequences; every wave computes it alike.
-__device__ __forceinline__ int span_of(const AttnArgs &a, const AttnPlan &p, int keys, int lane)
-{
-    int64_t sum = 0;
-    for (int b = lane; b < a.batch; b += 64)
-        sum += line_steps(a, p, keys, b);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        sum += __shfl_xor(sum, m);
-    return span_for(uniform64(sum), p);
-}
-
-// Sequence b that holds position `at` of the line, which becomes the position
-// in it; b = batch past the end.
-__device__ __forceinline__ int find_sequence(const AttnArgs &a, const AttnPlan &p, int keys,
-                                             int64_t &at, int lane)
-{
-    for (int base = 0; base < a.batch; base += 64) {
-        const int64_t n = line_steps(a, p, keys, base + lane), end = scan_lanes(n, lane);
-        const uint64_t hit = __ballot(at < end);
-        if (hit) {
-            const int k = __builtin_ctzll(hit);
-            at -= uniform64(__shfl(end - n, k));
-            return base + k;
-        }
-        at -= uniform64(__shfl(end, 63));
-    }
-    return a.batch;
-}
-
 // A workgroup's place in the line: its next steps are `step` .. of (head, row
 // block) `q` of the sequence in w, `left` steps remain.
 struct Cursor {
@@ -435,11 +427,11 @@ struct Cursor {
 };
 
 __device__ __forceinline__ void set_sequence(Cursor &c, const AttnArgs &a, const AttnPlan &p,
-                                             int keys, int b)
+                                             int keys, const Rows &w)
 {
-    c.w = rows_of(a, b);
-    c.steps = steps_of(c.w, keys);
-    c.blocks = blocks_of(a, p, c.w);
+    c.w = w;
+    c.steps = steps_of(w, keys);
+    c.blocks = blocks_of(a, p, w);
 }
 
 __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &p, int keys,
@@ -450,7 +442,7 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
     if (p.groups == 0) {
         // many heads: one workgroup for all the keys of each
         const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
-        set_sequence(c, a, p, keys, (int)b);
+        set_sequence(c, a, p, keys, rows_of(a, (int)b));
         const uint32_t q = blockIdx.x - b * per, h = q / p.row_blocks, rb = q - h * p.row_blocks;
         c.q = (int)(h * c.blocks + rb);
         c.step = 0;
@@ -458,22 +450,44 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
             c.left = c.steps;
         return c;
     }
-    int span, b = 0;
+    int span;
     int64_t at;
     if (a.batch == 1) {
-        set_sequence(c, a, p, keys, 0);
+        set_sequence(c, a, p, keys, rows_of(a, 0));
         const int64_t all = (int64_t)c.steps * c.blocks * a.kv_heads;
         span = span_for(all, p);
         at = (int64_t)blockIdx.x * span;
         if (at >= all)
             return c;
     } else {
-        span = span_of(a, p, keys, lane);
+        // by 64 sequences in the lanes; the first 64 are read once
+        const Entry e0 = line_entry(a, p, keys, lane);
+        const int64_t end0 = scan_lanes(e0.steps);
+        int64_t all = lane_of(end0, 63);
+        for (int base = 64; base < a.batch; base += 64)
+            all += lane_of(scan_lanes(line_entry(a, p, keys, base + lane).steps), 63);
+        span = span_for(all, p);
         at = (int64_t)blockIdx.x * span;
-        b = uniform(find_sequence(a, p, keys, at, lane));
-        if (b >= a.batch)
+        if (at >= all)
             return c;
-        set_sequence(c, a, p, keys, b);
+        Entry e = e0;
+        int64_t end = end0;
+        int base = 0;
+        uint64_t hit = __ballot(at < end);
+        while (!hit) {                           // found before the batch ends: at < all
+            at -= lane_of(end, 63);
+            base += 64;
+            e = line_entry(a, p, keys, base + lane);
+            end = scan_lanes(e.steps);
+            hit = __ballot(at < end);
+        }
+        const int k = __builtin_ctzll(hit);
+        at -= lane_of(end - e.steps, k);
+        Rows w;
+        w.b = base + k;
+        w.h = w.rb = 0;
+        set_lengths(w, a, lane_of(e.s0, k), lane_of(e.s1, k), lane_of(e.ctx, k));
+        set_sequence(c, a, p, keys, w);
     }
     // positions inside a sequence pass 31 bits only past 2^31 steps of it
     c.q = at < (int64_t(1) << 31) ? (int)((uint32_t)at / (uint32_t)max(c.steps, 1))
@@ -509,7 +523,7 @@ __device__ __forceinline__ bool next_work(Cursor &c, Work &k, const Launch &laun
             do {
                 if (++b >= a.batch)
                     return false;
-                set_sequence(c, a, p, keys, b);
+                set_sequence(c, a, p, keys, rows_of(a, b));
             } while (c.steps == 0);
         }
     }
@@ -703,9 +717,9 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const Launch &launch, 
         l[i] = x[i].l[0];
         f[i] = 1.0f;
     }
+    __syncthreads();                             // the fragments' region is free
     if constexpr (KG > 1) {
         const int mine = ((rg * KG + kg) * QT * 16 + col) * 2;
-        __syncthreads();
         if (g == 0)
 #pragma unroll
             for (int i = 0; i < QT; i++) {
@@ -738,44 +752,38 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const Launch &launch, 
             *q = make_float2(x[i].m, l[i]);
         }
     }
-    auto put = [&](int i, int t, f4 sum) {
-        if (!k.whole) {
-            const int ff = (rg * QT + i) * NT + t;
-            parts.sum[(slot * F + ff) * 64 + lane] = sum;
-        } else {
-            // nothing seen: zeros
-            store_frag<CT, D>(a, k.w, TILES, rg * QT + i, t, lane,
-                              l[i] == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / l[i]));
-        }
-    };
-    if constexpr (KG == 1) {
+    // The fragments pass through LDS, RED of a wave at a time, so that what
+    // is done with each is a loop: this code runs once, and a cold line of
+    // code costs more than the loop.
+    f4 *own = red + (rg * KG + kg) * (RED * 64) + lane, *group = red + rg * KG * (RED * 64) + lane;
+    constexpr int SHARE = RED / KG;
 #pragma unroll
-        for (int n = 0; n < MINE; n++)
-            put(n / NT, n % NT, x[n / NT].o[n % NT]);
-    } else {
-        constexpr int SHARE = RED / KG;
-        f4 *own = red + (rg * KG + kg) * (RED * 64) + lane;
-#pragma unroll
-        for (int f0 = 0; f0 < MINE; f0 += RED) {
-            if (f0)
-                __syncthreads();
-#pragma unroll
-            for (int n = 0; n < RED; n++)
-                if (f0 + n < MINE)
-                    own[n * 64] = x[(f0 + n) / NT].o[(f0 + n) % NT] * f[(f0 + n) / NT];
+    for (int f0 = 0; f0 < MINE; f0 += RED) {
+        if (KG > 1 && f0)
             __syncthreads();
-            // wave kg adds fragments kg * SHARE ..; their tile is known at
-            // compile time only through the loop over waves
 #pragma unroll
-            for (int n = 0; n < RED; n++) {
-                if (f0 + n >= MINE || n / SHARE != kg)
-                    continue;
-                const f4 *q = red + rg * KG * (RED * 64) + n * 64 + lane;
-                f4 sum = q[0];
+        for (int n = 0; n < RED; n++)
+            if (f0 + n < MINE)
+                own[n * 64] = x[(f0 + n) / NT].o[(f0 + n) % NT] * f[(f0 + n) / NT];
+        if (KG > 1)
+            __syncthreads();
+#pragma unroll 1
+        for (int n = kg * SHARE; n < min((kg + 1) * SHARE, MINE - f0); n++) {
+            f4 sum = group[n * 64];
 #pragma unroll
-                for (int e = 1; e < KG; e++)
-                    sum += q[e * (RED * 64)];
-                put((f0 + n) / NT, (f0 + n) % NT, sum);
+            for (int e = 1; e < KG; e++)
+                sum += group[(e * RED + n) * 64];
+            const int i = (f0 + n) / NT, t = (f0 + n) % NT;
+            if (!k.whole) {
+                parts.sum[(slot * F + (rg * QT + i) * NT + t) * 64 + lane] = sum;
+            } else {
+                float li = l[0];
+#pragma unroll
+                for (int e = 1; e < QT; e++)
+                    li = i == e ? l[e] : li;
+                // nothing seen: zeros
+                store_frag<CT, D>(a, k.w, TILES, rg * QT + i, t, lane,
+                                  li == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / li));
             }
         }
     }
@@ -912,7 +920,7 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
     using G = Geo<CT, D>;
     constexpr int KG = WAVES / RG, AUX = RG == 2 ? BUF_NT : 0;
     constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
-    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = KG > 1 ? WAVES * RED * 64 : 0;
+    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = WAVES * RED * 64;
     __shared__ h8 lds[2 * STAGE > JOIN ? 2 * STAGE : JOIN];
     __shared__ float ml[WAVES * QT * 16 * 2];
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
