@@ -775,7 +775,9 @@ __device__ __forceinline__ void finish(Query<D> (&x)[QT], const Launch &launch, 
                 sum += group[(e * RED + n) * 64];
             const int i = (f0 + n) / NT, t = (f0 + n) % NT;
             if (!k.whole) {
-                parts.sum[(slot * F + (rg * QT + i) * NT + t) * 64 + lane] = sum;
+                // rows past the tokens have no part
+                if ((k.w.rb * TILES + rg * QT + i) * 16 + col < k.w.T * a.group)
+                    parts.sum[(slot * F + (rg * QT + i) * NT + t) * 64 + lane] = sum;
             } else {
                 float li = l[0];
 #pragma unroll
@@ -1081,12 +1083,14 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
     mm = fmaxf(mm, __shfl_xor(mm, 32));
     float ll = 0.0f;
     f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int n = SHARED ? wave : 0; n < n_parts; n += SHARED ? WAVES : 1) {
-        const float2 t = mlp[slot(n) * ms];
-        const float f = __builtin_amdgcn_exp2f(t.x - mm);
-        ll += f * t.y;
-        sum += f * o[slot(n) * F * 64];
+    if ((w.rb * p.tiles + tile) * 16 + (lane & 15) < w.T * a.group) {
+#pragma unroll 8
+        for (int n = SHARED ? wave : 0; n < n_parts; n += SHARED ? WAVES : 1) {
+            const float2 t = mlp[slot(n) * ms];
+            const float f = __builtin_amdgcn_exp2f(t.x - mm);
+            ll += f * t.y;
+            sum += f * o[slot(n) * F * 64];
+        }
     }
     if constexpr (SHARED) {
         red[wave][lane] = sum;
