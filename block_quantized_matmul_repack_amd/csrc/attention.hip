@@ -10,7 +10,13 @@
 //
 // Bound: a single token's step reads every cached byte once and is bound by
 // HBM; trees multiply each dequantized key with many rows and are bound by
-// the matrix cores and the vector work around them.
+// the matrix cores.  Measured (32 query heads, 8 key heads of 128, Q8_0 unless
+// said): 64 sequences of 1600 to 16384 keys, one token: 233 us, 6.0 TB/s of
+// cache (loads alone, nothing computed: 5.9; a plain read of the bytes: 7.1);
+// one sequence of 8192 keys: 15 us, latency; 13 drafted tokens over 131000
+// keys: 84 us (steps at 5.4 TB/s, 9 us joining); 4 Q4_0 trees of up to 63
+// nodes over 20011 keys: 77 us (steps at 1.0 PFLOP/s counting the rows of
+// whole tiles; 7 us to start, 13 joining).
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
 // tile, so a cached byte serves all the query heads and tokens of its head.
@@ -25,7 +31,9 @@
 // once lane group g's tokens are 4g..4g+3 of each 16 (cache_layout.h places
 // the codes to match).  With more rows (k_attn_rows) the waves share the
 // dequantized operands of 64 keys through LDS, stored as the fragments that
-// the matrix instructions read.
+// the matrix instructions read.  Four row tiles a wave instead of two read
+// LDS half as often but leave one wave per SIMD: 112 us for the 13 tokens, 106
+// for the trees (70 and 63), so two it is.
 //
 // Rounding: the queries enter as fp16 after a scaling of each row by a power
 // of two that puts its largest element in [2^14, 2^15) (bf16 elements down to
@@ -48,12 +56,14 @@ constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -1e30f;
 constexpr int RED = 8;                           // fragments joined at a time
-#ifndef TG
-#define TG 512
-#define MC 512
-#define OU 2048
-#endif
-constexpr int64_t GROUPS = TG, MIN_KEYS = MC, OWN_UNITS = OU;
+// Workgroups that share the line of key steps: what is resident, two on each of
+// 256 compute units, one of heads wider than 128 (4 sequences, 32 tokens, 4
+// query heads a key head: 256 elements, 8192 Q8_0 keys: 65.9 us with 256 workgroups, 80.5 with 512;
+// 128 elements, 20000 Q4_0 keys: 88.0 and 77.6).  A span below MIN_KEYS keys costs more to join than it
+// saves (one token over 8192 keys: 15.6 us with 256, 14.8 with 512, 18.2 with
+// 1024).  From OWN_UNITS heads and row blocks on the chip is filled four times over
+// by a workgroup for each, and nothing is to be joined.
+constexpr int64_t GROUPS = 512, WIDE_GROUPS = 256, MIN_KEYS = 512, OWN_UNITS = 2048;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -1176,14 +1186,14 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     }
     p.row_blocks = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
     const int64_t units = batch * kv_heads * p.row_blocks;
-    // two workgroups are resident on each of the 256 compute units; a span
-    // is at least MIN_KEYS keys, and where the heads alone fill the chip
+    // a span is at least MIN_KEYS keys, and where the heads alone fill the chip
     // several times over each has a workgroup of its own
     const int keys = p.row_groups > 1 ? ROW_KEYS : STRIDE;
     const int64_t steps = units * ((max_keys + keys - 1) / keys);
     p.groups = units >= OWN_UNITS
                    ? 0
-                   : (int)std::min<int64_t>(GROUPS, std::max<int64_t>(1, steps / (MIN_KEYS / keys)));
+                   : (int)std::min<int64_t>(D <= 128 ? GROUPS : WIDE_GROUPS,
+                                            std::max<int64_t>(1, steps / (MIN_KEYS / keys)));
     return p;
 }
 
