@@ -6,9 +6,11 @@
 // stored, one pass).  A quad of lanes holds one 32-element block, 8 elements
 // per lane, as in the activation quantization, of four tokens in a row: where
 // those fill one group of four positions (a prompt's do), the values' bytes of
-// four tokens leave and enter as whole dwords, 32 bytes a lane; else one by
-// one.  8192 tokens of 8 heads of 128 in bf16: 16 us written (byte by
-// byte 33), 14 us read (24); a copy of as many bytes takes 10.6.
+// four tokens leave and enter as whole dwords, 32 bytes a lane, and the two
+// lanes that share pieces of Q8_0 keys trade tokens for whole pieces, 32 bytes
+// a lane too; else one by one.  8192 tokens of 8 heads of 128 in bf16: 13.4 us
+// written (key halves apart and loads after the slots: 16; byte by byte 33),
+// 12.1 us read (14, 24); a copy of as many bytes takes 10.6.
 #include <type_traits>
 
 #include "cache_layout.h"
@@ -133,6 +135,58 @@ template <int D> struct Unit {
     }
 };
 
+// One token's codes of a lane: element order, but for a Q4_0 key's shifts.
+template <int CT> __device__ __forceinline__ uint2 key_codes(uint2 code)
+{
+    if constexpr (CT == TQ_Q8_0)
+        return code;
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        w |= ((code.x >> (4 * e)) & 15u) << k4_shift(e);
+    return make_uint2(w, 0);
+}
+
+template <int CT, int D>
+__device__ __forceinline__ void store_key(uint8_t *chunk, int pos, int s, int c, uint2 code)
+{
+    code = key_codes<CT>(code);
+    uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
+    if constexpr (CT == TQ_Q8_0)
+        *(uint2 *)p = code;
+    else
+        *(uint32_t *)p = code.x;
+}
+
+// Q8_0 pieces of two blocks' codes.
+template <int CT, int D> constexpr bool shared_piece()
+{
+    return CT == TQ_Q8_0 && k_piece<CT, D>() == 16;
+}
+
+// Four tokens in a row of one block: the two lanes whose blocks share pieces
+// exchange tokens, and each stores two whole pieces.
+template <int CT, int D>
+__device__ __forceinline__ void store_keys(uint8_t *chunk, int pos, int s, int c,
+                                           const uint2 (&code)[4])
+{
+    if constexpr (shared_piece<CT, D>()) {
+        const bool odd = s & 1;
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const uint2 keep = odd ? code[2 + j] : code[j], give = odd ? code[j] : code[2 + j];
+            const uint2 got = make_uint2(__shfl_xor(give.x, 4), __shfl_xor(give.y, 4));
+            uint4 w = odd ? make_uint4(got.x, got.y, keep.x, keep.y)
+                          : make_uint4(keep.x, keep.y, got.x, got.y);
+            *(uint4 *)(chunk + k_offset<CT, D>(pos + 2 * odd + j, s & ~1, c)) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            store_key<CT, D>(chunk, pos + i, s, c, code[i]);
+    }
+}
+
 // blockIdx.y picks keys or values.
 template <int CT, int DT, int D>
 __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
@@ -149,31 +203,24 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
     uint16_t db[4];
     float v[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (q.slot[i] >= 0)
-            load_x8<DT>(v[i], a.x[which], (q.t0 + i) * a.ts[which] + u.h * a.hs[which] + 8 * u.uu);
+    for (int i = 0; i < 4; i++) {
+        // whatever the slot, so that the loads do not wait for it
+        const int64_t t = min(max(q.t0 + i, (int64_t)0), a.tokens - 1);
+        load_x8<DT>(v[i], a.x[which], t * a.ts[which] + u.h * a.hs[which] + 8 * u.uu);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         if (q.slot[i] < 0)
             continue;
         code[i] = quantize_lane<CT>(v[i], c, db[i]);
-        if (which && q.whole)
+        if (q.whole)
             continue;
         const int64_t page = q.slot[i] >> a.log_page;
         const int pos = (int)(q.slot[i] & (P - 1));
         uint8_t *chunk = a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
         uint16_t *scales = (uint16_t *)(chunk + P * TB);
         if (which == 0) {
-            uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
-            if constexpr (CT == TQ_Q8_0) {
-                *(uint2 *)p = code[i];
-            } else {
-                uint32_t w = 0;
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    w |= ((code[i].x >> (4 * e)) & 15u) << k4_shift(e);
-                *(uint32_t *)p = w;
-            }
+            store_key<CT, D>(chunk, pos, s, c, code[i]);
             if (c == 0)
                 scales[pos * (D / 32) + s] = db[i];
         } else {
@@ -192,11 +239,17 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
                 scales[s * P + pos] = db[i];
         }
     }
-    if (which == 0 || !q.whole)
+    if (!q.whole)
         return;
     const int64_t page = q.slot[0] >> a.log_page;
     const int pos = (int)(q.slot[0] & (P - 1));
-    uint8_t *chunk = a.cache[1] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+    uint8_t *chunk = a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+    uint16_t *scales = (uint16_t *)(chunk + P * TB);
+    if (which == 0) {
+        store_keys<CT, D>(chunk, pos, s, c, code);
+        scales[(pos + c) * (D / 32) + s] = c < 2 ? (c ? db[1] : db[0]) : (c == 2 ? db[2] : db[3]);
+        return;
+    }
     // byte b of the four tokens' dwords, in the order the layout asks for
     auto column = [&](uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, int b) {
         const uint32_t pick = (uint32_t)(0x0C0C0400 + 0x0101 * b);
@@ -222,7 +275,7 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(WriteArgs a)
                           column(code[0].x, code[2].x, code[1].x, code[3].x, 3));
     }
     if (c == 0)
-        *(uint2 *)((uint16_t *)(chunk + P * TB) + s * P + pos) =
+        *(uint2 *)(scales + s * P + pos) =
             make_uint2(db[0] | ((uint32_t)db[1] << 16), db[2] | ((uint32_t)db[3] << 16));
 }
 
@@ -233,6 +286,64 @@ struct ReadArgs {
     int64_t tokens, slots_total;
     int heads, log_page;
 };
+
+// One token's codes of a lane, as store_key left them.
+template <int CT, int D>
+__device__ __forceinline__ uint2 load_key(const uint8_t *chunk, int pos, int s, int c)
+{
+    const uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
+    if constexpr (CT == TQ_Q8_0)
+        return *(const uint2 *)p;
+    else
+        return make_uint2(*(const uint32_t *)p, 0);
+}
+
+// Four tokens in a row of one block: store_keys the other way round.
+template <int CT, int D>
+__device__ __forceinline__ void load_keys(uint2 (&code)[4], const uint8_t *chunk, int pos, int s,
+                                          int c)
+{
+    if constexpr (shared_piece<CT, D>()) {
+        const bool odd = s & 1;
+        uint4 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            w[j] = *(const uint4 *)(chunk + k_offset<CT, D>(pos + 2 * odd + j, s & ~1, c));
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const uint2 lo = make_uint2(w[j].x, w[j].y), hi = make_uint2(w[j].z, w[j].w);
+            const uint2 keep = odd ? hi : lo, give = odd ? lo : hi;
+            const uint2 got = make_uint2(__shfl_xor(give.x, 4), __shfl_xor(give.y, 4));
+            code[j] = odd ? got : keep;
+            code[2 + j] = odd ? keep : got;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            code[i] = load_key<CT, D>(chunk, pos + i, s, c);
+    }
+}
+
+// One token's value codes: 8 bytes, or nibbles in element order.
+template <int CT, int D>
+__device__ __forceinline__ uint2 load_value(const uint8_t *chunk, int pos, int uu)
+{
+    uint2 w = make_uint2(0, 0);
+    if constexpr (CT == TQ_Q8_0) {
+        const uint8_t *p = chunk + ((pos >> 2) * D + 8 * uu) * 4 + (pos & 3);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            w.x |= (uint32_t)p[4 * e] << (8 * e);
+            w.y |= (uint32_t)p[4 * (e + 4)] << (8 * e);
+        }
+    } else {
+        const uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * uu) * 4 + v4_byte(pos & 3);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            w.x |= (uint32_t)p[4 * e] << (8 * e);
+    }
+    return w;
+}
 
 // A slot outside the cache reads as zeros.
 template <int CT, int DT, int D>
@@ -274,44 +385,47 @@ __global__ __launch_bounds__(THREADS) void k_cache_read(ReadArgs a)
             }
         }
     } else {
+        // all four tokens' loads are on their way before the first is used
+        uint2 code[4];
+        uint16_t db[4];
+        if (q.whole) {
+            const int64_t page = q.slot[0] >> a.log_page;
+            const int pos = (int)(q.slot[0] & (P - 1));
+            const uint8_t *chunk = a.cache[0] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+            const int d = ((const uint16_t *)(chunk + P * TB))[(pos + c) * (D / 32) + s];
+            load_keys<CT, D>(code, chunk, pos, s, c);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                db[i] = (uint16_t)__shfl(d, (int)(threadIdx.x & 60) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                code[i] = make_uint2(0, 0);
+                db[i] = 0;
+                if (q.slot[i] < 0)
+                    continue;
+                const int64_t page = q.slot[i] >> a.log_page;
+                const int pos = (int)(q.slot[i] & (P - 1));
+                const uint8_t *chunk =
+                    a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
+                db[i] = ((const uint16_t *)(chunk +
+                                            P * TB))[which == 0 ? pos * (D / 32) + s : s * P + pos];
+                code[i] = which == 0 ? load_key<CT, D>(chunk, pos, s, c)
+                                     : load_value<CT, D>(chunk, pos, u.uu);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            if (q.slot[i] < 0)
-                continue;
-            const int64_t page = q.slot[i] >> a.log_page;
-            const int pos = (int)(q.slot[i] & (P - 1));
-            const uint8_t *chunk = a.cache[which] + (page * a.heads + u.h) * chunk_bytes(CT, D, P);
-            const uint16_t *scales = (const uint16_t *)(chunk + P * TB);
-            const float d =
-                f16_bits_to_f32(which == 0 ? scales[pos * (D / 32) + s] : scales[s * P + pos]);
-            int code[8];
-            if (which == 0) {
-                const uint8_t *p = chunk + k_offset<CT, D>(pos, s, c);
-                if constexpr (CT == TQ_Q8_0) {
-                    const uint2 x = *(const uint2 *)p;
+            const float d = f16_bits_to_f32(db[i]);
 #pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        code[e] = (int)(((e < 4 ? x.x : x.y) >> (8 * (e & 3))) & 255u) - 128;
-                } else {
-                    const uint32_t x = *(const uint32_t *)p;
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        code[e] = (int)((x >> k4_shift(e)) & 15u) - 8;
-                }
-            } else if constexpr (CT == TQ_Q8_0) {
-                const uint8_t *p = chunk + ((pos >> 2) * D + 8 * u.uu) * 4 + (pos & 3);
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    code[e] = (int)p[4 * e] - 128;
-            } else {
-                const uint8_t *p = chunk + ((pos >> 2) * (D / 2) + 4 * u.uu) * 4 + v4_byte(pos & 3);
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    code[e] = (int)((p[4 * (e >> 1)] >> (4 * (e & 1))) & 15u) - 8;
+            for (int e = 0; e < 8; e++) {
+                int x;
+                if constexpr (CT == TQ_Q8_0)
+                    x = (int)(((e < 4 ? code[i].x : code[i].y) >> (8 * (e & 3))) & 255u) - 128;
+                else
+                    x = (int)((code[i].x >> (which == 0 ? k4_shift(e) : 4 * e)) & 15u) - 8;
+                v[i][e] = d * (float)x;
             }
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                v[i][e] = d * (float)code[e];
         }
     }
 #pragma unroll
