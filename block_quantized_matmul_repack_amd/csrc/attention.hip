@@ -11,18 +11,18 @@
 // Bound: a single token's step reads every cached byte once and is bound by
 // HBM; trees multiply each dequantized key with many rows and are bound by
 // the matrix cores.  Measured (32 query heads, 8 key heads of 128, Q8_0 unless
-// said): 64 sequences of 1600 to 16384 keys, one token: 233 us, 6.0 TB/s of
+// said): 64 sequences of 1600 to 16384 keys, one token: 232 us, 6.0 TB/s of
 // cache (loads alone, nothing computed: 5.9; a plain read of the bytes: 7.1);
 // one sequence of 8192 keys: 15 us, latency; 13 drafted tokens over 131000
-// keys: 84 us (steps at 5.4 TB/s, 9 us joining); 4 Q4_0 trees of up to 63
-// nodes over 20011 keys: 77 us (steps at 1.0 PFLOP/s counting the rows of
-// whole tiles; 7 us to start, 13 joining).
+// keys: 77 us (k_attn_rows 67, of which 15 start and store; 7 joining); 4 Q4_0
+// trees of up to 63 nodes over 20011 keys: 70 us (58, and 10 joining; each
+// further key at 1.0 PFLOP/s, counting the rows of whole tiles).
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
 // tile, so a cached byte serves all the query heads and tokens of its head.
 // Key steps of all sequences and heads are laid out in one line and cut into
 // equal spans, one for each resident workgroup, so that unlike lengths cost
-// nothing; where a cut falls inside a head's keys, k_attn_combine joins the
+// little; where a cut falls inside a head's keys, k_attn_combine joins the
 // sums.  Up to 32 rows (k_attn) the four waves of a workgroup
 // hold the same rows and take every fourth group of 32 keys: keys and values
 // go from memory through registers into the matrix cores
@@ -30,7 +30,7 @@
 // lanes and keys in registers, which is the operand layout of O^T = V^T P^T
 // once lane group g's tokens are 4g..4g+3 of each 16 (cache_layout.h places
 // the codes to match).  With more rows (k_attn_rows) the waves share the
-// dequantized operands of 64 keys through LDS, stored as the fragments that
+// dequantized operands of 64 or 128 keys through LDS, stored as the fragments that
 // the matrix instructions read.  Four row tiles a wave instead of two read
 // LDS half as often but leave one wave per SIMD: 112 us for the 13 tokens, 106
 // for the trees (70 and 63), so two it is.
@@ -56,14 +56,20 @@ constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -1e30f;
 constexpr int RED = 8;                           // fragments joined at a time
-// Workgroups that share the line of key steps: what is resident, two on each of
-// 256 compute units, one of heads wider than 128 (4 sequences, 32 tokens, 4
-// query heads a key head: 256 elements, 8192 Q8_0 keys: 65.9 us with 256 workgroups, 80.5 with 512;
-// 128 elements, 20000 Q4_0 keys: 88.0 and 77.6).  A span below MIN_KEYS keys costs more to join than it
-// saves (one token over 8192 keys: 15.6 us with 256, 14.8 with 512, 18.2 with
-// 1024).  From OWN_UNITS heads and row blocks on the chip is filled four times over
-// by a workgroup for each, and nothing is to be joined.
-constexpr int64_t GROUPS = 512, WIDE_GROUPS = 256, MIN_KEYS = 512, OWN_UNITS = 2048;
+// What entering a head and row block costs, in keys, and the shortest span: one
+// below that costs more to join than it saves (one token over 8192 keys: 15.6 us
+// with 256, 14.8 with 512, 18.2 with 1024).  4 sequences of 20000 Q4_0 keys, 32
+// tokens: 77.6 us when entering was not counted, 70.2 so.
+constexpr int MIN_KEYS = 512;
+// Up to this many heads and row blocks, one for each compute unit, k_attn_rows
+// has one workgroup of eight waves there instead of two of four, and half as
+// many parts are joined: those 4 sequences then take 66.6 us, and 32 of 2000
+// Q8_0 keys and 16 tokens 42.0 instead of 50.0; but 64 of them 82.1 instead of
+// 70.2, because starts and ends have nothing to run beside.
+constexpr int FEW_UNITS = 256;
+// From OWN_UNITS on the chip is filled four times over by a workgroup for each,
+// and nothing is to be joined.
+constexpr int OWN_UNITS = 2048;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -371,15 +377,15 @@ __device__ __forceinline__ int blocks_of(const AttnArgs &a, const AttnPlan &p, c
 }
 
 // The line of key steps runs sequence by sequence, in it (head, row block) by
-// (head, row block).  A lane's sequence (none past the batch), and its steps.
+// (head, row block): a lane's sequence (none past the batch), its (head, row
+// block)s and the steps of one.
 struct Entry {
-    int s0, s1, ctx;
-    int64_t steps;
+    int s0, s1, ctx, steps, units;
 };
 
 __device__ __forceinline__ Entry line_entry(const AttnArgs &a, const AttnPlan &p, int keys, int b)
 {
-    Entry e{0, 0, 0, 0};
+    Entry e{0, 0, 0, 0, 0};
     if (b < a.batch) {
         e.s0 = a.starts[b];
         e.s1 = a.starts[b + 1];
@@ -387,7 +393,10 @@ __device__ __forceinline__ Entry line_entry(const AttnArgs &a, const AttnPlan &p
     }
     Rows w;
     set_lengths(w, a, e.s0, e.s1, e.ctx);
-    e.steps = b < a.batch ? (int64_t)steps_of(w, keys) * blocks_of(a, p, w) * a.kv_heads : 0;
+    if (b < a.batch) {
+        e.steps = steps_of(w, keys);
+        e.units = blocks_of(a, p, w) * a.kv_heads;
+    }
     return e;
 }
 
@@ -430,10 +439,11 @@ __device__ __forceinline__ int span_for(int64_t all, const AttnPlan &p)
 }
 
 // A workgroup's place in the line: its next steps are `step` .. of (head, row
-// block) `q` of the sequence in w, `left` steps remain.
+// block) `q` of the sequence in w, `left` steps remain, of which going on to
+// the next (head, row block) takes `enter`.
 struct Cursor {
     Rows w;
-    int q, steps, blocks, step, left, span;
+    int q, steps, blocks, step, left, span, enter;
 };
 
 __device__ __forceinline__ void set_sequence(Cursor &c, const AttnArgs &a, const AttnPlan &p,
@@ -448,7 +458,7 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
                                              int lane)
 {
     Cursor c;
-    c.left = 0;
+    c.left = c.enter = 0;
     if (p.groups == 0) {
         // many heads: one workgroup for all the keys of each
         const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
@@ -460,50 +470,83 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
             c.left = c.steps;
         return c;
     }
-    int span;
+    // To enter a (head, row block), with its lengths, rows, sums and outputs,
+    // takes about as long as MIN_KEYS of its keys, so the line has that many
+    // in front of each.  Where all have as many steps, each may be cut by
+    // itself for the workgroups there are for it, if no span gets longer:
+    // then none enters two.
+    c.enter = MIN_KEYS / keys;
+    auto cut_alike = [&](int steps, int64_t units) {
+        if (units > p.groups)
+            return false;
+        const uint32_t n = (uint32_t)p.groups / (uint32_t)units, cut = (steps + n - 1) / n;
+        if ((int64_t)(cut - 1) * p.groups >= (steps + c.enter) * units)
+            return false;
+        c.q = (int)(blockIdx.x / n);
+        c.step = (int)((blockIdx.x - c.q * n) * cut);
+        c.enter = 0;
+        c.span = (int)cut;
+        c.left = c.q < units ? min(c.span, steps - c.step) : 0;
+        return true;
+    };
     int64_t at;
     if (a.batch == 1) {
         set_sequence(c, a, p, keys, rows_of(a, 0));
-        const int64_t all = (int64_t)c.steps * c.blocks * a.kv_heads;
-        span = span_for(all, p);
-        at = (int64_t)blockIdx.x * span;
+        const int64_t units = (int64_t)c.blocks * a.kv_heads, all = (c.steps + c.enter) * units;
+        if (units == 0 || cut_alike(c.steps, units))
+            return c;
+        c.span = span_for(all, p);
+        at = (int64_t)blockIdx.x * c.span;
         if (at >= all)
             return c;
     } else {
         // by 64 sequences in the lanes; the first 64 are read once
-        const Entry e0 = line_entry(a, p, keys, lane);
-        const int64_t end0 = scan_lanes(e0.steps);
-        int64_t all = lane_of(end0, 63);
+        auto steps_in = [&](const Entry &e) { return (int64_t)(e.steps + c.enter) * e.units; };
+        auto sequence = [&](const Entry &e, int base, int k) {
+            Rows w;
+            w.b = base + k;
+            w.h = w.rb = 0;
+            set_lengths(w, a, lane_of(e.s0, k), lane_of(e.s1, k), lane_of(e.ctx, k));
+            set_sequence(c, a, p, keys, w);
+        };
+        Entry e = line_entry(a, p, keys, lane);
+        const int steps0 = lane_of(e.steps, 0), units0 = lane_of(e.units, 0);
+        if (units0 && a.batch <= 64 &&
+            !__any(lane < a.batch && (e.steps != steps0 || e.units != units0)) &&
+            cut_alike(steps0, (int64_t)units0 * a.batch)) {
+            if (c.left > 0) {
+                const int k = (int)((uint32_t)c.q / (uint32_t)units0);
+                c.q -= k * units0;
+                sequence(e, 0, k);
+            }
+            return c;
+        }
+        int64_t end = scan_lanes(steps_in(e)), all = lane_of(end, 63);
         for (int base = 64; base < a.batch; base += 64)
-            all += lane_of(scan_lanes(line_entry(a, p, keys, base + lane).steps), 63);
-        span = span_for(all, p);
-        at = (int64_t)blockIdx.x * span;
+            all += lane_of(scan_lanes(steps_in(line_entry(a, p, keys, base + lane))), 63);
+        c.span = span_for(all, p);
+        at = (int64_t)blockIdx.x * c.span;
         if (at >= all)
             return c;
-        Entry e = e0;
-        int64_t end = end0;
         int base = 0;
         uint64_t hit = __ballot(at < end);
         while (!hit) {                           // found before the batch ends: at < all
             at -= lane_of(end, 63);
             base += 64;
             e = line_entry(a, p, keys, base + lane);
-            end = scan_lanes(e.steps);
+            end = scan_lanes(steps_in(e));
             hit = __ballot(at < end);
         }
         const int k = __builtin_ctzll(hit);
-        at -= lane_of(end - e.steps, k);
-        Rows w;
-        w.b = base + k;
-        w.h = w.rb = 0;
-        set_lengths(w, a, lane_of(e.s0, k), lane_of(e.s1, k), lane_of(e.ctx, k));
-        set_sequence(c, a, p, keys, w);
+        at -= lane_of(end - steps_in(e), k);
+        sequence(e, base, k);
     }
     // positions inside a sequence pass 31 bits only past 2^31 steps of it
-    c.q = at < (int64_t(1) << 31) ? (int)((uint32_t)at / (uint32_t)max(c.steps, 1))
-                                  : (int)(at / max(c.steps, 1));
-    c.step = (int)(at - (int64_t)c.q * c.steps);
-    c.left = c.span = span;
+    const int each = c.steps + c.enter;
+    c.q = at < (int64_t(1) << 31) ? (int)((uint32_t)at / (uint32_t)each) : (int)(at / each);
+    const int place = (int)(at - (int64_t)c.q * each) - c.enter;
+    c.step = max(place, 0);
+    c.left = c.span + min(place, 0);
     return c;
 }
 
@@ -527,6 +570,7 @@ __device__ __forceinline__ bool next_work(Cursor &c, Work &k, const Launch &laun
         if (c.left <= 0 || p.groups == 0)
             return false;
         c.step = 0;
+        c.left -= c.enter;
         if (++c.q == c.blocks * a.kv_heads) {
             c.q = 0;
             int b = c.w.b;
@@ -917,41 +961,38 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
     }
 }
 
-// More rows: RG groups of waves with QT * 16 rows each, KG = 4 / RG waves per
-// group.  64 keys at a time lie dequantized in LDS, as the fragments of the
-// matrix instructions; each wave reads what its rows need (KG = 2: one 32-key
-// half) and meanwhile dequantizes a 16-key tile of the next 64 into a second
-// buffer, between its matrix instructions, so that one barrier a step is
-// enough; the codes after those are on their way.
-constexpr int ROW_KEYS = 16 * WAVES;
-
-template <int CT, int D, int QT, int RG>
-__global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
-    Launch launch)
+// More rows: W waves, RG groups of them with QT * 16 rows each, KG = W / RG
+// waves per group.  16 W keys at a time lie dequantized in LDS, as the fragments
+// of the matrix instructions; each wave reads its group's share of them (STEPS
+// times 32 keys) and meanwhile dequantizes a 16-key tile of the next ones into
+// a second buffer, between its matrix instructions, so that one barrier a step
+// is enough; the codes after those are on their way.
+template <int CT, int D, int QT, int RG, int W>
+__global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch launch)
 {
     using G = Geo<CT, D>;
-    constexpr int KG = WAVES / RG, AUX = RG == 2 ? BUF_NT : 0;
-    constexpr int K_FRAGS = WAVES * G::NB, V_FRAGS = WAVES / 2 * G::NT;
-    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = WAVES * RED * 64;
+    constexpr int KEYS = 16 * W, KG = W / RG, STEPS = W / 2 / KG, AUX = RG == 2 ? BUF_NT : 0;
+    constexpr int K_FRAGS = W * G::NB, V_FRAGS = W / 2 * G::NT;
+    constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = W * RED * 64;
     __shared__ h8 lds[2 * STAGE > JOIN ? 2 * STAGE : JOIN];
-    __shared__ float ml[WAVES * QT * 16 * 2];
+    __shared__ float ml[W * QT * 16 * 2];
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int rg = wave / KG, kg = wave % KG;
     const int P = 1 << launch.a.log_page;
-    Cursor cur = first_span(launch.a, launch.p, ROW_KEYS, lane0);
+    Cursor cur = first_span(launch.a, launch.p, KEYS, lane0);
     Work k;
-    for (bool first = true; next_work(cur, k, arguments(), ROW_KEYS, first); first = false) {
+    for (bool first = true; next_work(cur, k, arguments(), KEYS, first); first = false) {
         const Rows &w = k.w;
         const AttnArgs &a = arguments().a;
         const int lane = fresh(lane0), g = lane >> 4;
         const Place pl = place_of<CT, D>(a, k);
         Tile<CT, D> raw;
-        // the wave's tile of the 64 keys from kb
+        // the wave's tile of the keys from kb
         auto chunks = [&](int entry, int kb) { return chunks_at(pl, entry, kb + 16 * wave); };
         auto entry = [&](int kb) { return entry_at(pl, kb + 16 * wave); };
         bool whole_pages;
         auto keep_values = [&](int kb) {
-            if (kb + ROW_KEYS > pl.plain || !whole_pages) {
+            if (kb + KEYS > pl.plain || !whole_pages) {
                 const int key = kb + 16 * wave;
                 drop_values<CT, D>(raw, key + 4 * g, mapped(pl, entry_at(pl, key), key), w.ctx, w.L);
             }
@@ -970,7 +1011,7 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
 
         load_tile<CT, D, AUX>(raw, chunks(entry(k.begin), k.begin), (k.begin + 16 * wave) & (P - 1), P,
                          lane);
-        int en = entry(k.begin + ROW_KEYS);
+        int en = entry(k.begin + KEYS);
         whole_pages = all_mapped(pl, k.begin, lane);
         Query<D> x[QT];
 #pragma unroll
@@ -984,26 +1025,24 @@ __global__ __launch_bounds__(THREADS, D <= 128 ? 2 : 1) void k_attn_rows(
 #pragma unroll
         for (int t = 0; t < G::NT; t++)
             stage_value(lds, t);
-        load_tile<CT, D, AUX>(raw, chunks(en, k.begin + ROW_KEYS),
-                         (k.begin + ROW_KEYS + 16 * wave) & (P - 1), P, lane);
-        en = entry(k.begin + 2 * ROW_KEYS);
+        load_tile<CT, D, AUX>(raw, chunks(en, k.begin + KEYS),
+                         (k.begin + KEYS + 16 * wave) & (P - 1), P, lane);
+        en = entry(k.begin + 2 * KEYS);
         int turn = 0;
-        for (int kb = k.begin; kb < k.end; kb += ROW_KEYS, turn ^= 1) {
+        for (int kb = k.begin; kb < k.end; kb += KEYS, turn ^= 1) {
             const h8 *kf = lds + turn * STAGE, *vf = kf + K_FRAGS * 64;
             h8 *put = lds + (turn ^ 1) * STAGE;
-            const Chunks ch = chunks(en, kb + 2 * ROW_KEYS);
-            const int pos = (kb + 2 * ROW_KEYS + 16 * wave) & (P - 1);
-            en = entry(kb + 3 * ROW_KEYS);
-            keep_values(kb + ROW_KEYS);
+            const Chunks ch = chunks(en, kb + 2 * KEYS);
+            const int pos = (kb + 2 * KEYS + 16 * wave) & (P - 1);
+            en = entry(kb + 3 * KEYS);
+            keep_values(kb + KEYS);
             __syncthreads();
 #pragma unroll
-            for (int n = 0; n < 2; n++) {
-                if (KG == 2 && n != kg)
-                    continue;
-                const int kp = kb + STEP * n;
+            for (int i0 = 0; i0 < STEPS; i0++) {
+                const int n = kg * STEPS + i0, kp = kb + STEP * n;
                 if (kp >= k.end)
                     continue;                    // then nothing is to be staged either
-                const bool stage = KG == 2 || n == 0;
+                const bool stage = i0 == 0;
                 // all of a step's keys are asked for before the first product,
                 // all of its values before the softmax: the reads' latency
                 // passes behind them
@@ -1124,7 +1163,7 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
 {
     const int64_t units = (int64_t)a.batch * a.kv_heads * p.row_blocks;
     const int64_t blocks = p.groups ? p.groups : units;
-    if (!grid_fits(blocks, THREADS))
+    if (!grid_fits(blocks, 64 * p.waves))
         return hipErrorInvalidConfiguration;
     const int F = p.tiles * (D / 16);
     Parts parts{nullptr, nullptr, nullptr};
@@ -1135,11 +1174,19 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     }
     const dim3 grid((unsigned)blocks);
     constexpr int QT = rows_qt(D);
-    if (p.row_groups == 4)
-        k_attn_rows<CT, D, QT, 4><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
-    else if (p.row_groups == 2)
-        k_attn_rows<CT, D, QT, 2><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
-    else if (p.tiles == 1)
+    if (p.row_groups > 1 && p.waves == 4) {
+        if (p.row_groups == 4)
+            k_attn_rows<CT, D, QT, 4, 4><<<grid, 256, 0, s>>>(Launch{a, p, parts});
+        else
+            k_attn_rows<CT, D, QT, 2, 4><<<grid, 256, 0, s>>>(Launch{a, p, parts});
+    } else if (p.row_groups > 1) {
+        if constexpr (D <= 128) {
+            if (p.row_groups == 4)
+                k_attn_rows<CT, D, QT, 4, 8><<<grid, 512, 0, s>>>(Launch{a, p, parts});
+            else
+                k_attn_rows<CT, D, QT, 2, 8><<<grid, 512, 0, s>>>(Launch{a, p, parts});
+        }
+    } else if (p.tiles == 1)
         k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
     else if constexpr (D <= 128)
         k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
@@ -1186,14 +1233,17 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     }
     p.row_blocks = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
     const int64_t units = batch * kv_heads * p.row_blocks;
-    // a span is at least MIN_KEYS keys, and where the heads alone fill the chip
-    // several times over each has a workgroup of its own
-    const int keys = p.row_groups > 1 ? ROW_KEYS : STRIDE;
-    const int64_t steps = units * ((max_keys + keys - 1) / keys);
+    // as many workgroups as are resident: two of four waves on each of 256
+    // compute units, or one of eight; one of four where a head is wider than 128
+    // (256 elements, 4 sequences of 8192 keys, 32 tokens: 65.9 us, with two a
+    // unit in the line 80.5)
+    p.waves = p.row_groups > 1 && D <= 128 && units <= FEW_UNITS ? 8 : 4;
+    const int keys = p.waves * (p.row_groups > 1 ? 16 : STEP), least = MIN_KEYS / keys;
+    const int64_t line = units * ((max_keys + keys - 1) / keys + least);
     p.groups = units >= OWN_UNITS
                    ? 0
-                   : (int)std::min<int64_t>(D <= 128 ? GROUPS : WIDE_GROUPS,
-                                            std::max<int64_t>(1, steps / (MIN_KEYS / keys)));
+                   : (int)std::min<int64_t>(D > 128 || p.waves == 8 ? 256 : 512,
+                                            std::max<int64_t>(1, line / least));
     return p;
 }
 

@@ -423,11 +423,11 @@ struct AttnArgs {
                                      // group: query heads per key head
     float scale;
 };
-// Launch geometry, from host sizes alone: 16-row tiles per workgroup (in
-// row_groups groups of waves), row blocks of them, and how many workgroups
+// Launch geometry, from host sizes alone: waves and 16-row tiles per workgroup
+// (in row_groups groups of waves), row blocks of them, and how many workgroups
 // share the key steps (0: each head and row block has its own).
 struct AttnPlan {
-    int tiles, row_groups, row_blocks, groups;
+    int waves, tiles, row_groups, row_blocks, groups;
 };
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys);

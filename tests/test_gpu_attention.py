@@ -344,3 +344,45 @@ def test_empty(tq):
     out = tq.tree_attention(tq.Q8_0, s.q, s.kc, s.vc, s.table[:0], s.ctx[:0], s.starts[:1], 2, 16,
                             out=torch.full_like(s.q, 3.0))
     assert bool((out == 3).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("n", [18, 40])
+def test_many_short_trees(tq, kind, D, n):
+    """More heads and row blocks than compute units, with more than 32 and 64
+    rows each: the workgroups of four waves."""
+    seqs = [(i * 7 % 90, n - i % 3) for i in range(66)]
+    s = Setup(tq, kind, seqs, 8, 4, D, 16, seed=n + D)
+    masks = tree_masks(seqs, n)
+    s.check(s.run(mask=pack(masks)), masks=masks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,c,n", [(1, 3001, 1), (3, 2000, 1), (7, 1111, 6), (5, 900, 20),
+                                   (2, 2500, 45), (64, 130, 1), (65, 130, 1)])
+def test_lengths_alike(tq, kind, D, B, c, n):
+    """As many keys in every sequence: each head is cut by itself, or many
+    are in one line; bounds that are met and bounds far above."""
+    s = Setup(tq, kind, [(c, n)] * B, 6, 3, D, 32, seed=B + D)
+    s.check(s.run())
+    s.check(s.run(max_ctx=8 * c))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bounds_far_above(tq, kind):
+    """Lengths that fill a small part of the line that the bounds stand for:
+    spans shorter than what entering a head counts."""
+    s = Setup(tq, kind, [(300, 2), (0, 1), (77, 0), (1200, 9), (64, 3)], 8, 2, 128, 64, seed=9)
+    s.check(s.run(max_ctx=200000))
+    s.check(s.run(max_ctx=200000, max_nodes=64))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 1), (256, 1), (64, 20), (96, 40), (256, 20)])
+def test_workgroup_for_each_head(tq, kind, D, n):
+    """So many heads and row blocks that none is cut."""
+    seqs = [(i * 5 % 200, n - i % min(n, 3)) for i in range(130)]
+    s = Setup(tq, kind, seqs, 16, 16, D, 16, seed=n + D)
+    s.check(s.run())
