@@ -6,8 +6,11 @@
 //
 // The kernel is a read and a write of every element; statistics, products and
 // angles stay in fp32 (angles in fp64 turns) and each output is rounded once.
-// A wave owns one token and several heads: its lanes' angles are the same for
-// every head, so sines and cosines are computed once per wave and token.
+// A wave owns one token and several heads: its angles are the same for every
+// head, so each is computed once, by one lane, and passed on through LDS (each
+// lane computing the angles of its own elements, eight times as many, took
+// 44 us where this takes 40).  8192 tokens, 32 + 8 heads of 128, bf16, nothing
+// in the caches: 36.8 us, 4.6 TB/s; copies of the two tensors 35.
 #include <algorithm>
 
 #include "tq_internal.h"
@@ -17,6 +20,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
+constexpr int MAX_D = 512;
 
 // V consecutive elements from index i.
 template <int DT, int V>
@@ -79,7 +83,20 @@ __global__ __launch_bounds__(THREADS) void k_norm_rope(NormRopeArgs a, int log_l
     int o0[U], o1[U];
     bool live[U];
     float cs[U][V], sn[U][V];
+    __shared__ __align__(16) float turn[WAVES][2][MAX_D / 2];
+    float *cosines = turn[threadIdx.x >> 6][0], *sines = turn[threadIdx.x >> 6][1];
     const double pos = (double)a.pos[t] * 0.15915494309189533577;   // 1 / (2 pi)
+    for (int i = lane; i < half; i += 64) {
+        // the angle in turns, reduced to [-1/2, 1/2] before it leaves fp64
+        const double turns = pos * (double)a.freq[i];
+        float c, s;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        cosines[i] = c;
+        sines[i] = s;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
     for (int k = 0; k < U; k++) {
         const int u = li + k * lanes;
@@ -97,13 +114,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_rope(NormRopeArgs a, int log_l
         }
 #pragma unroll
         for (int e = 0; e < V; e++) {
-            cs[k][e] = 1.0f;
-            sn[k][e] = 0.0f;
-            if (live[k] && rotated) {
-                // the angle in turns, reduced to [-1/2, 1/2] before it leaves fp64
-                const double turns = pos * (double)a.freq[u * V + e];
-                sincospif((float)(2.0 * (turns - rint(turns))), &sn[k][e], &cs[k][e]);
-            }
+            cs[k][e] = live[k] && rotated ? cosines[u * V + e] : 1.0f;
+            sn[k][e] = live[k] && rotated ? sines[u * V + e] : 0.0f;
         }
     }
 
@@ -185,8 +197,9 @@ hipError_t launch_dt(const NormRopeArgs &a, hipStream_t s)
         log_lanes++;
     const int groups = 64 >> log_lanes;
     const int64_t rounds = (a.heads[0] + a.heads[1] + groups - 1) / groups;
-    // few tokens: a token's heads are spread over waves, one round each
-    int64_t parts = std::min<int64_t>(rounds, std::max<int64_t>(1, 4096 / a.tokens));
+    // few tokens: a token's heads are spread over waves, one round each; two
+    // waves of 8192 tokens' 5 rounds take 36.8 us, one 40.7, five 38.9
+    int64_t parts = std::min<int64_t>(rounds, std::max<int64_t>(1, 16384 / a.tokens));
     const int64_t blocks = (a.tokens * parts + WAVES - 1) / WAVES;
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
