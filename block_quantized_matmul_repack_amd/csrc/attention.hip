@@ -9,13 +9,14 @@
 // sums rescaled) only when some score passes it by 2^RAISE.
 //
 // Bound: a single token's step reads every cached byte once and is bound by
-// HBM; trees multiply each dequantized key with many rows and are bound by
-// the matrix cores.  Measured (32 query heads, 8 key heads of 128, Q8_0 unless
+// HBM; trees multiply each dequantized key with many rows: the vector pipe
+// (dequantization, softmax), LDS and the matrix cores are busy 46, 38 and 30 %
+// of the trees' launch.  Measured (32 query heads, 8 key heads of 128, Q8_0 unless
 // said): 64 sequences of 1600 to 16384 keys, one token: 232 us, 6.0 TB/s of
 // cache (loads alone, nothing computed: 5.9; a plain read of the bytes: 7.1);
 // one sequence of 8192 keys: 15 us, latency; 13 drafted tokens over 131000
-// keys: 77 us (k_attn_rows 67, of which 15 start and store; 7 joining); 4 Q4_0
-// trees of up to 63 nodes over 20011 keys: 70 us (58, and 10 joining; each
+// keys: 74 us (k_attn_rows 64, of which 15 start and store; 5 joining); 4 Q4_0
+// trees of up to 63 nodes over 20011 keys: 67 us (56, and 10 joining; each
 // further key at 1.0 PFLOP/s, counting the rows of whole tiles).
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
@@ -1045,13 +1046,16 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                 const bool stage = i0 == 0;
                 // all of a step's keys are asked for before the first product,
                 // all of its values before the softmax: the reads' latency
-                // passes behind them
+                // passes behind them.  The products go before the other wave's
+                // vector work on the same SIMD (4 sequences of 40000 Q4_0 keys,
+                // 32 tokens: 107.6 us, 116 without)
                 f4 s[QT][2];
                 h8 kv[2 * G::NB], vv[G::NT];
 #pragma unroll
                 for (int b = 0; b < 2 * G::NB; b++)
                     kv[b] = kf[(2 * n * G::NB + b) * 64 + lane];
                 __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int T = 0; T < 2; T++) {
 #pragma unroll
@@ -1066,6 +1070,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                             stage_key(put, b);
                     }
                 }
+                __builtin_amdgcn_s_setprio(0);
                 if (stage)
                     load_keys<CT, D, AUX>(raw, ch, pos, P, lane);
 #pragma unroll
@@ -1083,6 +1088,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
 #pragma unroll
                 for (int i = 0; i < QT; i++)
                     pr[i] = softmax_step<D>(s[i], x[i]);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int t = 0; t < G::NT; t++) {
 #pragma unroll
@@ -1091,6 +1097,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                     if (stage)
                         stage_value(put, t);
                 }
+                __builtin_amdgcn_s_setprio(0);
                 if (stage)
                     load_values<CT, D, AUX>(raw, ch, pos, P, lane);
             }
@@ -1099,16 +1106,18 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
     }
 }
 
-// Joins the parts of a head and row block, each rescaled to the largest
-// reference.  A wave adds one fragment's parts in order (the next ones' loads
-// in flight); with many parts (SHARED) the four waves of a workgroup take
-// every fourth part of one fragment, and their sums are joined through LDS.
+// Joins the parts of a head and row block, rescaled to the largest reference
+// so far.  A wave adds one fragment's parts in order, AHEAD of them and of their
+// references and sums loaded together; with many parts (SHARED) the four waves
+// of a workgroup take every fourth part of one fragment, and their sums are
+// joined through LDS.  16 parts of one token: 3.9 us; with the references read
+// before the parts 5.0.
 template <int CT, int D, bool SHARED>
 __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p, Parts parts)
 {
-    constexpr int NT = D / 16;
+    constexpr int NT = D / 16, AHEAD = 4, BY = SHARED ? WAVES : 1;
     __shared__ f4 red[WAVES][64];
-    __shared__ float redl[WAVES][64];
+    __shared__ float2 redm[WAVES][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
     const uint32_t q = blockIdx.x - b * per;
@@ -1125,30 +1134,50 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
     const float2 *mlp = parts.ml + tile * 16 + (lane & 15);
     const f4 *o = parts.sum + ff * 64 + lane;
     auto slot = [&](int n) { return (int64_t)(n ? (slot0 | 1) - 1 + 2 * n : slot0); };
-    float mm = NO_REF;
-    for (int n = lane >> 4; n < n_parts; n += 4)
-        mm = fmaxf(mm, mlp[slot(n) * ms].x);
-    mm = fmaxf(mm, __shfl_xor(mm, 16));
-    mm = fmaxf(mm, __shfl_xor(mm, 32));
-    float ll = 0.0f;
+    float mm = NO_REF, ll = 0.0f;
     f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if ((w.rb * p.tiles + tile) * 16 + (lane & 15) < w.T * a.group) {
-#pragma unroll 8
-        for (int n = SHARED ? wave : 0; n < n_parts; n += SHARED ? WAVES : 1) {
-            const float2 t = mlp[slot(n) * ms];
-            const float f = __builtin_amdgcn_exp2f(t.x - mm);
-            ll += f * t.y;
-            sum += f * o[slot(n) * F * 64];
+        for (int n0 = SHARED ? wave : 0; n0 < n_parts; n0 += AHEAD * BY) {
+            float2 t[AHEAD];
+            f4 v[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++) {
+                const int64_t at = slot(min(n0 + i * BY, n_parts - 1));
+                t[i] = mlp[at * ms];
+                v[i] = o[at * F * 64];
+            }
+            float top = mm;
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++)
+                top = n0 + i * BY < n_parts ? fmaxf(top, t[i].x) : top;
+            const float f = __builtin_amdgcn_exp2f(mm - top);
+            mm = top;
+            ll *= f;
+            sum *= f;
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++)
+                if (n0 + i * BY < n_parts) {
+                    const float fi = __builtin_amdgcn_exp2f(t[i].x - top);
+                    ll += fi * t[i].y;
+                    sum += fi * v[i];
+                }
         }
     }
     if constexpr (SHARED) {
         red[wave][lane] = sum;
-        redl[wave][lane] = ll;
+        redm[wave][lane] = make_float2(mm, ll);
         __syncthreads();
         if (wave)
             return;
-        sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-        ll = (redl[0][lane] + redl[1][lane]) + (redl[2][lane] + redl[3][lane]);
+        for (int i = 0; i < WAVES; i++)
+            mm = fmaxf(mm, redm[i][lane].x);
+        ll = 0.0f;
+        sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < WAVES; i++) {
+            const float f = __builtin_amdgcn_exp2f(redm[i][lane].x - mm);
+            ll += f * redm[i][lane].y;
+            sum += f * red[i][lane];
+        }
     }
     store_frag<CT, D>(a, w, p.tiles, tile, ff % NT, lane,
                       ll == 0.0f ? f4{0, 0, 0, 0} : sum * (1.0f / ll));
