@@ -178,15 +178,25 @@ def _out(q, N, out):
 # without clearing (calls on one stream never overlap).  A HIP graph captured
 # on a stream keeps that stream's workspace: replaying it on another stream
 # while calls run on the capture stream would share the workspace, so replay
-# it on the capture stream or keep the two apart in time.
+# it on the capture stream or keep the two apart in time.  A workspace that has
+# become too small is kept: a captured graph may still write to it.  A call
+# that is captured before a workspace large enough was there gets one of the
+# graph's own, zero-filled by every replay.
 _workspaces = {}
+_outgrown = []
 
 
 def workspace(device, stream_handle, nbytes):
     key = (device, stream_handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
+        size = max(nbytes, 1 << 16)
+        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            return torch.zeros(size, dtype=torch.uint8, device=device)
+        if ws is not None:
+            _outgrown.append(ws)
+            size = max(size, 2 * ws.numel())     # so that they stay few
+        ws = torch.zeros(size, dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws
 

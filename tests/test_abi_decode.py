@@ -227,3 +227,16 @@ def test_binding_refuses_on_the_gpu():
         with pytest.raises(tq.TiledqError):
             call()
             print("not refused:", n)
+
+
+def test_outgrown_workspaces_are_kept(monkeypatch):
+    """A captured graph may hold the address of one; none is cleared twice."""
+    from block_quantized_matmul_repack_amd import ops
+    monkeypatch.setattr(ops, "_workspaces", {})
+    monkeypatch.setattr(ops, "_outgrown", [])
+    cpu = torch.device("cpu")
+    first = ops.workspace(cpu, 1, 1 << 17)
+    assert ops.workspace(cpu, 1, 1 << 16) is first and ops.workspace(cpu, 2, 1 << 17) is not first
+    second = ops.workspace(cpu, 1, (1 << 17) + 1)
+    assert second.numel() >= 2 * first.numel() and not second.any()
+    assert ops._outgrown == [first] and ops.workspace(cpu, 1, 1 << 17) is second

@@ -113,6 +113,64 @@ def test_graph_replays_match_eager(tq):
     assert counters_zero()
 
 
+def captured(step, stream):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = step()
+    return graph, out
+
+
+def test_outgrown_workspace_stays_the_graphs(tq, monkeypatch):
+    """After a capture a longer call needs a larger workspace on the same
+    stream; replays still have theirs, and write nothing else."""
+    from block_quantized_matmul_repack_amd import ops
+    step = Step(tq)
+    want = [t.clone() for t in step()]
+    monkeypatch.setattr(ops, "_workspaces", {})
+    monkeypatch.setattr(ops, "_outgrown", [])
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.synchronize()
+    (old,) = ops._workspaces.values()
+    size = old.numel()
+    del old
+    graph, out = captured(step, stream)
+    q = torch.randn((B * N, H, D)).bfloat16().cuda()
+    with torch.cuda.stream(stream):
+        tq.tree_attention(tq.Q8_0, q, step.kc, step.vc, step.table, step.ctx, step.starts, HK, P,
+                          max_nodes=64, max_ctx=1 << 20)
+        assert max(w.numel() for w in ops._workspaces.values()) > size
+        others = [torch.full((size // 4,), 77, dtype=torch.uint8, device="cuda") for _ in range(9)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(bool((t == 77).all()) for t in others)
+
+
+def test_capture_before_there_is_a_workspace(tq, monkeypatch):
+    """The graph then fills its own; eager calls on its stream have another."""
+    from block_quantized_matmul_repack_amd import ops
+    step = Step(tq)
+    want = [t.clone() for t in step()]
+    monkeypatch.setattr(ops, "_workspaces", {})
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph, out = captured(step, stream)
+    assert not ops._workspaces
+    for _ in range(3):
+        with torch.cuda.stream(stream):
+            got = step()
+            stream.synchronize()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert counters_zero()
+
+
 def test_side_stream_matches_default(tq):
     step = Step(tq)
     want = [t.clone() for t in step()]
