@@ -15,7 +15,7 @@
 // said): 64 sequences of 1600 to 16384 keys, one token: 232 us, 6.0 TB/s of
 // cache (loads alone, nothing computed: 5.9; a plain read of the bytes: 7.1);
 // one sequence of 8192 keys: 15 us, latency; 13 drafted tokens over 131000
-// keys: 74 us (k_attn_rows 64, of which 15 start and store; 5 joining); 4 Q4_0
+// keys: 99 us in fp16, 73 in bf16 (k_attn_rows 64, of which 15 start and store; 5 joining); 4 Q4_0
 // trees of up to 63 nodes over 20011 keys: 67 us (56, and 10 joining; each
 // further key at 1.0 PFLOP/s, counting the rows of whole tiles).
 //
@@ -41,7 +41,14 @@
 // 2^-17 of that stay exact, below it they err by at most 2^-40 of the
 // largest); code * scale of a key or value rounds once to fp16 (2^-11), as do
 // the probabilities (taken times 2^BIAS against underflow: exact to 2^-11
-// down to 2^-24 of the reference).  Scores, sums and outputs are fp32.
+// down to 2^-24 of the reference).  Scores, sums and outputs are fp32.  Under a
+// bf16 output's 2^-8 that does not show; with fp16 (FINE) only the values round
+// so: a probability is two operands, itself and the rest of its rounding, and
+// keys are exact (k_attn: a second operand with the rest, k_attn_rows: the codes
+// as operands, the scales times the products in fp32).  The error is then 1.4
+// times that of rounding exact outputs to fp16, 3.6 times without, where some
+// channels of the keys are loud.  13 tokens over 131000 keys take 99 us so, 73
+// without; k_attn, bound by HBM, takes no longer.
 #include <algorithm>
 
 #include "cache_layout.h"
@@ -244,9 +251,9 @@ union Frag {
     h8 v;
 };
 
-// Block s of the lane's key: 8 elements.
+// Block s of the lane's key: the codes of 8 elements, and the scale.
 template <int CT, int D>
-__device__ __forceinline__ h8 key_frag(const Tile<CT, D> &raw, int s)
+__device__ __forceinline__ Frag key_codes(const Tile<CT, D> &raw, int s)
 {
     Frag f;
     if constexpr (CT == TQ_Q8_0) {
@@ -257,8 +264,21 @@ __device__ __forceinline__ h8 key_frag(const Tile<CT, D> &raw, int s)
         for (int i = 0; i < 4; i++)
             f.p[i] = codes4(raw.k[s] >> (4 * i));
     }
+    return f;
+}
+
+template <int CT, int D>
+__device__ __forceinline__ h2 key_scale(const Tile<CT, D> &raw, int s)
+{
     const h2 two = as_h2(raw.ks[s >> 1]);
-    const h2 dd = s & 1 ? two.yy : two.xx;
+    return s & 1 ? two.yy : two.xx;
+}
+
+template <int CT, int D>
+__device__ __forceinline__ h8 key_frag(const Tile<CT, D> &raw, int s)
+{
+    Frag f = key_codes<CT, D>(raw, s);
+    const h2 dd = key_scale<CT, D>(raw, s);
 #pragma unroll
     for (int i = 0; i < 4; i++)
         f.p[i] *= dd;
@@ -717,8 +737,8 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
 // reference, sum and outputs follow where a score passes it.  The sum is one
 // more product, with a row of ones: it then adds the rounded probabilities,
 // the same ones that weigh the values.
-template <int D>
-__device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
+template <int D, bool FINE>
+__device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x, h8 &rest)
 {
     // the median with +inf: a maximum without fmaxf's extra operation on each
     // product of the matrix cores (a NaN score shows in p, not here)
@@ -740,16 +760,24 @@ __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x)
             x.o[t] *= f;
     }
     const float ref = BIAS - x.m;
-    Frag p;
+    Frag p, r;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int T = i >> 1, e = 2 * (i & 1);
         const f2 y = {__builtin_amdgcn_exp2f(fmaf(s[T][e], x.c, ref)),
                       __builtin_amdgcn_exp2f(fmaf(s[T][e + 1], x.c, ref))};
         p.p[i] = __builtin_convertvector(y, h2);
+        if constexpr (FINE)
+            r.p[i] = __builtin_convertvector(
+                (f2{y[0] - (float)p.p[i][0], y[1] - (float)p.p[i][1]}), h2);
     }
     const _Float16 one = (_Float16)1.0f;
-    x.l = mfma(h8{one, one, one, one, one, one, one, one}, p.v, x.l);
+    const h8 ones = {one, one, one, one, one, one, one, one};
+    x.l = mfma(ones, p.v, x.l);
+    if constexpr (FINE) {
+        x.l = mfma(ones, r.v, x.l);
+        rest = r.v;
+    }
     return p.v;
 }
 
@@ -873,7 +901,7 @@ __device__ __forceinline__ bool all_mapped(const Place &c, int begin, int lane)
 }
 
 // Up to 32 rows: every wave has its own keys.
-template <int CT, int D, int QT>
+template <int CT, int D, int QT, bool FINE>
 __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_attn(
     Launch launch)
 {
@@ -907,10 +935,26 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
                     s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int b = 0; b < G::NB; b++) {
-                    const h8 kf = key_frag<CT, D>(tile, b);
+                    if constexpr (FINE) {
+                        const Frag c = key_codes<CT, D>(tile, b);
+                        const h2 dd = key_scale<CT, D>(tile, b);
+                        Frag hi, lo;
 #pragma unroll
-                    for (int i = 0; i < QT; i++)
-                        s[i][T] = mfma(kf, x[i].q[b], s[i][T]);
+                        for (int i = 0; i < 4; i++) {
+                            hi.p[i] = c.p[i] * dd;
+                            lo.p[i] = __builtin_elementwise_fma(c.p[i], dd, -hi.p[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < QT; i++) {
+                            s[i][T] = mfma(hi.v, x[i].q[b], s[i][T]);
+                            s[i][T] = mfma(lo.v, x[i].q[b], s[i][T]);
+                        }
+                    } else {
+                        const h8 kf = key_frag<CT, D>(tile, b);
+#pragma unroll
+                        for (int i = 0; i < QT; i++)
+                            s[i][T] = mfma(kf, x[i].q[b], s[i][T]);
+                    }
                 }
             };
             scores(raw[0], 0);
@@ -925,18 +969,21 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
                 drop_values<CT, D>(raw[0], kb + 4 * g, oka, w.ctx, w.L);
                 drop_values<CT, D>(raw[1], kb + 16 + 4 * g, okb, w.ctx, w.L);
             }
-            h8 pr[QT];
+            h8 pr[QT], rest[QT];
 #pragma unroll
             for (int i = 0; i < QT; i++)
-                pr[i] = softmax_step<D>(s[i], x[i]);
+                pr[i] = softmax_step<D, FINE>(s[i], x[i], rest[i]);
 #pragma unroll
             for (int t = 0; t < G::NT; t++) {
                 Frag f;
                 value_half<CT, D>(raw[0], t, f.p[0], f.p[1]);
                 value_half<CT, D>(raw[1], t, f.p[2], f.p[3]);
 #pragma unroll
-                for (int i = 0; i < QT; i++)
+                for (int i = 0; i < QT; i++) {
                     x[i].o[t] = mfma(f.v, pr[i], x[i].o[t]);
+                    if constexpr (FINE)
+                        x[i].o[t] = mfma(f.v, rest[i], x[i].o[t]);
+                }
             }
         };
 
@@ -968,7 +1015,7 @@ __global__ __launch_bounds__(THREADS, D <= 128 || CT == TQ_Q4_0 ? 2 : 1) void k_
 // times 32 keys) and meanwhile dequantizes a 16-key tile of the next ones into
 // a second buffer, between its matrix instructions, so that one barrier a step
 // is enough; the codes after those are on their way.
-template <int CT, int D, int QT, int RG, int W>
+template <int CT, int D, int QT, int RG, int W, bool FINE>
 __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch launch)
 {
     using G = Geo<CT, D>;
@@ -977,6 +1024,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
     constexpr int STAGE = (K_FRAGS + V_FRAGS) * 64, JOIN = W * RED * 64;
     __shared__ h8 lds[2 * STAGE > JOIN ? 2 * STAGE : JOIN];
     __shared__ float ml[W * QT * 16 * 2];
+    __shared__ __align__(16) float key_scales[FINE ? 2 * G::NB * KEYS : 4];
     const int lane0 = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int rg = wave / KG, kg = wave % KG;
     const int P = 1 << launch.a.log_page;
@@ -998,8 +1046,16 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                 drop_values<CT, D>(raw, key + 4 * g, mapped(pl, entry_at(pl, key), key), w.ctx, w.L);
             }
         };
-        auto stage_key = [&](h8 *buf, int b) {
-            buf[(wave * G::NB + b) * 64 + lane] = key_frag<CT, D>(raw, b);
+        auto stage_key = [&](int turn, int b) {
+            h8 *to = lds + turn * STAGE + (wave * G::NB + b) * 64 + lane;
+            if constexpr (FINE) {
+                *to = key_codes<CT, D>(raw, b).v;
+                if (g == (b & 3))
+                    key_scales[(turn * G::NB + b) * KEYS + 16 * wave + (lane & 15)] =
+                        (float)key_scale<CT, D>(raw, b)[0];
+            } else {
+                *to = key_frag<CT, D>(raw, b);
+            }
         };
         auto stage_value = [&](h8 *buf, int t) {
             union {
@@ -1022,7 +1078,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
         __syncthreads();                         // the last rows' fragments are used up
 #pragma unroll
         for (int b = 0; b < G::NB; b++)
-            stage_key(lds, b);
+            stage_key(0, b);
 #pragma unroll
         for (int t = 0; t < G::NT; t++)
             stage_value(lds, t);
@@ -1063,11 +1119,23 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                         s[i][T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int b = 0; b < G::NB; b++) {
+                        if constexpr (FINE) {
+                            const f4 d = *(const f4 *)&key_scales[(turn * G::NB + b) * KEYS +
+                                                                  STEP * n + 16 * T + 4 * g];
 #pragma unroll
-                        for (int i = 0; i < QT; i++)
-                            s[i][T] = mfma(kv[T * G::NB + b], x[i].q[b], s[i][T]);
+                            for (int i = 0; i < QT; i++) {
+                                const f4 part = mfma(kv[T * G::NB + b], x[i].q[b], f4{0, 0, 0, 0});
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    s[i][T][e] = fmaf(part[e], d[e], s[i][T][e]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < QT; i++)
+                                s[i][T] = mfma(kv[T * G::NB + b], x[i].q[b], s[i][T]);
+                        }
                         if (stage && T == b % 2)
-                            stage_key(put, b);
+                            stage_key(turn ^ 1, b);
                     }
                 }
                 __builtin_amdgcn_s_setprio(0);
@@ -1084,16 +1152,19 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attn_rows(Launch l
                     for (int i = 0; i < QT; i++)
                         mask_scores<D>(s[i], x[i], arguments().a, w, kp, oka, okb, g);
                 }
-                h8 pr[QT];
+                h8 pr[QT], rest[QT];
 #pragma unroll
                 for (int i = 0; i < QT; i++)
-                    pr[i] = softmax_step<D>(s[i], x[i]);
+                    pr[i] = softmax_step<D, FINE>(s[i], x[i], rest[i]);
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int t = 0; t < G::NT; t++) {
 #pragma unroll
-                    for (int i = 0; i < QT; i++)
+                    for (int i = 0; i < QT; i++) {
                         x[i].o[t] = mfma(vv[t], pr[i], x[i].o[t]);
+                        if constexpr (FINE)
+                            x[i].o[t] = mfma(vv[t], rest[i], x[i].o[t]);
+                    }
                     if (stage)
                         stage_value(put, t);
                 }
@@ -1187,6 +1258,30 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
 // with 256 elements a head the registers hold one.
 constexpr int rows_qt(int D) { return D <= 128 ? 2 : 1; }
 
+template <int CT, int D, bool FINE>
+void launch_steps(const Launch &args, unsigned grid, hipStream_t s)
+{
+    constexpr int QT = rows_qt(D);
+    const AttnPlan &p = args.p;
+    if (p.row_groups > 1 && p.waves == 4) {
+        if (p.row_groups == 4)
+            k_attn_rows<CT, D, QT, 4, 4, FINE><<<grid, 256, 0, s>>>(args);
+        else
+            k_attn_rows<CT, D, QT, 2, 4, FINE><<<grid, 256, 0, s>>>(args);
+    } else if (p.row_groups > 1) {
+        if constexpr (D <= 128) {
+            if (p.row_groups == 4)
+                k_attn_rows<CT, D, QT, 4, 8, FINE><<<grid, 512, 0, s>>>(args);
+            else
+                k_attn_rows<CT, D, QT, 2, 8, FINE><<<grid, 512, 0, s>>>(args);
+        }
+    } else if (p.tiles == 1) {
+        k_attn<CT, D, 1, FINE><<<grid, THREADS, 0, s>>>(args);
+    } else if constexpr (D <= 128) {
+        k_attn<CT, D, 2, FINE><<<grid, THREADS, 0, s>>>(args);
+    }
+}
+
 template <int CT, int D>
 hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStream_t s)
 {
@@ -1201,24 +1296,11 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
         parts.ml = (float2 *)(parts.sum + (size_t)2 * p.groups * F * 64);
         parts.list = (int2 *)(parts.ml + (size_t)2 * p.groups * p.tiles * 16);
     }
-    const dim3 grid((unsigned)blocks);
-    constexpr int QT = rows_qt(D);
-    if (p.row_groups > 1 && p.waves == 4) {
-        if (p.row_groups == 4)
-            k_attn_rows<CT, D, QT, 4, 4><<<grid, 256, 0, s>>>(Launch{a, p, parts});
-        else
-            k_attn_rows<CT, D, QT, 2, 4><<<grid, 256, 0, s>>>(Launch{a, p, parts});
-    } else if (p.row_groups > 1) {
-        if constexpr (D <= 128) {
-            if (p.row_groups == 4)
-                k_attn_rows<CT, D, QT, 4, 8><<<grid, 512, 0, s>>>(Launch{a, p, parts});
-            else
-                k_attn_rows<CT, D, QT, 2, 8><<<grid, 512, 0, s>>>(Launch{a, p, parts});
-        }
-    } else if (p.tiles == 1)
-        k_attn<CT, D, 1><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
-    else if constexpr (D <= 128)
-        k_attn<CT, D, 2><<<grid, THREADS, 0, s>>>(Launch{a, p, parts});
+    const Launch args{a, p, parts};
+    if (a.dtype == TQ_F16)
+        launch_steps<CT, D, true>(args, (unsigned)blocks, s);
+    else
+        launch_steps<CT, D, false>(args, (unsigned)blocks, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.groups <= 1)
         return e;

@@ -386,3 +386,24 @@ def test_workgroup_for_each_head(tq, kind, D, n):
     seqs = [(i * 5 % 200, n - i % min(n, 3)) for i in range(130)]
     s = Setup(tq, kind, seqs, 16, 16, D, 16, seed=n + D)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("seqs", [[(2000, 1)] * 3, [(1500, 6), (700, 8)], [(3000, 30)]])
+def test_fp16_keeps_its_precision(tq, kind, D, seqs):
+    """Against rounding the exact outputs to fp16: the values' rounding to fp16
+    is as large as that and independent of it, all else is exact to about
+    2^-20, so the error's norm is about sqrt(2) of the rounding's; over 1.5 it
+    is not.  Some channels of the keys are loud, so that scores are large."""
+    loud = 1.0 + 4.0 * (torch.arange(D) % 20 == 3)
+    s = Setup(tq, kind, seqs, 16, 4, D, 32, "fp16", seed=D,
+              k=lambda b, L: seeded(7 * b + D, (L, 4, D)) * loud)
+    out = s.run().cpu().double()
+    err = alone = row = 0
+    for b, (c, n) in enumerate(seqs):
+        o, _, _ = ref.attention(s.q[row:row + n].cpu(), s.k[b], s.v[b], s.see(b), D ** -0.5)
+        err += float((out[row:row + n] - o).square().sum())
+        alone += float((o.half().double() - o).square().sum())
+        row += n
+    assert err <= 1.5 ** 2 * alone, (err / alone) ** 0.5
