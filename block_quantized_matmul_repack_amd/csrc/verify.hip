@@ -51,6 +51,13 @@ template <int DT> __device__ __forceinline__ double prob(const void *p, int64_t 
 
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }
 
+// What a p - b q leaves, q a draft probability of `positive`.  A row that
+// does not count (b = 0) may hold anything, infinities too.
+__device__ __forceinline__ double residual(double a, double p, double b, double q)
+{
+    return positive(b != 0.0 ? a * p - b * q : a * p);
+}
+
 // Lane k's value, k uniform.
 __device__ __forceinline__ int lane_of(int x, int k) { return __builtin_amdgcn_readlane(x, k); }
 
@@ -147,7 +154,7 @@ __device__ __forceinline__ Found walk(const VerifyArgs &a, const Seq &s, const R
         x = ok ? x : 0;
         const int64_t row = s.n0 + max(parent, 0);
         const double pl = positive(prob<DT>(a.target, row * a.target_stride + x));
-        const double ql = a.draft ? prob<DT>(a.draft, row * a.draft_stride + x) : 0.0;
+        const double ql = a.draft ? positive(prob<DT>(a.draft, row * a.draft_stride + x)) : 0.0;
         uint64_t took = 0, children = __ballot(parent == f.node);
         while (children) {
             const int c = __builtin_ctzll(children);
@@ -169,7 +176,7 @@ __device__ __forceinline__ Found walk(const VerifyArgs &a, const Seq &s, const R
                     }
                     pending = false;
                 }
-                good = u * q < positive(f.a * p - f.b * q);
+                good = u * q < residual(f.a, p, f.b, q);
             } else {
                 // a sibling with the same token has taken its probability along
                 for (int k = 0; k < f.rejected; k += 64)
@@ -216,8 +223,11 @@ __device__ __forceinline__ Sums weights(const VerifyArgs &a, const Record &rec, 
 {
     const double p = prob<DT>(a.target, row * a.target_stride + x);
     if (a.draft) {
-        const double q = prob<DT>(a.draft, row * a.draft_stride + x);
-        return {positive(f.a * p - f.b * q), positive(f.a0 * p - f.b0 * q)};
+        // nothing was refused after this node: its draft row has no say
+        if (f.b == 0.0)
+            return {positive(f.a * p), positive(f.a0 * p)};
+        const double q = positive(prob<DT>(a.draft, row * a.draft_stride + x));
+        return {residual(f.a, p, f.b, q), residual(f.a0, p, f.b0, q)};
     }
     double now = positive(p);
     for (int k = 0; k < f.rejected; k++)
@@ -406,8 +416,8 @@ __global__ __launch_bounds__(THREADS) void k_verify_tree(VerifyArgs a, int tiles
         const int64_t row = s.n0 + node;
 #pragma unroll 8
         for (int64_t x = tid; x < a.vocab; x += THREADS)
-            v += positive(fa * prob<DT>(a.target, row * a.target_stride + x) -
-                          fb * prob<DT>(a.draft, row * a.draft_stride + x));
+            v += residual(fa, prob<DT>(a.target, row * a.target_stride + x), fb,
+                          positive(prob<DT>(a.draft, row * a.draft_stride + x)));
         v = wave_sum(v);
         __syncthreads();                         // red is free
         if (lane == 0)

@@ -540,7 +540,8 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
  * final_uniforms[b] times the sum (the last index of positive weight if none
  * does, -1 if the row has none).  Arithmetic in fp64.  A token outside the
  * vocabulary or a parent that does not come before its child is never
- * accepted; probabilities that are negative or NaN count as 0.
+ * accepted; probabilities, the draft's too, that are negative or NaN count as
+ * 0.  Draft rows of nodes without children are not used and may hold anything.
  *   dtype : of target and draft, rows of vocab at the given row strides.
  *   uniforms : device fp32 [nodes], final_uniforms [batch], in [0, 1).
  *   width : columns of the outputs, 1..1024, at least every sequence's nodes
