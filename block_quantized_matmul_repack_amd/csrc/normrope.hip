@@ -94,9 +94,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_rope(NormRopeArgs a, int log_l
         cosines[i] = c;
         sines[i] = s;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_handover();
 #pragma unroll
     for (int k = 0; k < U; k++) {
         const int u = li + k * lanes;

@@ -139,6 +139,15 @@ __device__ __forceinline__ void store_x8(void *y, int64_t i, const float (&v)[8]
     }
 }
 
+// What the lanes of a wave have stored in LDS is there for its other lanes
+// after this; nothing waits for other waves.
+__device__ __forceinline__ void wave_handover()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Max over the 4 lanes of a quad (DPP quad permutations, no LDS).
 __device__ __forceinline__ float quad_max(float v)
 {

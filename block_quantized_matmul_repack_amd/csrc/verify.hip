@@ -202,6 +202,7 @@ __device__ __forceinline__ Found walk(const VerifyArgs &a, const Seq &s, const R
             } else {
                 if (lane == 0)
                     rec.gone[f.rejected] = token;
+                wave_handover();                 // all lanes read it for the next sibling
                 f.rejected++;
                 left -= p;
             }
