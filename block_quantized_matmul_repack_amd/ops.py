@@ -6,6 +6,7 @@ Tensors must live on the GPU; outputs are allocated with torch unless given.
 """
 import ctypes
 import functools
+import threading
 
 import torch
 
@@ -175,7 +176,8 @@ def _out(q, N, out):
 
 # Zero-filled qgemv workspaces, one per (device, stream): every call leaves
 # its workspace zero-filled, so it is reused by later calls on the same stream
-# without clearing (calls on one stream never overlap).  A HIP graph captured
+# without clearing (on one stream no call's launches overlap another's, and
+# _with_workspace lets none come between them).  A HIP graph captured
 # on a stream keeps that stream's workspace: replaying it on another stream
 # while calls run on the capture stream would share the workspace, so replay
 # it on the capture stream or keep the two apart in time.  A workspace that has
@@ -201,6 +203,22 @@ def workspace(device, stream_handle, nbytes):
     return ws
 
 
+# A call may be several launches that hand something on in the workspace, and
+# threads may share a stream: each stream's calls are enqueued one at a time.
+_turns = {}
+
+
+def _with_workspace(entry, device, st, need, *args):
+    """entry(*args, workspace, its bytes, stream): its status."""
+    if not need:
+        return entry(*args, None, 0, st)
+    turn = _turns.get(st)
+    if turn is None:
+        turn = _turns.setdefault(st, threading.Lock())
+    with turn:
+        return entry(*args, workspace(device, st, need).data_ptr(), need, st)
+
+
 def qgemv(qtype, tiles, K, N, q, d, lut=None, out=None, split=True):
     """Decode product y [M, N] = W (tiles) x A (q, d), M <= 8.  split=False
     runs one workgroup per stripe (no workspace)."""
@@ -211,9 +229,8 @@ def qgemv(qtype, tiles, K, N, q, d, lut=None, out=None, split=True):
     out = _out(q, N, out)
     st = _stream(q)
     need = _size_query("tq_qgemv_workspace_bytes", qtype, K, N, M) if split else 0
-    ws = workspace(q.device, st, need) if need else None
-    check(lib().tq_qgemv(qtype, _ptr(tiles), K, N, _ptr(q), _ptr(d), M, _lut_arg(lut),
-                         _ptr(out), out.stride(0), _ptr(ws), need, st), "tq_qgemv")
+    check(_with_workspace(lib().tq_qgemv, q.device, st, need, qtype, _ptr(tiles), K, N, _ptr(q),
+                          _ptr(d), M, _lut_arg(lut), _ptr(out), out.stride(0)), "tq_qgemv")
     return out
 
 
@@ -248,10 +265,9 @@ def qgemv_x(qtype, tiles, K, N, x, lut=None, out=None, split=True):
     out = _out(x, N, out)
     st = _stream(x)
     need = _size_query("tq_qgemv_workspace_bytes", qtype, K, N, M) if split else 0
-    ws = workspace(x.device, st, need) if need else None
-    check(lib().tq_qgemv_x(qtype, _ptr(tiles), K, N, _DTYPES[x.dtype], _ptr(x), x.stride(0), M,
-                           _lut_arg(lut), _ptr(out), out.stride(0), _ptr(ws), need, st),
-          "tq_qgemv_x")
+    check(_with_workspace(lib().tq_qgemv_x, x.device, st, need, qtype, _ptr(tiles), K, N,
+                          _DTYPES[x.dtype], _ptr(x), x.stride(0), M, _lut_arg(lut), _ptr(out),
+                          out.stride(0)), "tq_qgemv_x")
     return out
 
 
@@ -283,9 +299,8 @@ def matmul(qtype, tiles, K, N, q, d, lut=None, out=None):
     out = _out(q, N, out)
     st = _stream(q)
     need = _size_query("tq_matmul_workspace_bytes", qtype, K, N, M)
-    ws = workspace(q.device, st, need) if need else None
-    check(lib().tq_matmul(qtype, _ptr(tiles), K, N, _ptr(q), _ptr(d), M, _lut_arg(lut),
-                          _ptr(out), out.stride(0), _ptr(ws), need, st), "tq_matmul")
+    check(_with_workspace(lib().tq_matmul, q.device, st, need, qtype, _ptr(tiles), K, N, _ptr(q),
+                          _ptr(d), M, _lut_arg(lut), _ptr(out), out.stride(0)), "tq_matmul")
     return out
 
 
@@ -306,10 +321,9 @@ def matmul_x(qtype, tiles, K, N, x, lut=None, out=None):
     out = _out(x, N, out)
     st = _stream(x)
     need = _size_query("tq_matmul_x_workspace_bytes", qtype, K, N, M)
-    ws = workspace(x.device, st, need) if need else None
-    check(lib().tq_matmul_x(qtype, _ptr(tiles), K, N, _DTYPES[x.dtype], _ptr(x), x.stride(0), M,
-                            _lut_arg(lut), _ptr(out), out.stride(0), _ptr(ws), need, st),
-          "tq_matmul_x")
+    check(_with_workspace(lib().tq_matmul_x, x.device, st, need, qtype, _ptr(tiles), K, N,
+                          _DTYPES[x.dtype], _ptr(x), x.stride(0), M, _lut_arg(lut), _ptr(out),
+                          out.stride(0)), "tq_matmul_x")
     return out
 
 
@@ -378,9 +392,8 @@ def matmul_mx(tiles, K, N, q, e, out=None):
     out = _out(q, N, out)
     st = _stream(q)
     need = _size_query("tq_matmul_mx_workspace_bytes", K, N, M)
-    ws = workspace(q.device, st, need) if need else None
-    check(lib().tq_matmul_mx(_ptr(tiles), K, N, _ptr(q), _ptr(e), M, _ptr(out), out.stride(0),
-                             _ptr(ws), need, st), "tq_matmul_mx")
+    check(_with_workspace(lib().tq_matmul_mx, q.device, st, need, _ptr(tiles), K, N, _ptr(q),
+                          _ptr(e), M, _ptr(out), out.stride(0)), "tq_matmul_mx")
     return out
 
 
@@ -637,12 +650,12 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
         o_ts, o_hs = _check_heads(name, "out", out, (out.shape[0], Hq, D), q.dtype, dev)
     st = _stream_of(dev)
     need = _size_query("tq_tree_attention_workspace_bytes", B, Hq, kv_heads, D, max_nodes, max_ctx)
-    ws = workspace(q.device, st, need).data_ptr() if need else None
-    status = lib().tq_tree_attention(
-        ctype, code, q.data_ptr(), q_ts, q_hs, T, Hq, kv_heads, D, k_cache.data_ptr(),
-        v_cache.data_ptr(), n_pages, page_size, page_table.data_ptr(), page_table.stride(0), width,
-        B, ctx_lens.data_ptr(), starts.data_ptr(), mp, stride, words, max_nodes, max_ctx,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), o_ts, o_hs, ws, need, st)
+    status = _with_workspace(
+        lib().tq_tree_attention, q.device, st, need, ctype, code, q.data_ptr(), q_ts, q_hs, T, Hq,
+        kv_heads, D, k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page_size,
+        page_table.data_ptr(), page_table.stride(0), width, B, ctx_lens.data_ptr(),
+        starts.data_ptr(), mp, stride, words, max_nodes, max_ctx,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), o_ts, o_hs)
     if status:
         check(status, name)
     return out
@@ -693,11 +706,11 @@ def verify_draft(target, tokens, starts, uniforms, final_uniforms, draft=None, p
     nodes = torch.empty_like(out_tokens)
     st = _stream_of(dev)
     need = _size_query("tq_verify_draft_workspace_bytes", B, V)
-    ws = workspace(device, st, need).data_ptr() if need else None
-    status = lib().tq_verify_draft(
-        code, target.data_ptr(), target.stride(0), dp, d_stride, N, V, tokens.data_ptr(), parp,
-        starts.data_ptr(), B, uniforms.data_ptr(), final_uniforms.data_ptr(), width,
-        accepted.data_ptr(), out_tokens.data_ptr(), nodes.data_ptr(), ws, need, st)
+    status = _with_workspace(
+        lib().tq_verify_draft, device, st, need, code, target.data_ptr(), target.stride(0), dp,
+        d_stride, N, V, tokens.data_ptr(), parp, starts.data_ptr(), B, uniforms.data_ptr(),
+        final_uniforms.data_ptr(), width, accepted.data_ptr(), out_tokens.data_ptr(),
+        nodes.data_ptr())
     if status:
         check(status, name)
     return accepted, out_tokens, nodes

@@ -294,7 +294,9 @@ int tq_matmul_path(int type, int64_t K, int64_t N, int64_t M);
  * first use and are left zero by every call; scratch starts at byte
  * TQ_NOALLOC_SCRATCH_BYTES (on TQ_PATH_GEMM_SPLIT, S * M * N fp32 partial
  * planes) and its contents do not matter.  So one zero-filled workspace, as
- * large as the largest call needs, serves calls of any shapes, in turn. */
+ * large as the largest call needs, serves calls of any shapes, in turn.  A call
+ * may be several launches: host threads that share a stream and a workspace
+ * enqueue their calls one at a time. */
 size_t tq_matmul_workspace_bytes(int type, int64_t K, int64_t N, int64_t M);
 
 /* The product for any M, on the path tq_matmul_path() names: tq_qgemv (M <= 8,
