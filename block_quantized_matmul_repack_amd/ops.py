@@ -461,11 +461,10 @@ def _check_index(name, what, t, n, dev):
 def _check_heads(name, what, t, shape, dtype, dev):
     """t is `shape` of dtype on device dev with contiguous rows; returns its
     token and head strides."""
-    ts, hs, es = t.stride()
-    if t.shape != shape or t.dtype is not dtype or (es != 1 and shape[2] > 1) or \
+    if t.shape != shape or t.dtype is not dtype or (t.stride(2) != 1 and shape[2] > 1) or \
             t.get_device() != dev:
         _refuse(name, what, f"{dtype} {tuple(shape)} with contiguous rows on device {dev}", t)
-    return ts, hs
+    return t.stride(0), t.stride(1)
 
 
 def _heads_of(name, what, t, dtypes):

@@ -107,3 +107,18 @@ def test_calls_on_one_stream_take_turns(library):
     assert library.calls == 20
     assert not library.shared
     assert len(ops._workspaces) == 1
+
+
+def test_outputs_of_another_rank_are_refused(library):
+    """The binding's own error, not Python's from taking strides apart."""
+    q, k = (gpu(torch.zeros((3, h, 64), dtype=torch.bfloat16)) for h in (8, 2))
+    pos, freq = gpu(torch.zeros(3, dtype=torch.int32)), gpu(torch.ones(32))
+    for bad in (gpu(torch.zeros((3, 8 * 64), dtype=torch.bfloat16)),
+                gpu(torch.zeros((1, 3, 8, 64), dtype=torch.bfloat16)),
+                gpu(torch.zeros((), dtype=torch.bfloat16))):
+        with pytest.raises(tq.TiledqError, match="q_out"):
+            tq.qk_norm_rope(q, k, pos, freq, q_out=bad)
+        with pytest.raises(tq.TiledqError, match="k_out"):
+            tq.qk_norm_rope(q, k, pos, freq, k_out=bad)
+    q_out, k_out = tq.qk_norm_rope(q, k, pos, freq)
+    assert q_out.shape == q.shape and k_out.shape == k.shape
