@@ -45,6 +45,7 @@ SIGNATURES = {
     "tq_qgemv_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
     "tq_qgemm_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
     "tq_matmul_flat": (INT, [INT, P, I64, I64, P, P, I64, P, P, I64, P]),
+    "tq_capture_id": (INT, [P, P]),
     "tq_qk_norm_rope": (INT, [INT, P, I64, I64, I64, P, I64, I64, I64, I64, I64, I64, INT, INT, P,
                               P, F32, P, P, P, I64, I64, P, I64, I64, P]),
     "tq_cache_bytes": (SZ, [INT, I64, I64, I64, I64]),

@@ -202,6 +202,24 @@ int tq_supported(int type, int64_t K, int64_t N, int64_t M, int path)
     return path == TQ_PATH_GEMM || path == TQ_PATH_GEMM_FLAT;
 }
 
+int tq_capture_id(hipStream_t stream, uint64_t *id)
+{
+    if (!id)
+        return TQ_E_NULL;
+    *id = 0;
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    unsigned long long n = 0;
+    if (hipStreamGetCaptureInfo(stream, &status, &n) != hipSuccess) {
+        (void)hipGetLastError();                 // not the next launch's error
+        return TQ_E_LAUNCH;
+    }
+    if (status == hipStreamCaptureStatusInvalidated)
+        return TQ_E_LAUNCH;
+    if (status == hipStreamCaptureStatusActive)
+        *id = (uint64_t)n + 1;                   // the runtime may count from 0
+    return TQ_OK;
+}
+
 const char *tq_status_string(int status)
 {
     switch (status) {

@@ -181,11 +181,32 @@ def _out(q, N, out):
 # on a stream keeps that stream's workspace: replaying it on another stream
 # while calls run on the capture stream would share the workspace, so replay
 # it on the capture stream or keep the two apart in time.  A workspace that has
-# become too small is kept: a captured graph may still write to it.  A call
-# that is captured before a workspace large enough was there gets one of the
-# graph's own, zero-filled by every replay.
+# become too small is kept: a captured graph may still write to it.  Calls that
+# are captured before a workspace large enough was there share one of the
+# graph's own, in its memory, of which every replay clears once what has to be
+# zero.  It is held until a later capture on that stream or an eager call there:
+# the capture's own tensors must not get its memory.
 _workspaces = {}
 _outgrown = []
+_captured = {}                       # (device, stream): capture's number, workspace
+_COUNTERS = 1 << 20                  # TQ_NOALLOC_SCRATCH_BYTES: what lies behind is scratch
+
+
+def _capture_of(stream_handle):
+    """Number of the capture that a stream is part of, 0 if none."""
+    n = ctypes.c_uint64()
+    check(lib().tq_capture_id(stream_handle, ctypes.byref(n)), "tq_capture_id")
+    return n.value
+
+
+def _captured_workspace(device, stream_handle, capture, nbytes):
+    key = (device, stream_handle)
+    number, ws = _captured.get(key, (0, None))
+    if number != capture or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:_COUNTERS].zero_()
+        _captured[key] = (capture, ws)
+    return ws
 
 
 def workspace(device, stream_handle, nbytes):
@@ -193,8 +214,10 @@ def workspace(device, stream_handle, nbytes):
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         size = max(nbytes, 1 << 16)
-        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-            return torch.zeros(size, dtype=torch.uint8, device=device)
+        capture = _capture_of(stream_handle) if device.type == "cuda" else 0
+        if capture:
+            return _captured_workspace(device, stream_handle, capture, size)
+        _captured.pop(key, None)
         if ws is not None:
             _outgrown.append(ws)
             size = max(size, 2 * ws.numel())     # so that they stay few

@@ -562,6 +562,13 @@ int tq_verify_draft(int dtype, const void *target, int64_t target_stride,
                     int64_t width, int32_t *accepted, int32_t *out_tokens, int32_t *out_nodes,
                     void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Which HIP graph capture `stream` is part of: *id becomes 0 outside one, else
+ * a number that no other capture of the process has.  For callers that keep a
+ * workspace: one allocated and cleared inside a capture belongs to its graph,
+ * whose replays clear it, and serves the other calls of that capture.
+ * TQ_E_LAUNCH where the runtime refuses to say (an invalidated capture). */
+int tq_capture_id(hipStream_t stream, uint64_t *id);
+
 /* Test instrument for the per-block integer dot ("Q2_0 Format" > "HVX
  * Vector Dot-Product": int8 products accumulated in 32-bit words, before the
  * row scale d of "Block-32 Quantized Formats" is applied): run the tq_qgemv

@@ -122,3 +122,23 @@ def test_outputs_of_another_rank_are_refused(library):
             tq.qk_norm_rope(q, k, pos, freq, k_out=bad)
     q_out, k_out = tq.qk_norm_rope(q, k, pos, freq)
     assert q_out.shape == q.shape and k_out.shape == k.shape
+
+
+def test_capture_number_needs_a_place():
+    assert ops.lib().tq_capture_id(None, None) == 1          # TQ_E_NULL
+
+
+def test_calls_of_a_capture_share_a_workspace(monkeypatch):
+    """A larger need gets a larger one, another capture or stream its own, and
+    only the counters are cleared."""
+    monkeypatch.setattr(ops, "_captured", {})
+    cpu = torch.device("cpu")
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: real(*a, **k).fill_(9))
+    first = ops._captured_workspace(cpu, 1, 11, 1 << 21)
+    assert ops._captured_workspace(cpu, 1, 11, 1 << 16) is first
+    assert not first[:1 << 20].any() and bool((first[1 << 20:] == 9).all())
+    larger = ops._captured_workspace(cpu, 1, 11, (1 << 21) + 1)
+    assert larger is not first and ops._captured_workspace(cpu, 1, 11, 1 << 21) is larger
+    assert ops._captured_workspace(cpu, 2, 11, 1 << 16) is not larger
+    assert ops._captured_workspace(cpu, 1, 12, 1 << 16) is not larger
