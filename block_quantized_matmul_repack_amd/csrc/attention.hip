@@ -475,6 +475,50 @@ __device__ __forceinline__ void set_sequence(Cursor &c, const AttnArgs &a, const
     c.blocks = blocks_of(a, p, w);
 }
 
+// Key head h and row block rb of sequence b (none where b is the batch).
+struct Unit {
+    int b, h, rb;
+};
+
+// Every sequence has the row blocks of max_nodes tokens.
+__device__ __forceinline__ Unit unit_of(const AttnArgs &a, const AttnPlan &p, uint32_t unit)
+{
+    const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = unit / per, q = unit - b * per;
+    const uint32_t h = q / p.row_blocks;
+    return {(int)min(b, (uint32_t)a.batch), (int)h, (int)(q - h * p.row_blocks)};
+}
+
+// Row blocks in the order of the rows, where max_nodes is far above what
+// sequences have.  With x(b) = rows before sequence b / rows of a block, its
+// row blocks, ceil(x(b + 1) - x(b)) at most, fit between first(b) = floor(x(b))
+// + b and first(b + 1), whatever the lengths: no sum over sequences is needed,
+// and a wave finds b in three turns of 64 looks.  Starts that go back lead to
+// some sequence inside the batch.
+__device__ __forceinline__ Unit unit_by_rows(const AttnArgs &a, const AttnPlan &p, uint32_t unit,
+                                             int lane)
+{
+    const uint32_t v = unit / (uint32_t)a.kv_heads;
+    auto first = [&](int b) {
+        const uint32_t t = (uint32_t)min(max((int64_t)a.starts[b], (int64_t)0), a.tokens);
+        return t * (uint32_t)a.group / (uint32_t)(p.tiles * 16) + (uint32_t)b;
+    };
+    int lo = 0, hi = a.batch;                    // lo <= b < hi
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) >> 6, b = lo + lane * step;
+        const uint64_t after = __ballot(b >= hi || first(b) > v);
+        const int k = after ? __builtin_ctzll(after) : 64;
+        if (k == 0)
+            return {a.batch, 0, 0};              // rows before the first sequence
+        lo += (k - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    const uint32_t f0 = (uint32_t)uniform((int)first(lo)), f1 = (uint32_t)uniform((int)first(lo + 1));
+    if (v < f0 || v >= f1)
+        return {a.batch, 0, 0};
+    const uint32_t n = f1 - f0, q = unit - f0 * (uint32_t)a.kv_heads, h = q / n;
+    return {lo, (int)h, (int)(q - h * n)};
+}
+
 __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &p, int keys,
                                              int lane)
 {
@@ -482,12 +526,14 @@ __device__ __forceinline__ Cursor first_span(const AttnArgs &a, const AttnPlan &
     c.left = c.enter = 0;
     if (p.groups == 0) {
         // many heads: one workgroup for all the keys of each
-        const uint32_t per = (uint32_t)a.kv_heads * p.row_blocks, b = blockIdx.x / per;
-        set_sequence(c, a, p, keys, rows_of(a, (int)b));
-        const uint32_t q = blockIdx.x - b * per, h = q / p.row_blocks, rb = q - h * p.row_blocks;
-        c.q = (int)(h * c.blocks + rb);
+        const uint32_t unit = blockIdx.y * gridDim.x + blockIdx.x;
+        const Unit u = p.by_rows ? unit_by_rows(a, p, unit, lane) : unit_of(a, p, unit);
+        if (u.b >= a.batch)
+            return c;
+        set_sequence(c, a, p, keys, rows_of(a, u.b));
+        c.q = u.h * c.blocks + u.rb;
         c.step = 0;
-        if ((int)rb < c.blocks)
+        if (u.h < a.kv_heads && u.rb < c.blocks)
             c.left = c.steps;
         return c;
     }
@@ -1259,7 +1305,7 @@ __global__ __launch_bounds__(THREADS) void k_attn_combine(AttnArgs a, AttnPlan p
 constexpr int rows_qt(int D) { return D <= 128 ? 2 : 1; }
 
 template <int CT, int D, bool FINE>
-void launch_steps(const Launch &args, unsigned grid, hipStream_t s)
+void launch_steps(const Launch &args, dim3 grid, hipStream_t s)
 {
     constexpr int QT = rows_qt(D);
     const AttnPlan &p = args.p;
@@ -1282,12 +1328,28 @@ void launch_steps(const Launch &args, unsigned grid, hipStream_t s)
     }
 }
 
+// Workgroups of an uncut launch: all sequences with the row blocks that
+// max_nodes asks for, or (by_rows) no more row blocks than `tokens` rows can
+// fill, one begun for each sequence.  Below 2^27 within the limits of the entry
+// point; the second grid dimension holds what the first does not.
+int64_t unit_count(const AttnArgs &a, const AttnPlan &p)
+{
+    return a.kv_heads * (p.by_rows ? a.tokens * a.group / (p.tiles * 16) + a.batch
+                                   : (int64_t)a.batch * p.row_blocks);
+}
+
+dim3 unit_grid(int64_t units)
+{
+    constexpr int64_t X = 1 << 20;
+    return units <= X ? dim3((unsigned)units) : dim3((unsigned)X, (unsigned)((units + X - 1) / X));
+}
+
 template <int CT, int D>
 hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStream_t s)
 {
     const int64_t units = (int64_t)a.batch * a.kv_heads * p.row_blocks;
-    const int64_t blocks = p.groups ? p.groups : units;
-    if (!grid_fits(blocks, 64 * p.waves))
+    const dim3 grid = p.groups ? dim3((unsigned)p.groups) : unit_grid(unit_count(a, p));
+    if (!grid_fits(grid.x, 64 * p.waves))
         return hipErrorInvalidConfiguration;
     const int F = p.tiles * (D / 16);
     Parts parts{nullptr, nullptr, nullptr};
@@ -1298,9 +1360,9 @@ hipError_t launch_cd(const AttnArgs &a, const AttnPlan &p, void *scratch, hipStr
     }
     const Launch args{a, p, parts};
     if (a.dtype == TQ_F16)
-        launch_steps<CT, D, true>(args, (unsigned)blocks, s);
+        launch_steps<CT, D, true>(args, grid, s);
     else
-        launch_steps<CT, D, false>(args, (unsigned)blocks, s);
+        launch_steps<CT, D, false>(args, grid, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.groups <= 1)
         return e;
@@ -1329,7 +1391,7 @@ hipError_t launch_c(int D, const AttnArgs &a, const AttnPlan &p, void *scratch, 
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys)
 {
-    AttnPlan p;
+    AttnPlan p{};
     const int64_t rows = max_nodes * (heads / kv_heads);
     const int qt = rows_qt(D);
     if (rows <= 16) {
@@ -1366,9 +1428,14 @@ size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_he
            (size_t)batch * kv_heads * p.row_blocks * sizeof(int2);
 }
 
-hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
+hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &plan,
                             void *scratch, hipStream_t s)
 {
+    AttnPlan p = plan;
+    p.by_rows = 1;
+    const int64_t by_rows = unit_count(a, p);
+    p.by_rows = 0;
+    p.by_rows = p.groups == 0 && by_rows < unit_count(a, p);
     return cache_type == TQ_Q8_0 ? launch_c<TQ_Q8_0>(D, a, p, scratch, s)
                                  : launch_c<TQ_Q4_0>(D, a, p, scratch, s);
 }

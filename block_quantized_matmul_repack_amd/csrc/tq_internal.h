@@ -313,8 +313,9 @@ __device__ __forceinline__ void q4k_scale_min(const uint32_t (&s3)[3], int j, ui
 
 // A dispatch counts work-items in 32 bits per grid dimension.  The shape
 // limits of the entry points keep every grid of the library below 2^31
-// work-items; each launcher still checks its grid (`blocks` workgroups of
-// `threads`) before converting it, and refuses an oversized one.
+// work-items per dimension (the attention's by its second one); each launcher
+// still checks its grid (`blocks` workgroups of `threads`) before converting
+// it, and refuses an oversized one.
 inline bool grid_fits(int64_t blocks, int threads)
 {
     return blocks >= 0 && blocks * threads < (int64_t(1) << 32);
@@ -434,9 +435,10 @@ struct AttnArgs {
 };
 // Launch geometry, from host sizes alone: waves and 16-row tiles per workgroup
 // (in row_groups groups of waves), row blocks of them, and how many workgroups
-// share the key steps (0: each head and row block has its own).
+// share the key steps (0: each head and row block has its own; by_rows: found
+// from the rows before each sequence, set at the launch).
 struct AttnPlan {
-    int waves, tiles, row_groups, row_blocks, groups;
+    int waves, tiles, row_groups, row_blocks, groups, by_rows;
 };
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
                    int64_t max_keys);
