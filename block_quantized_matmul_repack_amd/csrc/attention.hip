@@ -63,6 +63,10 @@ constexpr int STEP = 32;                         // keys per wave and step
 constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -1e30f;
+// 2^22: half a step of fp32 is 1/4 there.  Taking the other way past it costs the
+// trees of the table 1 us of 63, the long case under 1, single tokens nothing (a
+// branch by itself; shared with the raise it spills, 68 and 101 us).
+constexpr float FAR = 4194304.0f;
 constexpr int RED = 8;                           // fragments joined at a time
 // What entering a head and row block costs, in keys, and the shortest span: one
 // below that costs more to join than it saves (one token over 8192 keys: 15.6 us
@@ -687,7 +691,7 @@ __device__ __forceinline__ void store_frag(const AttnArgs &a, const Rows &w, int
 template <int D> struct Query {
     h8 q[D / 32];
     float c, m;
-    int node;
+    int node, far;                               // far: some row's reference is (uniform)
     f4 l, o[D / 16];                             // l: the sum in each element
 };
 
@@ -728,6 +732,7 @@ __device__ __forceinline__ void load_query(Query<D> &x, const AttnArgs &a, const
             x.q[s][e] = (_Float16)(v[s][e] * up);
     x.c = a.scale * 1.44269504088896f * down;
     x.m = NO_REF;
+    x.far = 0;
     x.l = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < D / 16; t++)
@@ -779,6 +784,17 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// The exponent where the reference is so large that fp32's steps there, which
+// a product rounded only with the sum would be off the reference by, are no
+// longer small: the product rounded by itself, as the reference was, so that
+// none passes it by more than RAISE.
+__device__ __forceinline__ float far_exponent(float s, float c, float m)
+{
+#pragma clang fp contract(off)
+    const float x = s * c;
+    return (x - m) + BIAS;
+}
+
 // Probabilities of 32 keys as the operand of the second product; the
 // reference, sum and outputs follow where a score passes it.  The sum is one
 // more product, with a row of ones: it then adds the rounded probabilities,
@@ -800,18 +816,28 @@ __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x, h8 &re
         const float mn = fmaxf(x.m, top);
         const float f = __builtin_amdgcn_exp2f(x.m - mn);
         x.m = mn;
+        x.far = uniform(__any(fabsf(mn) > FAR && mn != NO_REF));
         x.l *= f;
 #pragma unroll
         for (int t = 0; t < D / 16; t++)
             x.o[t] *= f;
     }
     const float ref = BIAS - x.m;
+    float z[2][4];
+    if (__builtin_expect(x.far, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            z[i >> 2][i & 3] = far_exponent(s[i >> 2][i & 3], x.c, x.m);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            z[i >> 2][i & 3] = fmaf(s[i >> 2][i & 3], x.c, ref);
+    }
     Frag p, r;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int T = i >> 1, e = 2 * (i & 1);
-        const f2 y = {__builtin_amdgcn_exp2f(fmaf(s[T][e], x.c, ref)),
-                      __builtin_amdgcn_exp2f(fmaf(s[T][e + 1], x.c, ref))};
+        const f2 y = {__builtin_amdgcn_exp2f(z[T][e]), __builtin_amdgcn_exp2f(z[T][e + 1])};
         p.p[i] = __builtin_convertvector(y, h2);
         if constexpr (FINE)
             r.p[i] = __builtin_convertvector(
