@@ -62,7 +62,7 @@ constexpr int THREADS = 64 * WAVES;
 constexpr int STEP = 32;                         // keys per wave and step
 constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
-constexpr float NO_REF = -1e30f;
+constexpr float NO_REF = -3e38f;                 // near the lowest number: no score seen yet
 // 2^22: half a step of fp32 is 1/4 there.  Taking the other way past it costs the
 // trees of the table 1 us of 63, the long case under 1, single tokens nothing (a
 // branch by itself; shared with the raise it spills, 68 and 101 us).

@@ -75,3 +75,12 @@ def test_scores_of_many_millions(tq, kind, dt, sign, seqs, Hq, Hkv):
             tol = (2 * 2.0 ** -11 + ref.half_step(s.q.dtype)) * v.abs() + 2.0 ** -24
             assert bool(((out[row + i] - v).abs() <= tol).all())
         row += n
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,Hq,Hkv", SHAPES)
+def test_scores_far_below_zero(tq, kind, seqs, Hq, Hkv):
+    """All scores of a row near -10^32: it sees keys all the same."""
+    s = equal_keys(seqs, Hq, Hkv, 128, "bf16", kind, FULL[kind] / 8)(tq)
+    s.q = torch.full_like(s.q, -2.0 ** 100 if FULL[kind] > 0 else 2.0 ** 100)
+    check_alike(s, s.run())
