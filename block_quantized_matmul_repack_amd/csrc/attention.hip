@@ -730,7 +730,8 @@ __device__ __forceinline__ void load_query(Query<D> &x, const AttnArgs &a, const
 #pragma unroll
         for (int e = 0; e < 8; e++)
             x.q[s][e] = (_Float16)(v[s][e] * up);
-    x.c = a.scale * 1.44269504088896f * down;
+    // not 0, which would make a number of the -inf of a key that is not seen
+    x.c = fmaxf(a.scale * 1.44269504088896f * down, 0x1p-126f);
     x.m = NO_REF;
     x.far = 0;
     x.l = f4{0.0f, 0.0f, 0.0f, 0.0f};

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import decode_ref as ref
-from test_gpu_attention import KINDS, Setup, tq  # noqa: F401
+from test_gpu_attention import KINDS, Setup, pack, tq, tree_masks  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,13 @@ def test_scores_far_below_zero(tq, kind, seqs, Hq, Hkv):
     s = equal_keys(seqs, Hq, Hkv, 128, "bf16", kind, FULL[kind] / 8)(tq)
     s.q = torch.full_like(s.q, -2.0 ** 100 if FULL[kind] > 0 else 2.0 ** 100)
     check_alike(s, s.run())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,Hq,Hkv", SHAPES)
+def test_scores_below_fp32(tq, kind, seqs, Hq, Hkv):
+    """Scores that are zero in fp32, beside keys that a mask hides."""
+    s = equal_keys(seqs, Hq, Hkv, 128, "bf16", kind, FULL[kind])(tq)
+    s.q = torch.full_like(s.q, 2.0 ** -120)
+    masks = tree_masks(seqs, 6)
+    check_alike(s, s.run(scale=1e-12, mask=pack(masks)), masks)
