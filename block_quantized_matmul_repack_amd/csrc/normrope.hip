@@ -9,8 +9,10 @@
 // A wave owns one token and several heads: its angles are the same for every
 // head, so each is computed once, by one lane, and passed on through LDS (each
 // lane computing the angles of its own elements, eight times as many, took
-// 44 us where this takes 40).  8192 tokens, 32 + 8 heads of 128, bf16, nothing
-// in the caches: 36.8 us, 4.6 TB/s; copies of the two tensors 35.
+// 44 us where this took 40, both with one wave a token).  8192 tokens, 32 + 8
+// heads of 128, bf16, nothing in the caches, two waves a token: 36.8 us, 4.6
+// TB/s; copies of the two tensors 35.  Called again and again on the same
+// tensors, half of which the caches then hold: 32.
 #include <algorithm>
 
 #include "tq_internal.h"
@@ -195,9 +197,19 @@ hipError_t launch_dt(const NormRopeArgs &a, hipStream_t s)
         log_lanes++;
     const int groups = 64 >> log_lanes;
     const int64_t rounds = (a.heads[0] + a.heads[1] + groups - 1) / groups;
-    // few tokens: a token's heads are spread over waves, one round each; two
-    // waves of 8192 tokens' 5 rounds take 36.8 us, one 40.7, five 38.9
-    int64_t parts = std::min<int64_t>(rounds, std::max<int64_t>(1, 16384 / a.tokens));
+    // Few tokens: a token's heads are spread over waves, one round each, as far
+    // as that fills the chip twice (256 units, 32 waves each).  Many: a wave has a
+    // few rounds, since its angles cost as much as one or two, and with all of
+    // them the last waves run alone.  5 rounds of 16-byte loads (32 + 8 heads of
+    // 128, bf16, caches flushed, one call): two waves a token 49.9, 67.3, 83.9 and
+    // 502 us for 8193, 12000, 16384 and 131072 tokens, one 54.0, 70.2, 88.5 and
+    // 503, five 48.0, 65.0, 82.5 and 533; 9 rounds: three 80.3 and 869 us for 8193
+    // and 131072, one 91.7 and 922.  Rounds of single elements are an eighth as
+    // long: 40 of them (32 + 8 heads of 72), four waves 115 and 789 us for 8193 and
+    // 65536, one 149 and 780, ten 120 and 873.
+    const int64_t least = (rounds + (wide ? 2 : 9)) / (wide ? 3 : 10);
+    int64_t parts = std::max(least, std::min<int64_t>(rounds, 16384 / a.tokens));
+    parts = std::max<int64_t>(1, std::min(parts, (int64_t(1) << 25) / a.tokens));  // the grid's limit
     const int64_t blocks = (a.tokens * parts + WAVES - 1) / WAVES;
     if (!grid_fits(blocks, THREADS))
         return hipErrorInvalidConfiguration;
