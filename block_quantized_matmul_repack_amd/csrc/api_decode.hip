@@ -202,7 +202,7 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
         return TQ_E_ALIGN;
     const tq::AttnPlan p = tq::attn_plan((int)D, batch, heads, kv_heads, max_nodes,
                                          max_ctx + max_nodes);
-    uint32_t *counters;
+    uint32_t *counters;                          // unused: the layout that all calls share
     void *scratch;
     const int st = scratch_of(
         workspace, workspace_bytes,

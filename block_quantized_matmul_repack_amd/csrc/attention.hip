@@ -10,14 +10,16 @@
 //
 // Bound: a single token's step reads every cached byte once and is bound by
 // HBM; trees multiply each dequantized key with many rows: the vector pipe
-// (dequantization, softmax), LDS and the matrix cores are busy 46, 38 and 30 %
+// (dequantization, softmax), LDS and the matrix cores are busy 45, 37 and 29 %
 // of the trees' launch.  Measured (32 query heads, 8 key heads of 128, Q8_0 unless
-// said): 64 sequences of 1600 to 16384 keys, one token: 232 us, 6.0 TB/s of
+// said): 64 sequences of 1600 to 16384 keys, one token: 229 us, 6.1 TB/s of
 // cache (loads alone, nothing computed: 5.9; a plain read of the bytes: 7.1);
-// one sequence of 8192 keys: 15 us, latency; 13 drafted tokens over 131000
-// keys: 99 us in fp16, 73 in bf16 (k_attn_rows 64, of which 15 start and store; 5 joining); 4 Q4_0
-// trees of up to 63 nodes over 20011 keys: 67 us (56, and 10 joining; each
-// further key at 1.0 PFLOP/s, counting the rows of whole tiles).
+// one sequence of 8192 keys: 14 us, latency; 13 drafted tokens over 131000
+// keys: 91 us in fp16 (k_attn_rows 92 and 5 joining when traced), 72 in bf16 (66,
+// of which 15 start and store, and 5); 4 Q4_0 trees of up to 63 nodes over 20011
+// keys: 62 us (58 and 11; each further key at 1.0 PFLOP/s, counting the rows of
+// whole tiles).  A prompt's rows multiply all keys up to its end, twice what they
+// see: 8192 tokens with none cached 1633 us, 337 TFLOP/s of what is seen.
 //
 // Split: rows are (token, query head) pairs of one key head, 16 per matrix
 // tile, so a cached byte serves all the query heads and tokens of its head.
@@ -33,8 +35,8 @@
 // the codes to match).  With more rows (k_attn_rows) the waves share the
 // dequantized operands of 64 or 128 keys through LDS, stored as the fragments that
 // the matrix instructions read.  Four row tiles a wave instead of two read
-// LDS half as often but leave one wave per SIMD: 112 us for the 13 tokens, 106
-// for the trees (70 and 63), so two it is.
+// LDS half as often but leave one wave per SIMD: 112 us for the 13 tokens in
+// bf16, 106 for the trees (70 and 63 with two, both then), so two it is.
 //
 // Rounding: the queries enter as fp16 after a scaling of each row by a power
 // of two that puts its largest element in [2^14, 2^15) (bf16 elements down to
@@ -47,8 +49,9 @@
 // keys are exact (k_attn: a second operand with the rest, k_attn_rows: the codes
 // as operands, the scales times the products in fp32).  The error is then 1.4
 // times that of rounding exact outputs to fp16, 3.6 times without, where some
-// channels of the keys are loud.  13 tokens over 131000 keys take 99 us so, 73
-// without; k_attn, bound by HBM, takes no longer.
+// channels of the keys are loud.  13 tokens over 131000 keys take 91 us so, 72
+// without; k_attn, bound by HBM, takes no longer.  k_attn_rows with heads of 128
+// then spills 3 to 22 of a lane's 256 registers, 16 to 60 bytes of scratch.
 #include <algorithm>
 
 #include "cache_layout.h"
@@ -63,9 +66,9 @@ constexpr int STEP = 32;                         // keys per wave and step
 constexpr int STRIDE = STEP * WAVES;
 constexpr float RAISE = 4.0f, BIAS = 10.0f;      // p <= 2^(RAISE + BIAS) = 2^14
 constexpr float NO_REF = -3e38f;                 // near the lowest number: no score seen yet
-// 2^22: half a step of fp32 is 1/4 there.  Taking the other way past it costs the
-// trees of the table 1 us of 63, the long case under 1, single tokens nothing (a
-// branch by itself; shared with the raise it spills, 68 and 101 us).
+// 2^22: half a step of fp32 is 1/4 there.  The branch for what lies past it costs
+// those trees 1 us of 63, the 13 tokens under 1 and single tokens nothing; in one
+// branch with the raise it needs more registers than there are (69 and 103 us).
 constexpr float FAR = 4194304.0f;
 constexpr int RED = 8;                           // fragments joined at a time
 // What entering a head and row block costs, in keys, and the shortest span: one
@@ -1433,10 +1436,14 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     }
     p.row_blocks = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
     const int64_t units = batch * kv_heads * p.row_blocks;
-    // as many workgroups as are resident: two of four waves on each of 256
-    // compute units, or one of eight; one of four where a head is wider than 128
-    // (256 elements, 4 sequences of 8192 keys, 32 tokens: 65.9 us, with two a
-    // unit in the line 80.5)
+    // Two workgroups of four waves for each of 256 compute units, or one of
+    // eight; one of four where a head is wider than 128 (256 elements, 4
+    // sequences of 8192 keys, 32 tokens: 65.9 us, with two a unit in the line
+    // 80.5).  That is what fits with 16 and more rows of heads of 96 and 128; by
+    // their registers, one row tile of 64 elements would leave room for four a
+    // unit, of 96 and 128 in Q4_0 for three, of 256 in Q4_0 for two.  One token
+    // for each of 64 sequences of 8192 keys reads 6.0 (64, Q8_0), 4.0 (64, Q4_0),
+    // 5.7 (128, Q4_0) and 5.7 TB/s (256, Q4_0) so, 6.4 with 128 in Q8_0.
     p.waves = p.row_groups > 1 && D <= 128 && units <= FEW_UNITS ? 8 : 4;
     const int keys = p.waves * (p.row_groups > 1 ? 16 : STEP), least = MIN_KEYS / keys;
     const int64_t line = units * ((max_keys + keys - 1) / keys + least);

@@ -24,9 +24,10 @@
 // workgroup, on a cache line of its sequence's own, since such atomics on one
 // line follow each other (with one per wave on a shared line 32 trees took 44
 // us).  One sequence of
-// 5 nodes over 128001 tokens: 11.7 us; 32 trees of up to 31 nodes: 21.7 us.
+// 5 nodes over 128001 tokens: 12.0 us; 32 trees of up to 31 nodes: 21.8 us.
 // Trees drafted with probabilities need whole-row sums during the walk and
-// run as one workgroup per sequence instead.
+// run as one workgroup per sequence instead: one of 31 nodes 32 us, 32 of them
+// 105.
 #include <algorithm>
 
 #include "tq_internal.h"
@@ -453,8 +454,9 @@ hipError_t launch_dt(const VerifyArgs &a, uint32_t *counters, double *sums, hipS
         k_verify_tree<DT><<<dim3((unsigned)a.batch), THREADS, rec, s>>>(a, tiles, sums);
         return hipGetLastError();
     }
-    // one tile a wave, or up to four where that gives more workgroups than
-    // the chip holds (256 compute units, two each)
+    // one tile a wave, or up to four where that gives more than 512 workgroups:
+    // two for each of 256 compute units, of which its registers let one run at a
+    // time (66 a lane; 64 would let two)
     const int64_t groups = (int64_t)a.batch * ((tiles + WAVES - 1) / WAVES);
     const int per = (int)std::min<int64_t>(MOST_TILES / WAVES, (groups + 511) / 512);
     const int x = (tiles + WAVES * per - 1) / (WAVES * per);

@@ -505,11 +505,14 @@ int tq_cache_read(int type, int dtype, const void *k_cache, const void *v_cache,
  *           sequence are not computed (their rows stay as they were); a
  *           longer cache than max_ctx costs speed, nothing else.
  *   workspace : 256-byte aligned, tq_tree_attention_workspace_bytes() bytes
- *           (0: may be NULL), laid out as tq_matmul's: the first
- *           TQ_NOALLOC_SCRATCH_BYTES zero before the first use and after
- *           every call, scratch behind.  A smaller one: TQ_E_SHAPE.
- * Queries enter the matrix cores as fp16 after an exact scaling of each row,
- * codes times scales and probabilities rounded once to fp16; sums in fp32.
+ *           (0: may be NULL), laid out as tq_matmul's, so that one serves both:
+ *           the first TQ_NOALLOC_SCRATCH_BYTES zero before the first use and
+ *           after every call (this one leaves them alone), scratch behind.  A
+ *           smaller one: TQ_E_SHAPE.
+ * Queries enter the matrix cores as fp16 after an exact scaling of each row;
+ * sums in fp32.  With TQ_BF16, codes times scales and probabilities are rounded
+ * once to fp16; with TQ_F16 only the values' are: keys enter exactly and
+ * probabilities to 22 bits.  Scores may have any size that fp32 holds.
  * Deterministic.  Domain: heads a multiple of kv_heads, both 1..1024; tokens
  * 0..2^20; batch 0..65535; table_pages * page_size and max_ctx up to 2^30;
  * scale finite and > 0. */
