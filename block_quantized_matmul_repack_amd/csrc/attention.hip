@@ -820,7 +820,8 @@ __device__ __forceinline__ h8 softmax_step(const f4 (&s)[2], Query<D> &x, h8 &re
         const float mn = fmaxf(x.m, top);
         const float f = __builtin_amdgcn_exp2f(x.m - mn);
         x.m = mn;
-        x.far = uniform(__any(fabsf(mn) > FAR && mn != NO_REF));
+        // (an infinite one has no way out, and its neighbours stay as they are)
+        x.far = uniform(__any(fabsf(mn) > FAR && fabsf(mn) < __builtin_inff() && mn != NO_REF));
         x.l *= f;
 #pragma unroll
         for (int t = 0; t < D / 16; t++)

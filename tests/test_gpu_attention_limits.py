@@ -94,3 +94,18 @@ def test_scores_below_fp32(tq, kind, seqs, Hq, Hkv):
     s.q = torch.full_like(s.q, 2.0 ** -120)
     masks = tree_masks(seqs, 6)
     check_alike(s, s.run(scale=1e-12, mask=pack(masks)), masks)
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_infinite_query_leaves_the_others_alone(tq, n):
+    """A row whose scores are infinite shares a wave with ordinary ones: those
+    keep their bits."""
+    s = Setup(tq, "q8_0", [(3000, n)], 4, 2, 128, 32, seed=4)
+    want = s.run()
+    q = s.q.clone()
+    q[1, 2] = float("inf")
+    q[n - 1, 1, 3] = -float("inf")
+    out = s.run(q=q)
+    keep = torch.ones((n, 4), dtype=torch.bool)
+    keep[1, 2] = keep[n - 1, 1] = False
+    assert torch.equal(out[keep.cuda()], want[keep.cuda()])
