@@ -59,6 +59,21 @@ SIGNATURES = {
     "tq_verify_draft_workspace_bytes": (SZ, [I64, I64]),
     "tq_verify_draft": (INT, [INT, P, I64, P, I64, I64, I64, P, P, P, I64, P, P, I64, P, P, P, P,
                               SZ, P]),
+    "tq_plan_step": (INT, [I64, P, P, P, P, I64, I64, I64, P, I64, P, I64, P, P, P, P, P, P, P]),
+    "tq_release_pages": (INT, [I64, P, P, P, I64, I64, P, I64, P, P, P, P]),
+    "tq_residual_norm": (INT, [INT, INT, P, I64, P, I64, I64, I64, INT, P, P, P, I64, I64, F32,
+                               F32, P, I64, P, I64, P, P, P]),
+    "tq_sample_workspace_bytes": (SZ, [I64, I64]),
+    "tq_sample": (INT, [INT, P, I64, I64, I64, P, P, P, P, P, P, P, SZ, P]),
+    "tq_sample_probs": (INT, [INT, P, I64, I64, I64, P, P, P, P, P, I64, P, SZ, P]),
+    "tq_cache_bounds": (INT, [INT, P, I64, I64, I64, I64, P, I64, I64, I64, P, P, I64, P, P, P]),
+    "tq_select_pages_width": (I64, [I64, I64, I64, I64, I64, I64]),
+    "tq_select_pages_workspace_bytes": (SZ, [I64, I64, I64]),
+    "tq_select_pages": (INT, [INT, P, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, I64,
+                              I64, P, P, I64, I64, I64, I64, I64, I64, P, P, P, SZ, P]),
+    "tq_tree_attention_heads": (INT, [INT, INT, P, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P,
+                                      I64, I64, I64, I64, P, P, P, I64, I64, I64, I64, F32, P, I64,
+                                      I64, P, SZ, P]),
 }
 
 

@@ -1,76 +1,7 @@
 // C ABI of the decode-step operators: host-side validation, then the launches
 // on the caller's stream, as in api.hip.
-#include <stdint.h>
+#include "api_checks.h"
 
-#include <cmath>
-
-#include "cache_layout.h"
-#include "tq_internal.h"
-
-namespace {
-
-constexpr int64_t MAX_TOKENS = int64_t(1) << 20;
-constexpr int64_t MAX_BATCH = 65535;
-constexpr int64_t MAX_HEADS = 1024;
-constexpr int64_t MAX_SLOTS = int64_t(1) << 31;
-// Positions of one sequence: key numbers plus a few steps stay below 2^31.
-constexpr int64_t MAX_POSITIONS = int64_t(1) << 30;
-constexpr int64_t MAX_PAGES = int64_t(1) << 26;
-constexpr int64_t MAX_STRIDE = int64_t(1) << 40;
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-int launch_status(hipError_t e) { return e == hipSuccess ? TQ_OK : TQ_E_LAUNCH; }
-bool valid_dtype(int t) { return t == TQ_F32 || t == TQ_BF16 || t == TQ_F16; }
-uintptr_t size_of(int dtype) { return dtype == TQ_F32 ? 4 : 2; }
-bool within(int64_t x, int64_t lo, int64_t hi) { return x >= lo && x <= hi; }
-
-bool valid_strides(int64_t ts, int64_t hs)
-{
-    return within(ts, 0, MAX_STRIDE) && within(hs, 0, MAX_STRIDE);
-}
-
-// An output's rows must be apart: heads inside a token, or tokens inside a head.
-bool apart(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t D)
-{
-    if (!valid_strides(ts, hs))
-        return false;
-    if (heads == 0)
-        return true;
-    const bool one_head = heads == 1, one_token = tokens <= 1;
-    if (one_head && one_token)
-        return true;
-    if (one_head)
-        return ts >= D;
-    if (one_token)
-        return hs >= D;
-    return (hs >= D && ts >= (heads - 1) * hs + D) || (ts >= D && hs >= (tokens - 1) * ts + D);
-}
-
-bool valid_cache(int64_t n_pages, int64_t page_size, int64_t kv_heads, int64_t D)
-{
-    return tq::cache_dim_ok(D) && tq::cache_page_ok(page_size) && within(kv_heads, 1, MAX_HEADS) &&
-           within(n_pages, 1, MAX_PAGES) && n_pages * page_size < MAX_SLOTS;
-}
-
-// The scratch region of a workspace of `bytes` bytes, or a status.
-int scratch_of(void *workspace, size_t bytes, size_t need, uint32_t **counters, void **scratch)
-{
-    *counters = nullptr;
-    *scratch = nullptr;
-    if (need == 0)
-        return TQ_OK;
-    if (!workspace)
-        return TQ_E_NULL;
-    if (!aligned(workspace, 256))
-        return TQ_E_ALIGN;
-    if (bytes < need)
-        return TQ_E_SHAPE;
-    *counters = (uint32_t *)workspace;
-    *scratch = (uint8_t *)workspace + TQ_NOALLOC_SCRATCH_BYTES;
-    return TQ_OK;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -170,15 +101,17 @@ size_t tq_tree_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t k
     return n ? TQ_NOALLOC_SCRATCH_BYTES + n : 0;
 }
 
-int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs,
-                      int64_t tokens, int64_t heads, int64_t kv_heads, int64_t D,
-                      const void *k_cache, const void *v_cache, int64_t n_pages,
-                      int64_t page_size, const int32_t *page_table, int64_t table_stride,
-                      int64_t table_pages, int64_t batch, const int32_t *ctx_lens,
-                      const int32_t *starts, const uint32_t *mask, int64_t mask_stride,
-                      int64_t mask_words, int64_t max_nodes, int64_t max_ctx, float scale,
-                      void *out, int64_t o_ts, int64_t o_hs, void *workspace,
-                      size_t workspace_bytes, hipStream_t stream)
+namespace {
+
+// table_head_stride 0: all key heads read the same pages.
+int attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs, int64_t tokens,
+              int64_t heads, int64_t kv_heads, int64_t D, const void *k_cache, const void *v_cache,
+              int64_t n_pages, int64_t page_size, const int32_t *page_table, int64_t table_stride,
+              int64_t table_head_stride, int64_t table_pages, int64_t batch,
+              const int32_t *ctx_lens, const int32_t *starts, const uint32_t *mask,
+              int64_t mask_stride, int64_t mask_words, int64_t max_nodes, int64_t max_ctx,
+              float scale, void *out, int64_t o_ts, int64_t o_hs, void *workspace,
+              size_t workspace_bytes, hipStream_t stream)
 {
     if (!tq::cache_type_ok(type) || (dtype != TQ_BF16 && dtype != TQ_F16))
         return TQ_E_TYPE;
@@ -186,6 +119,7 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
         heads % kv_heads || !within(tokens, 0, MAX_TOKENS) || !within(batch, 0, MAX_BATCH) ||
         !within(table_pages, 1, MAX_PAGES) || table_pages * page_size > MAX_POSITIONS ||
         !within(table_stride, batch > 1 ? table_pages : 0, MAX_STRIDE) ||
+        !within(table_head_stride, 0, MAX_STRIDE) ||
         !within(max_nodes, 1, MAX_TOKENS) || !within(max_ctx, 0, MAX_POSITIONS) ||
         !valid_strides(q_ts, q_hs) || !apart(o_ts, o_hs, tokens, heads, D) ||
         !(scale > 0.0f) || !std::isfinite(scale) ||
@@ -211,11 +145,45 @@ int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t 
     if (st != TQ_OK)
         return st;
     const tq::AttnArgs a{q, out, q_ts, q_hs, o_ts, o_hs, (const uint8_t *)k_cache,
-                         (const uint8_t *)v_cache, page_table, table_stride, ctx_lens, starts,
+                         (const uint8_t *)v_cache, page_table, table_stride, table_head_stride, ctx_lens, starts,
                          mask, mask_stride, n_pages, tokens, (int)table_pages,
                          tq::log2_of(page_size), (int)batch, (int)kv_heads,
                          (int)(heads / kv_heads), (int)max_nodes, (int)mask_words, dtype, scale};
     return launch_status(tq::launch_attention(type, (int)D, a, p, scratch, stream));
+}
+
+}  // namespace
+
+int tq_tree_attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs,
+                      int64_t tokens, int64_t heads, int64_t kv_heads, int64_t D,
+                      const void *k_cache, const void *v_cache, int64_t n_pages,
+                      int64_t page_size, const int32_t *page_table, int64_t table_stride,
+                      int64_t table_pages, int64_t batch, const int32_t *ctx_lens,
+                      const int32_t *starts, const uint32_t *mask, int64_t mask_stride,
+                      int64_t mask_words, int64_t max_nodes, int64_t max_ctx, float scale,
+                      void *out, int64_t o_ts, int64_t o_hs, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream)
+{
+    return attention(type, dtype, q, q_ts, q_hs, tokens, heads, kv_heads, D, k_cache, v_cache,
+                     n_pages, page_size, page_table, table_stride, 0, table_pages, batch, ctx_lens,
+                     starts, mask, mask_stride, mask_words, max_nodes, max_ctx, scale, out, o_ts,
+                     o_hs, workspace, workspace_bytes, stream);
+}
+
+int tq_tree_attention_heads(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs,
+                            int64_t tokens, int64_t heads, int64_t kv_heads, int64_t D,
+                            const void *k_cache, const void *v_cache, int64_t n_pages,
+                            int64_t page_size, const int32_t *page_tables, int64_t table_stride,
+                            int64_t table_head_stride, int64_t table_pages, int64_t batch,
+                            const int32_t *ctx_lens, const int32_t *starts, const uint32_t *mask,
+                            int64_t mask_stride, int64_t mask_words, int64_t max_nodes,
+                            int64_t max_ctx, float scale, void *out, int64_t o_ts, int64_t o_hs,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return attention(type, dtype, q, q_ts, q_hs, tokens, heads, kv_heads, D, k_cache, v_cache,
+                     n_pages, page_size, page_tables, table_stride, table_head_stride, table_pages,
+                     batch, ctx_lens, starts, mask, mask_stride, mask_words, max_nodes, max_ctx,
+                     scale, out, o_ts, o_hs, workspace, workspace_bytes, stream);
 }
 
 size_t tq_verify_draft_workspace_bytes(int64_t batch, int64_t vocab)

@@ -955,7 +955,7 @@ template <int CT, int D>
 __device__ __forceinline__ Place place_of(const AttnArgs &a, const Work &k)
 {
     Place c;
-    c.table = a.table + k.w.b * a.table_stride;
+    c.table = a.table + k.w.b * a.table_stride + k.w.h * a.table_head_stride;
     c.bytes = (int)chunk_bytes(CT, D, 1 << a.log_page);
     c.stride = (uint32_t)a.kv_heads * c.bytes;
     c.k = (uint64_t)a.kc + (uint32_t)(k.w.h * c.bytes);

@@ -423,8 +423,9 @@ struct AttnArgs {
     void *y;
     int64_t qts, qhs, yts, yhs;      // token and head strides, elements
     const uint8_t *kc, *vc;
-    const int32_t *table;            // [batch][table_pages] at row stride table_stride
-    int64_t table_stride;
+    const int32_t *table;            // [batch][table_pages] at row stride table_stride,
+    int64_t table_stride;            // or one for each key head, table_head_stride apart
+    int64_t table_head_stride;       // (0: all heads have the same)
     const int32_t *ctx, *starts;
     const uint32_t *mask;            // [tokens][mask_words] or null
     int64_t mask_stride;             // words
@@ -459,5 +460,90 @@ struct VerifyArgs {
 size_t verify_scratch_bytes(int64_t batch, int64_t vocab);
 hipError_t launch_verify(int dtype, const VerifyArgs &a, uint32_t *counters, void *scratch,
                          hipStream_t s);
+
+// A step's rows and pages from the requests' lengths.
+struct PlanArgs {
+    const int32_t *lens, *new_tokens, *owned;    // [batch]
+    int32_t *table;
+    int64_t table_stride, table_pages;
+    const int32_t *free_pages, *free_count;
+    int64_t free_capacity, batch, tokens;
+    int log_page;
+    int32_t *starts, *positions, *slots, *new_lens, *new_owned, *free_left;
+};
+hipError_t launch_plan(const PlanArgs &a, hipStream_t s);
+
+struct ReleaseArgs {
+    const int32_t *done, *owned;                 // [batch]
+    int32_t *table;
+    int64_t table_stride, table_pages;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int64_t free_capacity, batch;
+    int32_t *new_owned, *free_left;
+};
+hipError_t launch_release(const ReleaseArgs &a, hipStream_t s);
+
+// Norms around a block with gate and residual scale.
+struct ResNormArgs {
+    const void *y, *x;
+    int64_t y_ts, x_ts;
+    int y_dtype, w_dtype;
+    const void *post, *pre, *gate;               // of w_dtype, or null
+    int64_t gate_ts, gate_es;                    // token and element strides of the gate
+    float scale, eps;
+    int64_t tokens;
+    int n;
+    void *x_out, *z;                             // z, or q and d
+    int64_t xo_ts, z_ts;
+    int8_t *q;
+    uint16_t *d;
+};
+hipError_t launch_residual_norm(int dtype, const ResNormArgs &a, hipStream_t s);
+
+// Tokens from logits; probs: the distributions instead.
+struct SampleArgs {
+    const void *logits;
+    int64_t stride, rows, vocab;
+    int dtype, bits;                             // bits: weights are multiples of 2^-bits
+    const float *temperature, *top_p, *min_p;    // [rows], or null
+    const int32_t *top_k;
+    const float *u;
+    int32_t *tokens;
+    float *probs;
+    int64_t probs_stride;
+};
+size_t sample_scratch_bytes(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const SampleArgs &a, void *scratch, hipStream_t s);
+
+// Bounds of a page's keys: [page][kv head][D / 32] blocks of 32 codes of the
+// largest and 32 of the smallest, and a scale each.
+struct BoundsArgs {
+    const uint8_t *k_cache;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *begin, *end;                  // [batch]: positions that are new
+    int8_t *codes;
+    uint16_t *scales;
+    int64_t pages;
+    int table_pages, log_page, batch, kv_heads;
+};
+hipError_t launch_bounds(int cache_type, int D, const BoundsArgs &a, int64_t max_new, hipStream_t s);
+
+struct SelectArgs {
+    const void *q;
+    int64_t qts, qhs, tokens;
+    const int8_t *codes;
+    const uint16_t *scales;
+    int64_t pages;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *ctx, *starts;
+    int table_pages, log_page, batch, kv_heads, group, max_nodes, dtype;
+    int first, last, keep, width;
+    int32_t *out, *ctx_out;                      // [batch][kv_heads][width], [batch]
+};
+size_t select_scratch_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages);
+hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, void *scratch, hipStream_t s);
 
 }  // namespace tq

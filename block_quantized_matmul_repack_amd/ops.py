@@ -628,6 +628,18 @@ def cache_read(ctype, k_cache, v_cache, slots, kv_heads, D, page_size, dtype=tor
     return k, v
 
 
+def _check_table(name, t, dev, kv_heads=0):
+    """A page table int32 [batch, pages], or with kv_heads [batch, kv_heads,
+    pages], with contiguous rows on device dev; returns batch, pages and the
+    strides before the last."""
+    dims = t.dim()
+    shape, strides = t.shape, t.stride()
+    if (dims != 2 and (dims != 3 or shape[1] != kv_heads)) or t.dtype is not torch.int32 or \
+            t.get_device() != dev or (shape[-1] > 1 and strides[-1] != 1):
+        _refuse(name, "page_table", f"int32 [batch, pages], rows contiguous, on device {dev}", t)
+    return shape[0], shape[-1], strides[:-1]
+
+
 _ATTN_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -637,18 +649,14 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
     that already holds their keys and values.  Sequence b: rows starts[b] ..
     starts[b+1]-1 of q, pages page_table[b] (int32 [B, pages]), ctx_lens[b]
     tokens before the new ones.  mask: int32 [T, words], bit j of a row = new
-    token j of the sequence is seen (None: the chain, j <= i).  max_nodes and
-    max_ctx bound the new and the cached tokens of a sequence; they default
+    token j of the sequence is seen (None: the chain, j <= i).  page_table may
+    be [B, kv_heads, pages], a table for each key head, as select_pages gives
+    (then with its ctx_lens).  max_nodes and max_ctx bound the new and the cached tokens of a sequence; they default
     to all rows of q and all of the table.  scale defaults to D ** -0.5."""
     name = "tq_tree_attention"
     shape, q_ts, q_hs, dev, code = _heads_of(name, "q", q, _ATTN_DTYPES)
     T, Hq, D = shape
-    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or \
-            page_table.get_device() != dev or (page_table.shape[1] > 1 and
-                                               page_table.stride(1) != 1):
-        _refuse(name, "page_table", f"int32 [batch, pages], rows contiguous, on device {dev}",
-                page_table)
-    B, width = page_table.shape
+    B, width, t_stride = _check_table(name, page_table, dev, kv_heads)
     _check_index(name, "ctx_lens", ctx_lens, B, dev)
     _check_index(name, "starts", starts, B + 1, dev)
     n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D, dev)
@@ -672,12 +680,12 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
         o_ts, o_hs = _check_heads(name, "out", out, (out.shape[0], Hq, D), q.dtype, dev)
     st = _stream_of(dev)
     need = _size_query("tq_tree_attention_workspace_bytes", B, Hq, kv_heads, D, max_nodes, max_ctx)
+    entry = lib().tq_tree_attention if page_table.dim() == 2 else lib().tq_tree_attention_heads
     status = _with_workspace(
-        lib().tq_tree_attention, q.device, st, need, ctype, code, q.data_ptr(), q_ts, q_hs, T, Hq,
-        kv_heads, D, k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page_size,
-        page_table.data_ptr(), page_table.stride(0), width, B, ctx_lens.data_ptr(),
-        starts.data_ptr(), mp, stride, words, max_nodes, max_ctx,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), o_ts, o_hs)
+        entry, q.device, st, need, ctype, code, q.data_ptr(), q_ts, q_hs, T, Hq, kv_heads, D,
+        k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page_size, page_table.data_ptr(),
+        *t_stride, width, B, ctx_lens.data_ptr(), starts.data_ptr(), mp, stride, words, max_nodes,
+        max_ctx, D ** -0.5 if scale is None else scale, out.data_ptr(), o_ts, o_hs)
     if status:
         check(status, name)
     return out
@@ -736,6 +744,293 @@ def verify_draft(target, tokens, starts, uniforms, final_uniforms, draft=None, p
     if status:
         check(status, name)
     return accepted, out_tokens, nodes
+
+
+def plan_step(lens, new_tokens, owned, page_table, free_pages, free_count, page_size, tokens):
+    """Rows, positions and cache slots of a step's new tokens, with the pages that
+    they need taken off the free stack, all on the GPU.  lens, new_tokens, owned
+    int32 [B]: tokens cached, tokens to come and pages owned of each request;
+    page_table int32 [B, pages]: its new pages are written in place (-1 where
+    none was left); free_pages int32, free_count int32 [1]: the stack; tokens:
+    rows to fill (at least the sum of new_tokens; the rest get position 0 and slot
+    -1).  Returns int32 (starts [B + 1], positions [tokens], slots [tokens],
+    new lens [B], new owned [B], new free_count [1]: below 0 if pages lacked)."""
+    name = "tq_plan_step"
+    dev = page_table.get_device()
+    if dev < 0:
+        _refuse(name, "page_table", "int32 on the GPU", page_table)
+    if page_table.dim() != 2:
+        _refuse(name, "page_table", "int32 [batch, pages]", page_table)
+    B, width, strides = _check_table(name, page_table, dev)
+    for what, t, n in (("lens", lens, B), ("new_tokens", new_tokens, B), ("owned", owned, B),
+                       ("free_pages", free_pages, 0), ("free_count", free_count, 1)):
+        _check_index(name, what, t, n, dev)
+    if not 0 <= tokens <= 1 << 20:
+        raise TiledqError(f"{name}: tokens must be in 0 .. 2^20, got {tokens}")
+    # one allocation; parts begin at multiples of four elements
+    sizes = (B + 1, tokens, tokens, B, B, 1)
+    at = [0]
+    for n in sizes:
+        at.append(at[-1] + (n + 3 & ~3))
+    buf = torch.empty(at[-1], dtype=torch.int32, device=page_table.device)
+    base = buf.data_ptr()
+    status = lib().tq_plan_step(
+        B, lens.data_ptr(), new_tokens.data_ptr(), owned.data_ptr(), page_table.data_ptr(),
+        strides[0], width, page_size, free_pages.data_ptr(), free_pages.shape[0],
+        free_count.data_ptr(), tokens, *(base + 4 * a for a in at[:-1]), _stream_of(dev))
+    if status:
+        check(status, name)
+    return tuple(buf[a:a + n] for a, n in zip(at, sizes))
+
+
+def release_pages(done, owned, page_table, free_pages, free_count):
+    """The pages of requests with done [B] (int32, not 0) back on the free stack:
+    free_pages and page_table (their entries become -1) are written in place.
+    Returns int32 (new owned [B], new free_count [1])."""
+    name = "tq_release_pages"
+    dev = page_table.get_device()
+    if dev < 0:
+        _refuse(name, "page_table", "int32 on the GPU", page_table)
+    if page_table.dim() != 2:
+        _refuse(name, "page_table", "int32 [batch, pages]", page_table)
+    B, width, strides = _check_table(name, page_table, dev)
+    for what, t, n in (("done", done, B), ("owned", owned, B), ("free_pages", free_pages, 0),
+                       ("free_count", free_count, 1)):
+        _check_index(name, what, t, n, dev)
+    new_owned = torch.empty(B, dtype=torch.int32, device=page_table.device)
+    left = torch.empty(1, dtype=torch.int32, device=page_table.device)
+    status = lib().tq_release_pages(
+        B, done.data_ptr(), owned.data_ptr(), page_table.data_ptr(), strides[0], width,
+        free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), new_owned.data_ptr(),
+        left.data_ptr(), _stream_of(dev))
+    if status:
+        check(status, name)
+    return new_owned, left
+
+
+def _rows_of(name, what, t, shape, dtype, dev):
+    """The row stride of t, `shape` (2-D) of dtype with contiguous rows on dev."""
+    if t.shape != shape or t.dtype is not dtype or (shape[1] > 1 and t.stride(1) != 1) or \
+            t.get_device() != dev:
+        _refuse(name, what, f"{dtype} {tuple(shape)} with contiguous rows on device {dev}", t)
+    return t.stride(0)
+
+
+def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6,
+                  quantize=False, x_out=None, z_out=None):
+    """x' = scale * x + gate * p and z, in one pass: p is y [T, N] (fp32 / bf16 /
+    fp16), normed (RMS) and times post_weight [N] if that is given; z is x' (of
+    x's type), normed and times pre_weight [N] if given, in x's type or, with
+    quantize, as the int8 activations (q [T, N], d [T, N/32]) that matmul takes.
+    gate: [N], [T, N], [T, 1] or [1], of the weights' type.  x_out may be x.
+    Returns (x', z) or (x', (q, d))."""
+    name = "tq_residual_norm"
+    code = _DTYPES.get(x.dtype)
+    dev = x.get_device()
+    if x.dim() != 2 or code is None or dev < 0 or (x.shape[1] > 1 and x.stride(1) != 1):
+        _refuse(name, "x", "[tokens, N] fp32, bf16 or fp16 with contiguous rows", x)
+    shape = x.shape
+    T, N = shape
+    ycode = _DTYPES.get(y.dtype)
+    if ycode is None or y.dim() != 2:
+        _refuse(name, "y", f"{tuple(shape)} fp32, bf16 or fp16", y)
+    y_ts = _rows_of(name, "y", y, shape, y.dtype, dev)
+    wtype = None
+    ptr = [None, None, None]
+    for i, (what, w) in enumerate((("post_weight", post_weight), ("pre_weight", pre_weight),
+                                   ("gate", gate))):
+        if w is None:
+            continue
+        if wtype is None:
+            wtype = w.dtype
+        if w.dtype is not wtype or wtype not in _DTYPES or w.get_device() != dev or \
+                (i < 2 and (w.dim() != 1 or w.shape[0] != N or not w.is_contiguous())):
+            _refuse(name, what, f"contiguous fp32, bf16 or fp16 [{N}], the weights and the gate of "
+                                f"one type, on device {dev}", w)
+        ptr[i] = w.data_ptr()
+    gate_ts = gate_es = 0
+    if gate is not None:
+        dims, gs = gate.dim(), gate.shape
+        if dims not in (1, 2) or gs[-1] not in (1, N) or (dims == 2 and gs[0] not in (1, T)) or \
+                (gs[-1] > 1 and gate.stride(-1) not in (0, 1)):
+            _refuse(name, "gate", f"[{N}], [{T}, {N}], [{T}, 1] or [1] with contiguous rows", gate)
+        gate_es = gate.stride(-1) if gs[-1] > 1 else 0
+        gate_ts = gate.stride(0) if dims == 2 and gs[0] > 1 else 0
+    if x_out is None:
+        x_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        xo_ts = N
+    else:
+        xo_ts = _rows_of(name, "x_out", x_out, shape, x.dtype, dev)
+    zp = qp = dp = None
+    z_ts = 0
+    if quantize:
+        if z_out is None:
+            z_out = (torch.empty(shape, dtype=torch.int8, device=x.device),
+                     torch.empty((T, N // 32), dtype=torch.float16, device=x.device))
+        q, d = z_out
+        if q.shape != shape or q.dtype is not torch.int8 or q.get_device() != dev or \
+                not q.is_contiguous():
+            _refuse(name, "q", f"contiguous int8 {tuple(shape)} on device {dev}", q)
+        if d.shape != (T, N // 32) or d.dtype is not torch.float16 or d.get_device() != dev or \
+                not d.is_contiguous():
+            _refuse(name, "d", f"contiguous float16 {(T, N // 32)} on device {dev}", d)
+        qp, dp = q.data_ptr(), d.data_ptr()
+    else:
+        if z_out is None:
+            z_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+            z_ts = N
+        else:
+            z_ts = _rows_of(name, "z_out", z_out, shape, x.dtype, dev)
+        zp = z_out.data_ptr()
+    status = lib().tq_residual_norm(
+        code, ycode, y.data_ptr(), y_ts, x.data_ptr(), x.stride(0), T, N,
+        _DTYPES.get(wtype, code), *ptr, gate_ts, gate_es, scale, eps, x_out.data_ptr(), xo_ts, zp,
+        z_ts, qp, dp, _stream_of(dev))
+    if status:
+        check(status, name)
+    return x_out, z_out
+
+
+_SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32),
+             ("min_p", torch.float32))
+
+
+def _sample_args(name, logits, settings):
+    code = _DTYPES.get(logits.dtype)
+    dev = logits.get_device()
+    if logits.dim() != 2 or code is None or dev < 0 or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _refuse(name, "logits", "[rows, vocab] fp32, bf16 or fp16 with contiguous rows", logits)
+    N, V = logits.shape
+    ptr = []
+    for (what, dtype), t in zip(_SETTINGS, settings):
+        if t is not None and (t.dtype is not dtype or t.dim() != 1 or t.shape[0] < N or
+                              t.get_device() != dev or not t.is_contiguous()):
+            _refuse(name, what, f"contiguous {dtype}, 1-D, >= {N} elements, on device {dev}", t)
+        ptr.append(None if t is None else t.data_ptr())
+    return code, dev, N, V, ptr
+
+
+def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None):
+    """Tokens int32 [N] drawn from logits [N, V] (fp32 / bf16 / fp16) with
+    uniforms fp32 [N].  Settings of each row, [N] each or None: temperature, top_p,
+    min_p fp32, top_k int32 (tq_sample says what they keep).  -1 for a row of
+    nothing above -infinity."""
+    name = "tq_sample"
+    code, dev, N, V, ptr = _sample_args(name, logits, (temperature, top_k, top_p, min_p))
+    if uniforms.dtype is not torch.float32 or uniforms.dim() != 1 or uniforms.shape[0] < N or \
+            uniforms.get_device() != dev or not uniforms.is_contiguous():
+        _refuse(name, "uniforms", f"contiguous float32, 1-D, >= {N} elements, on device {dev}",
+                uniforms)
+    tokens = torch.empty(N, dtype=torch.int32, device=logits.device)
+    st = _stream_of(dev)
+    need = _size_query("tq_sample_workspace_bytes", N, V)
+    status = _with_workspace(lib().tq_sample, logits.device, st, need, code, logits.data_ptr(),
+                             logits.stride(0), N, V, *ptr, uniforms.data_ptr(), tokens.data_ptr())
+    if status:
+        check(status, name)
+    return tokens
+
+
+def sample_probs(logits, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+    """The distributions fp32 [N, V] that sample draws from: a target or draft of
+    verify_draft."""
+    name = "tq_sample_probs"
+    code, dev, N, V, ptr = _sample_args(name, logits, (temperature, top_k, top_p, min_p))
+    if out is None:
+        out = torch.empty((N, V), dtype=torch.float32, device=logits.device)
+    else:
+        _rows_of(name, "out", out, logits.shape, torch.float32, dev)
+    st = _stream_of(dev)
+    need = _size_query("tq_sample_workspace_bytes", N, V)
+    status = _with_workspace(lib().tq_sample_probs, logits.device, st, need, code,
+                             logits.data_ptr(), logits.stride(0), N, V, *ptr, out.data_ptr(),
+                             out.stride(0))
+    if status:
+        check(status, name)
+    return out
+
+
+def _check_bounds(name, codes, scales, dev):
+    """Bounds of pages: codes int8 [n_pages, kv_heads, D/32, 2, 32], scales fp16
+    [n_pages, kv_heads, D/32]; returns n_pages, kv_heads, D."""
+    shape = codes.shape
+    if len(shape) != 5 or shape[3:] != (2, 32) or codes.dtype is not torch.int8 or \
+            codes.get_device() != dev or not codes.is_contiguous():
+        _refuse(name, "codes", f"contiguous int8 [pages, heads, D/32, 2, 32] on device {dev}", codes)
+    if scales.shape != shape[:3] or scales.dtype is not torch.float16 or \
+            scales.get_device() != dev or not scales.is_contiguous():
+        _refuse(name, "scales", f"contiguous float16 {tuple(shape[:3])} on device {dev}", scales)
+    return shape[0], shape[1], 32 * shape[2]
+
+
+def cache_bounds(ctype, k_cache, page_table, begin, end, kv_heads, D, page_size, codes, scales,
+                 max_new=None):
+    """The largest and smallest keys, codes int8 [n_pages, kv_heads, D/32, 2, 32]
+    with scales fp16 [n_pages, kv_heads, D/32], of every page that holds a position
+    in [begin[b], end[b]) (int32 [B]) of sequence b, over its positions below
+    end[b], brought up to date in place; after cache_write has stored them.
+    max_new bounds end - begin; it defaults to all of the table."""
+    name = "tq_cache_bounds"
+    dev = page_table.get_device()
+    if dev < 0 or page_table.dim() != 2:
+        _refuse(name, "page_table", "int32 [batch, pages] on the GPU", page_table)
+    B, width, strides = _check_table(name, page_table, dev)
+    _check_index(name, "begin", begin, B, dev)
+    _check_index(name, "end", end, B, dev)
+    n_pages = _cache_pages(name, ctype, k_cache, k_cache, page_size, kv_heads, D, dev)
+    if _check_bounds(name, codes, scales, dev) != (n_pages, kv_heads, D):
+        raise TiledqError(f"{name}: codes {tuple(codes.shape)} are not those of {n_pages} pages of "
+                          f"{kv_heads} heads of {D}")
+    status = lib().tq_cache_bounds(
+        ctype, k_cache.data_ptr(), n_pages, page_size, kv_heads, D, page_table.data_ptr(),
+        strides[0], width, B, begin.data_ptr(), end.data_ptr(),
+        width * page_size if max_new is None else max_new, codes.data_ptr(), scales.data_ptr(),
+        _stream_of(dev))
+    if status:
+        check(status, name)
+
+
+def select_pages(q, codes, scales, page_table, ctx_lens, starts, page_size, keep, first=1, last=1,
+                 max_nodes=None, max_ctx=None):
+    """The pages that the new tokens q [T, Hq, D] (bf16 / fp16) read of each
+    sequence and key head, from the bounds that cache_bounds keeps: the first
+    `first`, all from `last` before the new tokens' on, and the `keep` best of
+    those between.  Sequences as in tree_attention.  Returns int32 (page tables
+    [B, kv_heads, pages], -1 behind the last; cached tokens on them [B]), which
+    tree_attention takes."""
+    name = "tq_select_pages"
+    shape, q_ts, q_hs, dev, code = _heads_of(name, "q", q, _ATTN_DTYPES)
+    T, Hq, D = shape
+    n_pages, Hk, Db = _check_bounds(name, codes, scales, dev)
+    if Db != D:
+        raise TiledqError(f"{name}: the bounds are of heads of {Db}, q of {D}")
+    if page_table.dim() != 2:
+        _refuse(name, "page_table", "int32 [batch, pages]", page_table)
+    B, table_pages, strides = _check_table(name, page_table, dev)
+    _check_index(name, "ctx_lens", ctx_lens, B, dev)
+    _check_index(name, "starts", starts, B + 1, dev)
+    if max_nodes is None:
+        max_nodes = max(T, 1)
+    if max_ctx is None:
+        max_ctx = table_pages * page_size
+    width = _size_query("tq_select_pages_width", page_size, table_pages, first, last, keep,
+                        max_nodes)
+    if width == 0:
+        raise TiledqError(f"{name}: page_size {page_size}, first {first}, last {last}, keep {keep} "
+                          f"or max_nodes {max_nodes} out of range")
+    tables = torch.empty((B, Hk, width), dtype=torch.int32, device=q.device)
+    ctx = torch.empty(B, dtype=torch.int32, device=q.device)
+    st = _stream_of(dev)
+    need = _size_query("tq_select_pages_workspace_bytes", B, Hk, table_pages)
+    status = _with_workspace(
+        lib().tq_select_pages, q.device, st, need, code, q.data_ptr(), q_ts, q_hs, T, Hq, Hk, D,
+        codes.data_ptr(), scales.data_ptr(), n_pages, page_size, page_table.data_ptr(), strides[0],
+        table_pages, B, ctx_lens.data_ptr(), starts.data_ptr(), max_nodes, max_ctx, first, last,
+        keep, width, tables.data_ptr(), ctx.data_ptr())
+    if status:
+        check(status, name)
+    return tables, ctx
 
 
 STREAM_READ_BLOCKS = 2048       # TQ_STREAM_READ_BLOCKS: words of the sink

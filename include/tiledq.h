@@ -565,6 +565,156 @@ int tq_verify_draft(int dtype, const void *target, int64_t target_stride,
                     int64_t width, int32_t *accepted, int32_t *out_tokens, int32_t *out_nodes,
                     void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- The rest of a serving step: pages, norms, sampling, pages worth reading ----
+ *
+ * tq_plan_step: page tables, positions and cache slots of a step's new tokens,
+ * from the requests' lengths, which stay on the device.  Request b has lens[b]
+ * tokens cached, owns the first owned[b] pages of its row of page_table, and
+ * brings new_tokens[b] (0: none this step).  Its rows are starts[b] ..
+ * starts[b+1]-1 (running sums of new_tokens; tokens past the `tokens` rows there
+ * are, in that order, are left out); row starts[b] + i has position lens[b] + i
+ * and that position's slot (page * page_size + position in it).  Pages that
+ * positions below lens[b] + new_tokens[b] need beyond the owned ones come off
+ * the top of the stack free_pages[0 .. *free_count - 1], requests in order, and
+ * are written to the table's row; where none is left, or past the row's
+ * table_pages, a table entry and a slot are -1 (tq_cache_write skips those).
+ *   positions, slots : int32 [tokens]; rows past starts[batch]: 0 and -1.
+ *   new_lens  : lens + the new tokens;  new_owned : pages owned now.
+ *   free_left : the stack's new count; below 0, as many pages were missing.
+ * The state (lens, owned, free_count) is read and the next one written apart,
+ * so the two must not overlap (TQ_E_SHAPE).  Numbers below 0 count as 0, lens
+ * past 2^30 as 2^30.  A request that gives back cached tokens (drafts that were
+ * refused) lowers its length and keeps its pages.
+ * tq_release_pages: the pages of requests with done[b] != 0 go back on the stack
+ * (free_pages from *free_count on, at most free_capacity in all), their table
+ * entries become -1 and new_owned 0; the others stay.  free_left as above.
+ * Deterministic.  Domain: batch 0..65535, tokens 0..2^20, page_size as below,
+ * table_pages * page_size up to 2^30, free_capacity 0..2^26. */
+int tq_plan_step(int64_t batch, const int32_t *lens, const int32_t *new_tokens,
+                 const int32_t *owned, int32_t *page_table, int64_t table_stride,
+                 int64_t table_pages, int64_t page_size, const int32_t *free_pages,
+                 int64_t free_capacity, const int32_t *free_count, int64_t tokens,
+                 int32_t *starts, int32_t *positions, int32_t *slots, int32_t *new_lens,
+                 int32_t *new_owned, int32_t *free_left, hipStream_t stream);
+int tq_release_pages(int64_t batch, const int32_t *done, const int32_t *owned, int32_t *page_table,
+                     int64_t table_stride, int64_t table_pages, int32_t *free_pages,
+                     int64_t free_capacity, const int32_t *free_count, int32_t *new_owned,
+                     int32_t *free_left, hipStream_t stream);
+
+/* tq_residual_norm: the norm after a block, its gate and residual scale, and
+ * the norm before the next block, one pass.  For each token's row of N:
+ *   p  = y * post_weight / sqrt(mean(y^2) + eps)   (post_weight NULL: p = y)
+ *   x' = scale * x + gate * p, rounded to dtype    (gate NULL: 1)
+ *   z  = x' * pre_weight / sqrt(mean(x'^2) + eps)  (pre_weight NULL: z = x')
+ * Statistics and products in fp32; z is rounded once.
+ *   y       : device, y_dtype, [tokens][N] at row stride y_ts (the products'
+ *             fp32 outputs, or 16-bit ones).
+ *   x       : of dtype at x_ts;  x_out : at xo_ts; may be x itself (same stride).
+ *   post_weight, pre_weight : [N] of w_dtype;  gate : of w_dtype, element i of
+ *             token t at gate[t * gate_ts + i * gate_es], gate_es 0 or 1 (gate_ts
+ *             0: one for all tokens; gate_es 0: one number a token).
+ *   z       : of dtype at row stride z_ts, or NULL and instead
+ *   q, d    : int8 [tokens][N] (4-byte aligned) and fp16 bits [tokens][N/32], z
+ *             by tq_quantize_act's rule (from its fp32 value), for tq_matmul.
+ * Outputs must not overlap inputs otherwise.  Domain: N 1..32768 (with q: a
+ * multiple of 32), tokens 0..2^20, scale finite. */
+int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const void *x,
+                     int64_t x_ts, int64_t tokens, int64_t N, int w_dtype, const void *post_weight,
+                     const void *pre_weight, const void *gate, int64_t gate_ts, int64_t gate_es,
+                     float scale, float eps, void *x_out, int64_t xo_ts, void *z, int64_t z_ts,
+                     int8_t *q, uint16_t *d, hipStream_t stream);
+
+/* Sampling from logits with given uniform numbers.  Each row has settings of its
+ * own, device arrays [rows] or NULL (off): temperature T (NULL: 1; not above 0:
+ * the first of the largest logits), top_k (not above 0: off), top_p (1 and above:
+ * off), min_p (not above 0: off; above 1 as 1).  Weights w_i = exp((x_i - max x) /
+ * T) in whole multiples of 2^-s, fp64 before that rounding; s = min(45, 62 -
+ * ceil(log2 vocab)).  In the order of falling x (ties: the lower index first)
+ * top_k keeps the first k, top_p the shortest prefix of those that holds top_p of
+ * their sum (the first element at least), min_p what weighs min_p of the
+ * largest or more.
+ *   tq_sample : tokens[r] = the first index whose running sum (in index order) of
+ *     kept weights exceeds uniforms[r] (in [0, 1)) times their sum; -1 for a row
+ *     without a logit above -infinity.
+ *   tq_sample_probs : probs[r][i] = the kept weights over their sum, fp32 (zeros
+ *     for such a row): what tq_verify_draft takes as target or draft.
+ * A logit that is NaN or -infinity weighs nothing; at +infinity all such share the
+ * row.  Sums are exact, so results do not depend on any order: deterministic.
+ *   logits : of dtype, rows of vocab at row stride `stride` elements (0: one row
+ *     for all).
+ *   workspace : as tq_tree_attention's, tq_sample_workspace_bytes() (0: NULL will
+ *     do).
+ * Domain: rows 0..2^20, vocab 1..2^27, rows * vocab below 2^34. */
+size_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab);
+int tq_sample(int dtype, const void *logits, int64_t stride, int64_t rows, int64_t vocab,
+              const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, const float *uniforms, int32_t *tokens, void *workspace,
+              size_t workspace_bytes, hipStream_t stream);
+int tq_sample_probs(int dtype, const void *logits, int64_t stride, int64_t rows, int64_t vocab,
+                    const float *temperature, const int32_t *top_k, const float *top_p,
+                    const float *min_p, float *probs, int64_t probs_stride, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+
+/* Attention over the pages worth reading.  tq_cache_bounds keeps, for each page
+ * and key head, the largest and the smallest key of each channel; tq_select_pages
+ * picks from them the pages of each sequence and key head that a step reads;
+ * tq_tree_attention_heads attends over those.
+ *
+ * Bounds: codes int8 [n_pages][kv_heads][D/32][2][32] (largest, then smallest),
+ * scales fp16 bits [n_pages][kv_heads][D/32]: per 32 channels one Q8_0 block
+ * (tq_quantize_act's rule) of the 64 numbers, of the keys as the cache holds them.
+ * tq_cache_bounds writes them for every page that holds a position in [begin[b],
+ * end[b]) of sequence b, over all of the page's positions below end[b]; to be
+ * called once tq_cache_write has stored those.  Other pages' stay as they were.
+ *   max_new : at least every end[b] - begin[b]; pages past it are not done.
+ *   Table entries outside the cache are passed over; a page must not lie in two
+ *   ranges of one call unless both give the same.
+ *
+ * tq_select_pages: with T new tokens behind ctx_lens[b] cached ones (as in
+ * tq_tree_attention, T at most max_nodes), sequence b has ceil((ctx + T) /
+ * page_size) pages.  The first `first`, and all from `last` before page ctx /
+ * page_size on, are always read; of those between, the `keep` with the highest
+ * scores for a key head (all if no more).  A page's score is the largest, over the
+ * query rows of the head (new tokens x heads / kv_heads), of sum_d max(q_d hi_d,
+ * q_d lo_d) with q quantized in blocks of 32 as the bounds are (its scale in fp32;
+ * a block of nothing above 2^-100 * 127 counts as zeros), sums in fp64, rounded
+ * once to fp32; equal scores: the earlier page.  A page outside the cache comes last.
+ *   tables : int32 [batch][kv_heads][width]: the pages in order, then -1; width at
+ *     least tq_select_pages_width() (0: invalid arguments).
+ *   ctx_out : int32 [batch], the cached tokens on them: ctx_lens less whole pages.
+ *   max_ctx : shapes the launch only.
+ *   workspace : as tq_tree_attention's, tq_select_pages_workspace_bytes().
+ * tq_tree_attention_heads: tq_tree_attention with a page table for each key head,
+ * table_head_stride entries apart (0: the same for all); for selected pages pass
+ * `tables`, table_pages = width and ctx_out.  Mask bits count new tokens, so a
+ * tree's mask serves as it is.
+ * Deterministic.  Domain: as tq_tree_attention's; batch * kv_heads up to 2^20;
+ * first, last, keep 0..2^26. */
+int tq_cache_bounds(int type, const void *k_cache, int64_t n_pages, int64_t page_size,
+                    int64_t kv_heads, int64_t D, const int32_t *page_table, int64_t table_stride,
+                    int64_t table_pages, int64_t batch, const int32_t *begin, const int32_t *end,
+                    int64_t max_new, int8_t *codes, uint16_t *scales, hipStream_t stream);
+int64_t tq_select_pages_width(int64_t page_size, int64_t table_pages, int64_t first, int64_t last,
+                              int64_t keep, int64_t max_nodes);
+size_t tq_select_pages_workspace_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages);
+int tq_select_pages(int dtype, const void *q, int64_t q_ts, int64_t q_hs, int64_t tokens,
+                    int64_t heads, int64_t kv_heads, int64_t D, const int8_t *codes,
+                    const uint16_t *scales, int64_t n_pages, int64_t page_size,
+                    const int32_t *page_table, int64_t table_stride, int64_t table_pages,
+                    int64_t batch, const int32_t *ctx_lens, const int32_t *starts,
+                    int64_t max_nodes, int64_t max_ctx, int64_t first, int64_t last, int64_t keep,
+                    int64_t width, int32_t *tables, int32_t *ctx_out, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+int tq_tree_attention_heads(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs,
+                            int64_t tokens, int64_t heads, int64_t kv_heads, int64_t D,
+                            const void *k_cache, const void *v_cache, int64_t n_pages,
+                            int64_t page_size, const int32_t *page_tables, int64_t table_stride,
+                            int64_t table_head_stride, int64_t table_pages, int64_t batch,
+                            const int32_t *ctx_lens, const int32_t *starts, const uint32_t *mask,
+                            int64_t mask_stride, int64_t mask_words, int64_t max_nodes,
+                            int64_t max_ctx, float scale, void *out, int64_t o_ts, int64_t o_hs,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Which HIP graph capture `stream` is part of: *id becomes 0 outside one, else
  * a number that no other capture of the process has.  For callers that keep a
  * workspace: one allocated and cleared inside a capture belongs to its graph,
