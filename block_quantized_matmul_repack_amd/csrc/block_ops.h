@@ -22,6 +22,11 @@ template <int CTRL, int ROWS> __device__ __forceinline__ float dpp_bits(float x)
     return __builtin_bit_cast(float, dpp_bits<CTRL, ROWS>(__builtin_bit_cast(uint32_t, x)));
 }
 
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_bits(double x)
+{
+    return __builtin_bit_cast(double, dpp_bits<CTRL, ROWS>(__builtin_bit_cast(uint64_t, x)));
+}
+
 // Running sum over the lanes of a wave: shifts by 1, 2, 4, 8 in each row of 16
 // lanes, then the last lane of a row added to the rows behind it.  Lanes that a
 // step brings nothing to add 0.
@@ -50,6 +55,11 @@ __device__ __forceinline__ uint64_t lane_value(uint64_t x, int k)
 __device__ __forceinline__ float lane_value(float x, int k)
 {
     return __builtin_bit_cast(float, lane_value(__builtin_bit_cast(uint32_t, x), k));
+}
+
+__device__ __forceinline__ double lane_value(double x, int k)
+{
+    return __builtin_bit_cast(double, lane_value(__builtin_bit_cast(uint64_t, x), k));
 }
 
 template <typename T> __device__ __forceinline__ T wave_sum(T v)
