@@ -67,6 +67,14 @@ template <typename T> __device__ __forceinline__ T wave_sum(T v)
     return lane_value(scan_wave(v), 63);
 }
 
+// Largest over the lanes.
+__device__ __forceinline__ float wave_max(float v)
+{
+    for (int m = 1; m < 64; m <<= 1)
+        v = fmaxf(v, __shfl_xor(v, m));
+    return v;
+}
+
 // Running sum over a workgroup of WAVES waves, before this thread, and the sum
 // of all.  `lds` holds WAVES values; it may be used again after the next barrier
 // that all threads pass.

@@ -20,37 +20,43 @@ namespace {
 constexpr int WAVES = 16, THREADS = 64 * WAVES;
 constexpr int DIGITS = 256;
 
+// Bins of the exponent (see k_bins): 60 to one of it.
+constexpr float BIN_RATE = 60.0f;
+
 // The settings of a row.
 struct Setting {
-    double rate;                                 // log2(e) / T; 0 or less: the likeliest token
+    double rate;                                 // log2(e) / T; below 0: the likeliest token
     double p;                                    // >= 1: off
     uint64_t min_w;                              // the least weight that min-p keeps
-    int64_t k;                                   // <= 0: off
-    float u;
+    int k;                                       // <= 0: off
     int bits;                                    // s
+    float u;
+    float grid;                                  // bins for one of a logit
 };
+
+__device__ __forceinline__ float temperature_of(const SampleArgs &a, int64_t row)
+{
+    return a.temperature ? a.temperature[row] : 1.0f;
+}
 
 __device__ __forceinline__ Setting setting_of(const SampleArgs &a, int64_t row)
 {
     Setting s;
-    const float t = a.temperature ? a.temperature[row] : 1.0f;
-    s.rate = t > 0.0f ? 1.4426950408889634074 / (double)t : 0.0;
-    if (!(t > 0.0f))
-        s.rate = -1.0;
-    const float p = a.top_p ? a.top_p[row] : 1.0f;
-    s.p = p < 1.0f ? (double)p : 1.0;            // NaN: off
+    const float t = temperature_of(a, row), p = a.top_p ? a.top_p[row] : 1.0f;
     const float m = a.min_p ? a.min_p[row] : 0.0f;
+    s.rate = t > 0.0f ? 1.4426950408889634074 / (double)t : -1.0;
+    s.p = p < 1.0f ? (double)p : 1.0;            // NaN: off
     s.min_w = m > 0.0f ? (uint64_t)ceil(ldexp((double)fminf(m, 1.0f), a.bits)) : 0;
     s.k = a.top_k ? a.top_k[row] : 0;
-    s.u = a.u ? a.u[row] : 0.0f;
     s.bits = a.bits;
+    s.u = a.u ? a.u[row] : 0.0f;
+    s.grid = BIN_RATE / t;
     return s;
 }
 
-// 2^t as a whole number, nearest, for t <= 51: 2^n times a polynomial for 2^f, |f| <=
-// 1/2 (interpolated in Chebyshev's points, off by 2^-51), whose bits come to the
-// low end of a mantissa by adding 2^52.
-__device__ __forceinline__ uint64_t whole_exp2(double t)
+// 2^52 + 2^t, rounded to a whole number, for -1000 < t < 52: 2^n times a polynomial
+// for 2^f, |f| <= 1/2 (interpolated in Chebyshev's points, off by 2^-51).
+__device__ __forceinline__ double whole_exp2(double t)
 {
     const double n = rint(t), f = t - n;
     double p = 7.072585949269223e-09;
@@ -64,18 +70,24 @@ __device__ __forceinline__ uint64_t whole_exp2(double t)
     p = fma(p, f, 0.24022650695910097);
     p = fma(p, f, 0.69314718055995);
     p = fma(p, f, 1.0);
-    const uint64_t scaled = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(int64_t)(int)n << 52);
-    const double magic = __builtin_bit_cast(double, scaled) + 0x1p52;
-    return __builtin_bit_cast(uint64_t, magic) & 0xFFFFFFFFFFFFFull;
+    const uint64_t scaled = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(uint32_t)(int)n << 52);
+    return __builtin_bit_cast(double, scaled) + 0x1p52;
 }
 
 // A weight in units of 2^-bits; 0 for what is no number, or -infinity.
 __device__ __forceinline__ uint64_t weight(float x, float top, const Setting &s)
 {
     const double t = ((double)x - (double)top) * s.rate + (double)s.bits;
-    const uint64_t w = whole_exp2(fmax(t, -2.0));                // 1/4: rounds to 0; so does NaN
+    // 1/4 rounds to 0, and so do NaN and what is far below
+    const uint64_t w = __builtin_bit_cast(uint64_t, whole_exp2(fmax(t, -2.0))) & 0xFFFFFFFFFFFFFull;
     const uint64_t got = x > -__builtin_inff() ? w : 0;
     return x == top ? uint64_t(1) << s.bits : got;
+}
+
+// The same as a double, for an element that is in a bin (below): then -16 < t.
+__device__ __forceinline__ double weight_in_bin(float x, float top, const Setting &s)
+{
+    return whole_exp2(((double)x - (double)top) * s.rate + (double)s.bits) - 0x1p52;
 }
 
 // Whether an element with `before` weights in front of it is inside top-p's
@@ -162,7 +174,7 @@ __device__ __forceinline__ Found find_key(const Walker &r, const Setting &s, Row
         uint64_t all_mass;
         const uint32_t cb = f.count_before + scan_before<WAVES>(own, l.scan32, all_count);
         const uint64_t mb = f.mass_before + scan_before<WAVES>(mass, l.scan, all_mass);
-        const bool last = own && (K ? cb < s.k : inside(mb, s.p, total));
+        const bool last = own && (K ? cb < (uint32_t)s.k : inside(mb, s.p, total));
         if (last)
             atomicMax(&l.hit, tid);
         __syncthreads();
@@ -175,7 +187,7 @@ __device__ __forceinline__ Found find_key(const Walker &r, const Setting &s, Row
         const uint32_t digit = 255 - hit;        // a row has an element of weight: its largest
         f.key |= digit << shift;
         f.ties = l.count[digit];
-        if (K && shift == 24 && (int64_t)all_count <= s.k)
+        if (K && shift == 24 && all_count <= (uint32_t)s.k)
             f.all = true;
         f.count_before = l.count_before;
         f.mass_before = l.mass_before;
@@ -233,7 +245,7 @@ __device__ __forceinline__ Cut find_cut(const Walker &r, const Setting &s, RowLd
     if (s.k > 0) {
         f = find_key<true>(r, s, l, 0);
         if (!f.all) {
-            m = (uint32_t)(s.k - f.count_before);
+            m = (uint32_t)s.k - f.count_before;
             total = f.mass_before + m * weight(key_value(f.key), r.top, s);
             cut = true;
         }
@@ -318,8 +330,7 @@ __device__ __forceinline__ uint64_t walk_row(const SampleArgs &a, const Walker &
 
 __device__ __forceinline__ float max_all(float v, float *lds)
 {
-    for (int m = 1; m < 64; m <<= 1)
-        v = fmaxf(v, __shfl_xor(v, m));
+    v = wave_max(v);
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -370,24 +381,23 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 // elements by their place below it, in bins of 1 / BIN_RATE in the exponent on a
 // grid that all tiles share.  A bin's count and its mass come from one 64-bit add in
 // LDS: the mass, in the low half, in fixed point relative to the bin, whose
-// weights lie within 7 % of each other.
-// k_gather: each workgroup adds up the bins of the row and learns in which of them
-// top-k and top-p cut (the masses err by a known margin, so at times two come into
-// question), sums the exact weights of what is surely kept, and lists the elements
-// of the bins in question.
+// weights lie within 2 % of each other.
+// k_range: one workgroup a row adds up its bins and learns in which of them top-k and
+// top-p cut (the masses err by a known margin, so at times two come into question).
+// k_gather: each workgroup sums the exact weights of what is surely kept, and lists
+// the elements of the bins in question.
 // k_cut: one workgroup a row ranks the list, which gives the cut, and draws.
 // k_probs writes the distribution instead.
 // A vocabulary of one tile takes one launch (k_one) and no scratch.  Rows that the
-// grid does not suit (a largest logit or a rate past what fp32 holds) or whose list
-// does not fit (thousands of equal logits) are left to the search through the whole
-// row, by k_cut's workgroup.
+// grid does not suit (logits far above the temperature) or whose list does not fit
+// (thousands of equal logits) are left to the search through the whole row, by
+// k_cut's workgroup.
 
-constexpr int BINS = 512;
 // 32 in the exponent and more weigh nothing (2^-46); a bin more for the grid.
-constexpr float BIN_RATE = 15.0f;
+constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int MASS_BITS = 17;                    // of a bin's first weight: 16384 elements fit 32 bits
 constexpr int MOST_TILES = 64;
-constexpr int LIST = 4096, SUBS = THREADS;
+constexpr int LIST = 4096, SHORT = 128, SUBS = THREADS;
 constexpr int MOST_ROWS = 4096;                  // of one launch; more take several
 
 // Exact weights: kept: surely, and heavy enough for min-p; below: surely inside
@@ -406,15 +416,17 @@ struct Range {
 
 // What a row has in scratch.
 struct RowScratch {
-    float top[MOST_TILES];                       // of each tile
-    int first[MOST_TILES];                       // its first place
-    Sums sums[MOST_TILES];
-    uint64_t list[LIST];                         // entry()
+    Setting setting;
     Range range;
+    float row_top;
     uint32_t listed;
     uint32_t key;                                // the cut, and the sum of what is kept
     int32_t last;
     uint64_t sum;
+    float top[MOST_TILES];                       // of each tile
+    int first[MOST_TILES];                       // its first place
+    Sums sums[MOST_TILES];
+    uint64_t list[LIST];                         // entry()
 };
 
 // An element in the order of what is kept: falling logits, rising index.
@@ -424,11 +436,6 @@ __device__ __forceinline__ uint64_t entry(float x, uint32_t i)
 }
 
 __device__ __forceinline__ float entry_value(uint64_t e) { return key_value(~(uint32_t)(e >> 32)); }
-
-__device__ __forceinline__ float grid_rate(const Setting &s)
-{
-    return (float)(s.rate * (BIN_RATE * 0.69314718055994531));
-}
 
 // Whether fp32 resolves the grid around a row's largest logit: places there err by
 // less than half a bin.
@@ -478,19 +485,11 @@ __device__ __forceinline__ float top_of(const float (&x)[PER], float *red)
     return max_all(top, red);
 }
 
-// The row's largest logit from its tiles'.
-__device__ __forceinline__ float top_of(const RowScratch &r, int tiles)
-{
-    const int lane = threadIdx.x & 63;
-    float top = lane < tiles ? r.top[lane] : -__builtin_inff();
-    for (int m = 1; m < 64; m <<= 1)
-        top = fmaxf(top, __shfl_xor(top, m));
-    return top;
-}
-
-// Adds a tile's elements to its bins (zeroed, and a barrier since).
+// Adds a tile's elements to its bins (zeroed, and a barrier since).  Without top-k
+// only the masses are asked for, and 32-bit adds meet in half as many banks.
 template <int PER>
-__device__ __forceinline__ void add_bins(const float (&x)[PER], float top, float rate, uint64_t *bins)
+__device__ __forceinline__ void add_bins(const float (&x)[PER], float top, float rate, bool counted,
+                                         uint64_t *bins)
 {
     const float place = floorf(top * rate);
 #pragma unroll
@@ -499,8 +498,11 @@ __device__ __forceinline__ void add_bins(const float (&x)[PER], float top, float
         if (d < (float)BINS) {
             const float part = fmaf(x[e], rate, -whole);
             const float m = __builtin_amdgcn_exp2f(part * (1.44269504f / BIN_RATE));
-            atomicAdd((unsigned long long *)&bins[(int)d],
-                      (1ull << 32) | (uint32_t)fmaf(m, (float)(1 << MASS_BITS), 0.5f));
+            const uint32_t units = (uint32_t)fmaf(m, (float)(1 << MASS_BITS), 0.5f);
+            if (counted)
+                atomicAdd((unsigned long long *)&bins[(int)d], (1ull << 32) | units);
+            else
+                atomicAdd((uint32_t *)bins + (int)d, units);
         }
     }
 }
@@ -525,134 +527,176 @@ __global__ __launch_bounds__(THREADS) void k_bins(SampleArgs a, RowScratch *scra
     __shared__ int first;
     const int tid = threadIdx.x, tile = blockIdx.x;
     const int64_t row = blockIdx.y, i0 = ((int64_t)tile * THREADS + tid) * PER;
-    const Setting s = setting_of(a, row);
+    const float t = temperature_of(a, row);
+    const int k = a.top_k ? a.top_k[row] : 0;
+    const bool counted = k > 0, cut = counted || (a.top_p && a.top_p[row] < 1.0f);
     float x[PER];
     load_tile<PER, DT>(x, a, row, i0);
-    if (tid < BINS)
-        bins[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; i++)
+        bins[i * THREADS + tid] = 0;
     if (tid == 0)
         first = 0x7FFFFFFF;
     const float top = top_of(x, red);
     RowScratch &r = scratch[row];
-    if (s.rate < 0.0) {                          // greedy: its place is all there is to know
+    if (!(t > 0.0f)) {                           // greedy: its place is all there is to know
         note_first(x, top, i0, &first);
         __syncthreads();
-    } else if (cuts(s)) {
-        add_bins(x, top, grid_rate(s), bins);
+    } else if (cut) {
+        add_bins(x, top, BIN_RATE / t, counted, bins);
         __syncthreads();
-        if (tid < BINS)
-            planes[(row * gridDim.x + tile) * BINS + tid] = bins[tid];
+        // without counts: 32-bit masses in the first half of its place
+        uint64_t *out = planes + (row * gridDim.x + tile) * BINS;
+#pragma unroll
+        for (int i = 0; i < EACH; i++)
+            if (counted || i < EACH / 2)
+                out[i * THREADS + tid] = bins[i * THREADS + tid];
     }
     if (tid == 0) {
         r.top[tile] = top;
         r.first[tile] = first;
-        if (tile == 0)
-            r.listed = 0;
     }
 }
 
 struct RangeLds {
-    uint32_t half_count[BINS];
-    uint64_t half_units[BINS];
-    int shift[MOST_TILES];
-    uint32_t scan32[WAVES];
-    double scan[WAVES];
+    uint32_t scan32[EACH][WAVES];
+    float scan[EACH][WAVES];
     int lo, hi, kbin;
     uint32_t k_before;
-    double mass_k, mass_through;
+    float mass_k, mass_through;
 };
 
-// From the bins of all tiles (or of this one, in LDS) to those that cut.
-template <bool ALONE>
-__device__ __forceinline__ Range find_range(RangeLds &l, const Setting &s, const RowScratch *r,
-                                            const uint64_t *planes, int tiles, float top)
+// The largest number of the threads with `is`, into *p: one add to it a wave.
+__device__ __forceinline__ void note_last(bool is, int number, int *p)
 {
-    const int tid = threadIdx.x, b = tid & (BINS - 1), half = tid / BINS;
-    const float rate = grid_rate(s), place = floorf(top * rate);
+    const uint64_t some = __ballot(is);
+    if (some && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(some))
+        atomicMax(p, number);
+}
+
+// From the bins of the row (thread t: bins t, t + THREADS, ...) to those that cut.
+__device__ __forceinline__ Range find_range(RangeLds &l, const uint32_t (&count)[EACH],
+                                            const uint64_t (&units)[EACH], const Setting &s, float top)
+{
+    const int tid = threadIdx.x;
+    const float place = floorf(top * s.grid);
     Range g{BINS, -1, BINS, 0, 0};
-    if (!on_grid(top, rate)) {
-        g.odd = 1;
-        return g;
-    }
-    uint32_t count = 0;
-    uint64_t units = 0;
-    if constexpr (ALONE) {
-        if (half == 0) {
-            count = (uint32_t)(planes[b] >> 32);
-            units = (uint32_t)planes[b];
-        }
-    } else {
-        if (tid < tiles)
-            l.shift[tid] = bin_of(r->top[tid], place, rate);
-        __syncthreads();
-        // by fours: the loads of four tiles are on their way together
-        for (int c0 = half * 4; c0 < tiles; c0 += 8) {
-            uint64_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int c = min(c0 + k, tiles - 1), i = b - l.shift[c];
-                v[k] = planes[c * BINS + max(i, 0)];
-                if (i < 0 || c0 + k >= tiles)
-                    v[k] = 0;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                count += (uint32_t)(v[k] >> 32);
-                units += (uint32_t)v[k];
-            }
-        }
-        if (half) {
-            l.half_count[b] = count;
-            l.half_units[b] = units;
-        }
-        __syncthreads();
-        if (!half) {
-            count += l.half_count[b];
-            units += l.half_units[b];
-        }
-    }
-    if (half) {
-        count = 0;
-        units = 0;
-    }
     if (tid == 0)
         l.lo = l.hi = l.kbin = -1;
-    uint32_t all;
-    double total;
-    const double mass = (double)units * (double)exp2f((float)b * (-1.44269504f / BIN_RATE));
-    const uint32_t before = scan_before<WAVES>(count, l.scan32, all);
-    const double mass_before = scan_before<WAVES>(mass, l.scan, total);
-    const bool k_cuts = s.k > 0 && (int64_t)all > s.k;
-    if (k_cuts && count && before < s.k)
-        atomicMax(&l.kbin, b);
-    __syncthreads();
-    g.kbin = k_cuts ? l.kbin : BINS;
-    if (!half && b == g.kbin) {
-        l.k_before = before;
-        l.mass_k = mass_before;
-        l.mass_through = mass_before + mass;
+    uint32_t all = 0, before[EACH];
+    float total = 0.0f, mass[EACH], ahead[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; i++) {
+        uint32_t c;
+        float m;
+        mass[i] = (float)units[i] * exp2f((float)(tid + i * THREADS) * (-1.44269504f / BIN_RATE));
+        before[i] = all + scan_before<WAVES>(count[i], l.scan32[i], c);
+        ahead[i] = total + scan_before<WAVES>(mass[i], l.scan[i], m);
+        all += c;
+        total += m;
     }
-    __syncthreads();
-    if (k_cuts) {
-        g.lo = g.hi = g.kbin;
+    float least = total, most = total;
+    if (s.k > 0 && all > (uint32_t)s.k) {
+#pragma unroll
+        for (int i = 0; i < EACH; i++)
+            note_last(count[i] && before[i] < (uint32_t)s.k, tid + i * THREADS, &l.kbin);
+        __syncthreads();
+        g.kbin = g.lo = g.hi = l.kbin;
+#pragma unroll
+        for (int i = 0; i < EACH; i++)
+            if (tid + i * THREADS == g.kbin) {
+                l.k_before = before[i];
+                l.mass_k = ahead[i];
+                l.mass_through = ahead[i] + mass[i];
+            }
+        __syncthreads();
         g.k_before = l.k_before;
+        least = l.mass_k;
+        most = l.mass_through;
     }
     if (s.p < 1.0) {
-        const double least = k_cuts ? l.mass_k : total, most = k_cuts ? l.mass_through : total;
-        // A weight's part of its bin is rounded to 2^-18 of it; the grid's rate and a
-        // place on it err by 2^-24 of the place, yet the part stays within its bin.
-        const double margin = 0x1p-15 + fmin((double)(fabsf(place) + BINS) * 0x1p-22, 0.08);
-        if (count && (before == 0 ||
-                      mass_before * (1.0 + margin) < s.p * least * (1.0 - margin)))
-            atomicMax(&l.lo, b);
-        if (count && (before == 0 ||
-                      mass_before * (1.0 - margin) <= s.p * most * (1.0 + margin)))
-            atomicMax(&l.hi, b);
+        // A weight's part of its bin is rounded to 2^-18 of it, sums of 2048 bins to
+        // 2^-19 (by lanes and waves); the grid's rate and a place on it err by 2^-24
+        // of the place, yet the part stays within its bin.
+        const float margin = 0x1p-15f + fminf((fabsf(place) + BINS) * 0x1p-23f, 0.02f);
+        const float p = (float)s.p, sure = p * least * (1.0f - margin), some = p * most * (1.0f + margin);
+#pragma unroll
+        for (int i = 0; i < EACH; i++) {
+            const int b = tid + i * THREADS;
+            note_last(count[i] && (b == 0 || ahead[i] * (1.0f + margin) < sure), b, &l.lo);
+            note_last(count[i] && (b == 0 || ahead[i] * (1.0f - margin) <= some), b, &l.hi);
+        }
         __syncthreads();
-        g.lo = l.lo;
+        g.lo = max(l.lo, 0);
         g.hi = min(l.hi, g.kbin);
     }
     return g;
+}
+
+// COUNTED: the tiles' bins hold counts, too.
+template <bool COUNTED>
+__device__ __forceinline__ void add_tiles(uint32_t (&count)[EACH], uint64_t (&units)[EACH],
+                                          const uint64_t *from, int tiles, int shift)
+{
+    const int tid = threadIdx.x;
+    for (int c0 = 0; c0 < tiles; c0 += 8) {
+        uint64_t v[8][EACH];                     // the loads of eight tiles together
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int c = min(c0 + k, tiles - 1), down = __builtin_amdgcn_readlane(shift, c);
+#pragma unroll
+            for (int i = 0; i < EACH; i++) {
+                const int b = tid + i * THREADS - down;
+                if constexpr (COUNTED)
+                    v[k][i] = from[c * BINS + max(b, 0)];
+                else
+                    v[k][i] = ((const uint32_t *)(from + c * BINS))[max(b, 0)];
+                if (b < 0 || c0 + k >= tiles)
+                    v[k][i] = 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+#pragma unroll
+            for (int i = 0; i < EACH; i++) {
+                count[i] += (uint32_t)(COUNTED ? v[k][i] >> 32 : v[k][i] != 0);
+                units[i] += (uint32_t)v[k][i];
+            }
+    }
+}
+
+__global__ __launch_bounds__(THREADS) void k_range(SampleArgs a, RowScratch *scratch,
+                                                   const uint64_t *planes, int tiles)
+{
+    __shared__ RangeLds l;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x;
+    RowScratch &r = scratch[row];
+    const float tile_top = lane < tiles ? r.top[lane] : -__builtin_inff();
+    const Setting s = setting_of(a, row);
+    const float top = wave_max(tile_top);
+    Range g{BINS, -1, BINS, 0, 0};
+    if (top > -__builtin_inff() && s.rate >= 0.0 && cuts(s)) {
+        if (on_grid(top, s.grid)) {
+            const int shift = bin_of(tile_top, floorf(top * s.grid), s.grid);    // of lane's tile
+            const uint64_t *from = planes + row * tiles * BINS;
+            uint32_t count[EACH] = {};
+            uint64_t units[EACH] = {};
+            if (s.k > 0)
+                add_tiles<true>(count, units, from, tiles, shift);
+            else
+                add_tiles<false>(count, units, from, tiles, shift);
+            g = find_range(l, count, units, s, top);
+        } else {
+            g.odd = 1;
+        }
+    }
+    if (tid == 0) {
+        r.setting = s;
+        r.range = g;
+        r.row_top = top;
+        r.listed = 0;
+    }
 }
 
 // A workgroup's sums, to all of its threads.
@@ -681,65 +725,84 @@ template <int PER>
 __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float top, const Setting &s,
                                        const Range &g, uint64_t *list, uint32_t most, uint32_t *listed)
 {
-    const float rate = grid_rate(s), place = floorf(top * rate);
+    const float rate = s.grid, place = floorf(top * rate);
     Sums mine{0, 0, 0};
     if (g.odd)
         return mine;
-    const bool cut = g.hi >= 0 || g.kbin < BINS;
+    if (g.lo == BINS && !on_grid(top, rate)) {
+        // nothing cuts: any element may be kept
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            const uint64_t w = weight(x[e], top, s);
+            mine.kept += w >= s.min_w ? w : 0;
+        }
+        return mine;
+    }
+    float d[PER];
+    const float end = (float)(g.kbin < BINS ? g.kbin + 1 : BINS);
+    bool some = false;
 #pragma unroll
     for (int e = 0; e < PER; e++) {
-        const int bin = cut || on_grid(top, rate) ? bin_of(x[e], place, rate) : 0;
-        if (bin >= BINS || (bin > g.kbin))
-            continue;
-        const uint64_t w = weight(x[e], top, s);
-        mine.limit += bin < g.kbin ? w : 0;
-        if (bin < g.lo) {
-            mine.below += w;
-            mine.kept += w >= s.min_w ? w : 0;
-        } else if (w && (bin <= g.hi || bin == g.kbin)) {
-            const uint32_t at = atomicAdd(listed, 1u);
-            if (at < most)
-                list[at] = entry(x[e], (uint32_t)(i0 + e));
-        }
+        d[e] = place - floorf(x[e] * rate);
+        some = some || d[e] < end;
     }
-    return mine;
+    if (!__any(some))
+        return mine;                             // a wave of what top-k leaves out
+    const float lo = (float)g.lo, hi = (float)g.hi, kbin = (float)g.kbin;
+    // whole numbers below 2^50: exact in any order
+    const double min_w = (double)s.min_w;
+    double kept = 0.0, below = 0.0, limit = 0.0;
+    uint32_t question = 0;
+#pragma unroll
+    for (int e = 0; e < PER; e++) {
+        const double w = d[e] < end ? weight_in_bin(x[e], top, s) : 0.0;
+        limit += d[e] < kbin ? w : 0.0;
+        const double b = d[e] < lo ? w : 0.0;
+        below += b;
+        kept += b >= min_w ? b : 0.0;
+        question |= w > 0.0 && ((d[e] >= lo && d[e] <= hi) || d[e] == kbin) ? 1u << e : 0u;
+    }
+    if (question) {
+        uint32_t at = atomicAdd(listed, (uint32_t)__builtin_popcount(question));
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            if (question >> e & 1) {
+                if (at < most)
+                    list[at] = entry(x[e], (uint32_t)(i0 + e));
+                at++;
+            }
+    }
+    return Sums{(uint64_t)kept, (uint64_t)below, (uint64_t)limit};
 }
 
 template <int PER, int DT>
-__global__ __launch_bounds__(THREADS) void k_gather(SampleArgs a, RowScratch *scratch,
-                                                    const uint64_t *planes)
+__global__ __launch_bounds__(THREADS, 8) void k_gather(SampleArgs a, RowScratch *scratch)
 {
-    constexpr int MOST = PER * THREADS < LIST ? PER * THREADS : LIST;
-    __shared__ RangeLds range;
-    __shared__ uint64_t list[MOST], sums[3][WAVES];
+    __shared__ uint64_t list[LIST], sums[3][WAVES];
     __shared__ uint32_t listed, base;
-    const int tid = threadIdx.x, tile = blockIdx.x, tiles = gridDim.x;
+    const int tid = threadIdx.x, tile = blockIdx.x;
     const int64_t row = blockIdx.y, i0 = ((int64_t)tile * THREADS + tid) * PER;
-    const Setting s = setting_of(a, row);
     RowScratch &r = scratch[row];
     float x[PER];
     load_tile<PER, DT>(x, a, row, i0);
-    const float top = top_of(r, tiles);
+    const Setting s = r.setting;
+    const Range g = r.range;
+    const float top = r.row_top;
     if (top == -__builtin_inff() || s.rate < 0.0)
         return;
     if (tid == 0)
         listed = 0;
     __syncthreads();
-    Range g{BINS, -1, BINS, 0, 0};
-    if (cuts(s))
-        g = find_range<false>(range, s, &r, planes + row * tiles * BINS, tiles, top);
-    const Sums all = sum_up(gather(x, i0, top, s, g, list, MOST, &listed), sums);
+    const Sums all = sum_up(gather(x, i0, top, s, g, list, LIST, &listed), sums);
     const uint32_t n = listed;
     if (tid == 0) {
         r.sums[tile] = all;
-        if (tile == 0)
-            r.range = g;
         if (n)
             base = atomicAdd(&r.listed, n);
     }
     if (n) {
         __syncthreads();
-        for (uint32_t i = tid; i < min(n, (uint32_t)MOST) && base + i < LIST; i += THREADS)
+        for (uint32_t i = tid; i < min(n, (uint32_t)LIST) && base + i < LIST; i += THREADS)
             r.list[base + i] = list[i];
     }
 }
@@ -800,6 +863,65 @@ __device__ __forceinline__ void rank_in(CutLds &l, uint32_t n, int sub, uint32_t
     }
 }
 
+// What a short list's cut is: threads in a row share an entry and count what comes
+// before it.
+__device__ __forceinline__ Cut rank_short(CutLds &l, const Setting &s, const Range &g, uint32_t n,
+                                          const Sums &all, float top, int tile_size)
+{
+    const int tid = threadIdx.x;
+    const float rate = s.grid, place = floorf(top * rate);
+    const bool k_cuts = g.kbin < BINS;
+    int P = THREADS / SHORT;
+    while (P < 64 && n * P * 2 <= THREADS)
+        P *= 2;
+    if (tid == 0) {
+        l.cut = l.part = 0;
+        l.low = 0;
+    }
+    __syncthreads();
+    if (tid < n) {
+        const float x = entry_value(l.list[tid]);
+        l.weight[tid] = weight(x, top, s);
+        if (k_cuts && bin_of(x, place, rate) < g.kbin)
+            atomicAdd(&l.low, 1u);
+    }
+    __syncthreads();
+    const uint32_t i = (uint32_t)tid / P;
+    const bool in = i < n && !(tid & (P - 1));
+    const uint64_t e = i < n ? l.list[i] : 0, w = i < n ? l.weight[i] : 0;
+    uint32_t rank = 0;
+    uint64_t before = 0;
+    if (i < n) {
+#pragma unroll 4
+        for (uint32_t j = tid & (P - 1); j < n; j += P) {
+            const bool ahead = l.list[j] < e;
+            rank += ahead;
+            before += ahead ? l.weight[j] : 0;
+        }
+    }
+    for (int d = 1; d < P; d <<= 1) {
+        rank += __shfl_xor(rank, d);
+        before += __shfl_xor((unsigned long long)before, d);
+    }
+    const int bin = bin_of(entry_value(e), place, rate);
+    const bool in_k = !k_cuts || bin < g.kbin || rank - l.low < (uint32_t)s.k - g.k_before;
+    uint64_t total = all.limit;
+    if (k_cuts && s.p < 1.0) {
+        if (in && in_k && bin == g.kbin)
+            atomicAdd(&l.part, (unsigned long long)w);
+        __syncthreads();
+        total += l.part;
+    }
+    if (in && in_k && bin <= g.hi && inside(all.below + before, s.p, total)) {
+        atomicMax(&l.cut, (unsigned long long)e);
+        if (w >= s.min_w)
+            atomicAdd((unsigned long long *)&l.tile_kept[(uint32_t)e / tile_size],
+                      (unsigned long long)w);
+    }
+    __syncthreads();
+    return Cut{~(uint32_t)(l.cut >> 32), (int64_t)(uint32_t)l.cut};
+}
+
 // The cut, from the list in LDS (n entries); adds what is kept of it to the tiles'
 // sums.  Sub-bins of the list's own range, in falling order, bring it down to the
 // few elements around a cut; those are ranked one by one.
@@ -807,7 +929,7 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
                                          const Sums &all, float top, int tile_size)
 {
     const int tid = threadIdx.x;
-    const float rate = grid_rate(s), place = floorf(top * rate);
+    const float rate = s.grid, place = floorf(top * rate);
     const bool k_cuts = g.kbin < BINS;
     l.sub_count[tid] = 0;
     l.sub_mass[tid] = 0;
@@ -832,11 +954,15 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
             low_mass += w;
         }
     }
-    if (most) {
+    for (int d = 1; d < 64; d <<= 1) {
+        least = min(least, (uint32_t)__shfl_xor(least, d));
+        most = max(most, (uint32_t)__shfl_xor(most, d));
+    }
+    low = wave_sum(low);
+    low_mass = wave_sum(low_mass);
+    if ((tid & 63) == 0) {
         atomicMin(&l.least, least);
         atomicMax(&l.most, most);
-    }
-    if (low) {
         atomicAdd(&l.low, low);
         atomicAdd(&l.low_mass, (unsigned long long)low_mass);
     }
@@ -857,7 +983,7 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
     const uint32_t before = scan_before<WAVES>(count, l.scan32, all_count);
     const uint64_t mass_before = scan_before<WAVES>(mass, l.scan, all_mass);
     // top-k keeps k_rank entries of the list: those above kbin and some in it
-    const uint32_t k_rank = k_cuts ? (uint32_t)(s.k - g.k_before) + l.low : ~0u;
+    const uint32_t k_rank = k_cuts ? (uint32_t)s.k - g.k_before + l.low : ~0u;
     uint64_t total = all.limit;
     if (k_cuts) {
         if (count && before < k_rank)
@@ -912,7 +1038,8 @@ __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, Cut
         return walk_row(a, walker, s, c, row, rl);
     }
     if (n)
-        c = rank_list(l, s, g, n, all, top, PER * THREADS);
+        c = n <= SHORT ? rank_short(l, s, g, n, all, top, PER * THREADS)
+                       : rank_list(l, s, g, n, all, top, PER * THREADS);
     // the tile, then the element in it, where the running sum passes u
     const uint64_t v = lane < tiles ? l.tile_kept[lane] : 0, run = scan_wave(v);
     const uint64_t sum = lane_value(run, 63), thr = place_in(s.u, sum);
@@ -952,9 +1079,10 @@ __global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scrat
     __shared__ int first;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
-    Setting s = setting_of(a, row);
     RowScratch &r = scratch[row];
-    const float top = top_of(r, tiles);
+    const uint64_t e0 = r.list[tid];             // before it is known how many there are
+    const Setting s = r.setting;
+    const float top = r.row_top;
     const bool none = top == -__builtin_inff();
     Cut c{0, a.vocab};
     uint64_t sum = 0;
@@ -980,7 +1108,8 @@ __global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scrat
             v = r.sums[tid];
             l.tile_kept[tid] = v.kept;
         }
-        for (uint32_t i = tid; i < min(n, (uint32_t)LIST); i += THREADS)
+        l.list[tid] = e0;
+        for (uint32_t i = THREADS + tid; i < min(n, (uint32_t)LIST); i += THREADS)
             l.list[i] = r.list[i];
         const Sums all = sum_up(v, sums);
         float x[PER];
@@ -1035,13 +1164,12 @@ template <int PER, int DT>
 __global__ __launch_bounds__(THREADS) void k_probs(SampleArgs a, const RowScratch *scratch)
 {
     const int64_t row = blockIdx.y, i0 = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * PER;
-    Setting s = setting_of(a, row);
-    set_greedy(s);
     const RowScratch &r = scratch[row];
     float x[PER];
     load_tile<PER, DT>(x, a, row, i0);
-    const float top = top_of(r, gridDim.x);
-    write_probs(a, row, i0, x, top, s, Cut{r.key, r.last}, r.sum);
+    Setting s = r.setting;
+    set_greedy(s);
+    write_probs(a, row, i0, x, r.row_top, s, Cut{r.key, r.last}, r.sum);
 }
 
 // A vocabulary of one tile.
@@ -1058,8 +1186,9 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
     Setting s = setting_of(a, row);
     float x[PER];
     load_tile<PER, DT>(x, a, row, i0);
-    if (tid < BINS)
-        bins[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; i++)
+        bins[i * THREADS + tid] = 0;
     if (tid == 0) {
         first = 0x7FFFFFFF;
         listed = 0;
@@ -1081,9 +1210,22 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
     } else {
         Range g{BINS, -1, BINS, 0, 0};
         if (cuts(s)) {
-            add_bins(x, top, grid_rate(s), bins);
-            __syncthreads();
-            g = find_range<true>(range, s, nullptr, bins, 1, top);
+            if (on_grid(top, s.grid)) {
+                const bool counted = s.k > 0;
+                add_bins(x, top, s.grid, counted, bins);
+                __syncthreads();
+                uint32_t count[EACH];
+                uint64_t units[EACH];
+#pragma unroll
+                for (int i = 0; i < EACH; i++) {
+                    const int b = tid + i * THREADS;
+                    units[i] = counted ? (uint32_t)bins[b] : ((const uint32_t *)bins)[b];
+                    count[i] = counted ? (uint32_t)(bins[b] >> 32) : units[i] != 0;
+                }
+                g = find_range(range, count, units, s, top);
+            } else {
+                g.odd = 1;
+            }
         }
         const Sums all = sum_up(gather(x, i0, top, s, g, l.list, LIST, &listed), sums);
         const uint32_t n = listed;
@@ -1096,30 +1238,28 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
         write_probs(a, row, i0, x, top, s, c, sum);
 }
 
-constexpr int PER = 8;
+// Elements a thread: 8, or 16 where the tiles were too many else.  (16 for 64 rows
+// of 128001: 64 us a call, 60 with 8.)
+bool large_tiles(int64_t vocab) { return vocab > (int64_t)8 * THREADS * MOST_TILES; }
 
-int64_t tiles_of(int64_t vocab) { return (vocab + PER * THREADS - 1) / (PER * THREADS); }
-
-template <int DT> hipError_t launch_dt(SampleArgs a, void *scratch, hipStream_t s)
+int64_t tiles_of(int64_t vocab)
 {
-    const int64_t tiles = tiles_of(a.vocab), rows = a.rows;
-    if (tiles == 1 || tiles > MOST_TILES) {
-        if (!grid_fits(rows, THREADS))
-            return hipErrorInvalidConfiguration;
-        if (tiles == 1)
-            k_one<PER, DT><<<dim3((unsigned)rows), THREADS, 0, s>>>(a);
-        else
-            k_sample_row<<<dim3((unsigned)rows), THREADS, 0, s>>>(a);
-        return hipGetLastError();
-    }
+    const int64_t size = (large_tiles(vocab) ? 16 : 8) * THREADS;
+    return (vocab + size - 1) / size;
+}
+
+template <int PER, int DT>
+hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t s)
+{
     RowScratch *r = (RowScratch *)scratch;
-    uint64_t *planes = (uint64_t *)(r + std::min<int64_t>(rows, MOST_ROWS));
-    const int64_t size = DT == TQ_F32 ? 4 : 2;
+    uint64_t *planes = (uint64_t *)(r + std::min<int64_t>(a.rows, MOST_ROWS));
+    const int64_t rows = a.rows, size = DT == TQ_F32 ? 4 : 2;
     for (int64_t at = 0; at < rows; at += MOST_ROWS) {
         const int64_t n = std::min<int64_t>(rows - at, MOST_ROWS);
         const dim3 grid((unsigned)tiles, (unsigned)n);
         k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
-        k_gather<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
+        k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)tiles);
+        k_gather<PER, DT><<<grid, THREADS, 0, s>>>(a, r);
         k_cut<PER, DT><<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, (int)tiles);
         if (a.probs)
             k_probs<PER, DT><<<grid, THREADS, 0, s>>>(a, r);
@@ -1136,6 +1276,21 @@ template <int DT> hipError_t launch_dt(SampleArgs a, void *scratch, hipStream_t 
         a.probs += a.probs ? MOST_ROWS * a.probs_stride : 0;
     }
     return hipSuccess;
+}
+
+template <int DT> hipError_t launch_dt(const SampleArgs &a, void *scratch, hipStream_t s)
+{
+    const int64_t tiles = tiles_of(a.vocab);
+    if (tiles > 1 && tiles <= MOST_TILES)
+        return large_tiles(a.vocab) ? launch_tiles<16, DT>(a, tiles, scratch, s)
+                                            : launch_tiles<8, DT>(a, tiles, scratch, s);
+    if (!grid_fits(a.rows, THREADS))
+        return hipErrorInvalidConfiguration;
+    if (tiles == 1)
+        k_one<8, DT><<<dim3((unsigned)a.rows), THREADS, 0, s>>>(a);
+    else
+        k_sample_row<<<dim3((unsigned)a.rows), THREADS, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
