@@ -4,6 +4,7 @@ No compute happens here; a missing library is an error (there is no fallback).
 """
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtiledq.so")
@@ -74,7 +75,29 @@ SIGNATURES = {
     "tq_tree_attention_heads": (INT, [INT, INT, P, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P,
                                       I64, I64, I64, I64, P, P, P, I64, I64, I64, I64, F32, P, I64,
                                       I64, P, SZ, P]),
+    "tq_packed": (INT, [INT, ctypes.c_char_p]),
 }
+
+# Calls that go through tq_packed, by their number there.
+PACKED = ("tq_tree_attention", "tq_tree_attention_heads", "tq_plan_step", "tq_release_pages",
+          "tq_residual_norm", "tq_sample", "tq_sample_probs", "tq_cache_bounds", "tq_select_pages")
+
+
+class _Packed:
+    """An entry point called with its arguments packed into one (plain numbers,
+    0 for no pointer); others are left to ctypes."""
+
+    def __init__(self, which, plain, packed):
+        self.which, self.plain, self.packed = which, plain, packed
+        self.pack = struct.Struct("<" + "".join("f4x" if a is F32 else "q"
+                                                for a in plain.argtypes)).pack
+
+    def __call__(self, *args):
+        try:
+            slots = self.pack(*args)
+        except (struct.error, OverflowError):
+            return self.plain(*args)
+        return self.packed(self.which, slots)
 
 
 class TiledqError(RuntimeError):
@@ -94,6 +117,8 @@ def lib():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        for which, name in enumerate(PACKED):
+            setattr(L, name, _Packed(which, getattr(L, name), L.tq_packed))
         _lib = L
     return _lib
 

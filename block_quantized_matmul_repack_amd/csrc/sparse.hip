@@ -21,9 +21,14 @@ namespace tq {
 namespace {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVES = 4, THREADS = 64 * WAVES;
-constexpr int SEL_WAVES = 16, SEL_THREADS = 64 * SEL_WAVES;
+constexpr int SEL_WAVES = 8, SEL_THREADS = 64 * SEL_WAVES;
+constexpr int CHOOSE_WAVES = 16;
+constexpr int SCORE_WAVES = 8, SCORE_THREADS = 64 * SCORE_WAVES;
+constexpr int MOST_KEYS = 8192;                  // pages whose keys LDS holds
+constexpr int SPREAD_TURNS = 2, SPREAD_UNITS = 128;
 
 // ---- bounds ----------------------------------------------------------------
 
@@ -128,169 +133,288 @@ __device__ __forceinline__ Span span_of(const SelectArgs &a, int b)
     return s;
 }
 
-// The scores of 16 pages a wave and turn, written as order keys.
-template <int DT, int D> __global__ __launch_bounds__(THREADS) void k_scores(SelectArgs a, uint32_t *keys)
+// Query rows that are in LDS at a time: as 16-row operands of the matrix cores, and
+// their blocks' scales.
+constexpr int row_tiles(int D) { return D <= 128 ? 8 : 4; }
+
+template <int D> struct QueryLds {
+    i4 code[row_tiles(D)][D / 32][64];
+    double scale[row_tiles(D)][D / 32][16];
+};
+
+// Quantizes rows r0 .. of a head's query rows, a 16-row tile's block a wave at a
+// time.  Lane (g, r): elements 16 (g & 1) .. of the block of row r; g < 2 their
+// positive parts, to meet the largest keys, else the negative.  Rows past the last
+// repeat it.
+template <int DT, int D, int W>
+__device__ __forceinline__ void quantize_rows(QueryLds<D> &l, const SelectArgs &a, const Span &sp,
+                                              int h, int r0, int tiles)
 {
     constexpr int NB = D / 32;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
-    const Span sp = span_of(a, b);
-    if (sp.keep == sp.tail - sp.first)
-        return;                                  // all of them are read
-    const int32_t *table = a.table + b * a.table_stride;
-    uint32_t *out = keys + (int64_t)blockIdx.x * a.table_pages;
     const int rows = sp.T * a.group;
-    for (int64_t p0 = sp.first + ((int64_t)blockIdx.y * WAVES + wave) * 16; p0 < sp.tail;
-         p0 += (int64_t)gridDim.y * WAVES * 16) {
-        // lane (g, r): bytes 16g .. of the codes of page p0 + r
-        const int64_t page = min(p0 + r, (int64_t)sp.tail - 1);
-        int64_t id = table[page];
-        const bool there = id >= 0 && id < a.pages;
-        id = there ? id : 0;
-        const int64_t block = (id * a.kv_heads + h) * NB;
-        i4 codes[NB];
-        float scale[NB];
+    for (int item = threadIdx.x >> 6; item < tiles * NB; item += W) {
+        const int tile = item / NB, s = item % NB;
+        const int row = min(r0 + tile * 16 + r, rows - 1), node = row / a.group;
+        const int64_t at = (sp.tok0 + node) * a.qts + (h * a.group + row - node * a.group) * a.qhs +
+                           32 * s + 16 * (g & 1);
+        float v[2][8], big = 0.0f;
+        load_x8<DT>(v[0], a.q, at);
+        load_x8<DT>(v[1], a.q, at + 8);
 #pragma unroll
-        for (int s = 0; s < NB; s++) {
-            codes[s] = *(const i4 *)(a.codes + (block + s) * 64 + g * 16);
-            scale[s] = f16_bits_to_f32(a.scales[block + s]);
+        for (int e = 0; e < 16; e++) {
+            float &x = v[e >> 3][e & 7];
+            x = x != x ? 0.0f : fminf(fmaxf(x, -3.0e38f), 3.0e38f);
+            big = fmaxf(big, fabsf(x));
         }
-        double best[4];
+        big = fmaxf(big, __shfl_xor(big, 16));
+        const float d = big / 127.0f, inv = d > 0x1p-100f ? 1.0f / d : 0.0f;
+        i4 q;
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-            best[e] = -__builtin_inf();
-        for (int r0 = 0; r0 < rows; r0 += 16) {
-            const int row = min(r0 + r, rows - 1);                   // the last one again
-            const int node = row / a.group;
-            const int64_t at = (sp.tok0 + node) * a.qts + (h * a.group + row - node * a.group) * a.qhs;
-            double sum[4] = {0.0, 0.0, 0.0, 0.0};
+        for (int w = 0; w < 4; w++) {
+            uint32_t x = 0;
 #pragma unroll
-            for (int s = 0; s < NB; s++) {
-                // lane (g, r): elements 16 (g & 1) .. of block s of row r; g < 2
-                // their positive parts, to meet the largest keys, else the negative
-                float v[16], big = 0.0f;
-                {
-                    float x[8];
-                    load_x8<DT>(x, a.q, at + 32 * s + 16 * (g & 1));
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        v[e] = x[e];
-                    load_x8<DT>(x, a.q, at + 32 * s + 16 * (g & 1) + 8);
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        v[8 + e] = x[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    v[e] = v[e] != v[e] ? 0.0f : fminf(fmaxf(v[e], -3.0e38f), 3.0e38f);
-                    big = fmaxf(big, fabsf(v[e]));
-                }
-                big = fmaxf(big, __shfl_xor(big, 16));
-                const float d = big / 127.0f, inv = d > 0x1p-100f ? 1.0f / d : 0.0f;
-                i4 q;
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t x = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int c = round_away(v[4 * w + e], inv);
-                        x |= ((uint32_t)(g < 2 ? max(c, 0) : min(c, 0)) & 0xFFu) << (8 * e);
-                    }
-                    q[w] = (int)x;
-                }
-                // pages in the rows of the result, queries in its columns (lanes)
-                const i4 dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(codes[s], q, i4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float ds = __shfl(scale[s], 4 * g + e);
-                    sum[e] += (double)dot[e] * ((double)d * (double)ds);
-                }
+            for (int e = 0; e < 4; e++) {
+                const int c = round_away(v[w >> 1][4 * (w & 1) + e], inv);
+                x |= ((uint32_t)(g < 2 ? max(c, 0) : min(c, 0)) & 0xFFu) << (8 * e);
             }
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                best[e] = fmax(best[e], sum[e]);
+            q[w] = (int)x;
         }
-        const uint64_t mapped = __ballot(there);
+        l.code[tile][s][lane] = q;
+        if (g == 0)
+            l.scale[tile][s][r] = (double)d;
+    }
+}
+
+// One page a lane r: bytes 16g .. of its blocks' codes, and the scales.
+template <int D> struct PageBounds {
+    i4 code[D / 32];
+    uint16_t scale[D / 32];
+    bool there;
+};
+
+template <int D>
+__device__ __forceinline__ void load_bounds(PageBounds<D> &p, const SelectArgs &a, int64_t id, int h,
+                                            int g)
+{
+    constexpr int NB = D / 32;
+    p.there = id >= 0 && id < a.pages;
+    const int64_t block = ((p.there ? id : 0) * a.kv_heads + h) * NB;
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            for (int m = 1; m < 16; m <<= 1)
-                best[e] = fmax(best[e], __shfl_xor(best[e], m));
-            const int64_t p = p0 + 4 * g + e;
-            // a page that is not there comes last
-            if (r == 0 && p < sp.tail)
-                out[p] = (mapped >> (4 * g + e)) & 1 ? order_key((float)best[e]) : 0u;
+    for (int s = 0; s < NB; s++) {
+        p.code[s] = *(const i4 *)(a.codes + (block + s) * 64 + g * 16);
+        p.scale[s] = a.scales[block + s];
+    }
+}
+
+// Scores of pages [begin, end), 16 a wave and turn, as order keys into keys[page].
+// With AHEAD the next turn's bounds are on their way while this one's are scored.
+template <int DT, int D, int W, bool AHEAD>
+__device__ __forceinline__ void score_pages(QueryLds<D> &l, const SelectArgs &a, const Span &sp, int h,
+                                            int begin, int end, uint32_t *keys)
+{
+    constexpr int NB = D / 32, RT = row_tiles(D);
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t *table = a.table + (blockIdx.x / a.kv_heads) * a.table_stride;
+    const int rows = sp.T * a.group;
+    for (int r0 = 0; r0 < max(rows, 1); r0 += 16 * RT) {
+        const int tiles = min((rows - r0 + 15) / 16, RT);
+        int p0 = begin + wave * 16;
+        PageBounds<D> now, next;
+        if (p0 < end)
+            load_bounds<D>(now, a, table[min(p0 + r, end - 1)], h, g);
+        if (r0)
+            __syncthreads();                     // the rows before have been read
+        quantize_rows<DT, D, W>(l, a, sp, h, r0, tiles);
+        __syncthreads();
+        for (; p0 < end; p0 += W * 16) {
+            const int p1 = p0 + W * 16;
+            if (AHEAD && p1 < end)
+                load_bounds<D>(next, a, table[min(p1 + r, end - 1)], h, g);
+            double best = -__builtin_inf();
+            for (int t = 0; t < tiles; t++) {
+                double sum[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+                for (int s = 0; s < NB; s++) {
+                    // queries in the rows of the result, pages in its columns (lanes)
+                    const i4 dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(l.code[t][s][lane], now.code[s],
+                                                                       i4{0, 0, 0, 0}, 0, 0, 0);
+                    const double page = (double)f16_bits_to_f32(now.scale[s]);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        sum[e] += (double)dot[e] * (l.scale[t][s][4 * g + e] * page);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    best = fmax(best, sum[e]);
+            }
+            // rounding keeps the order: the largest is rounded, whatever comes first
+            float score = (float)best;
+            score = fmaxf(score, __shfl_xor(score, 16));
+            score = fmaxf(score, __shfl_xor(score, 32));
+            if (g == 0 && p0 + r < end) {
+                // a page that is not there comes last
+                const uint32_t key = now.there ? order_key(score) : 0u;
+                keys[p0 + r] = r0 ? max(keys[p0 + r], key) : key;
+            }
+            if (AHEAD)
+                now = next;
+            else if (p1 < end)
+                load_bounds<D>(now, a, table[min(p1 + r, end - 1)], h, g);
         }
     }
 }
 
 // ---- choice ----------------------------------------------------------------
 
-// One workgroup for each sequence and key head: the key of the last page that
-// is kept, eight bits at a time, then the pages in order.
-__global__ __launch_bounds__(SEL_THREADS) void k_select(SelectArgs a, const uint32_t *all_keys)
+template <int W> struct ChoiceLds {
+    uint32_t count[64 * W], scan[2][W];
+    uint32_t least, most, before, own;
+    int sub;
+};
+
+// The pages that are kept, in order, by a workgroup: those of the span's ends, and
+// the `keep` largest keys of the others.  Sub-bins of the keys' range, one a thread,
+// bring it down to the one that the last kept page is in, and so on inside that, until it is
+// kept whole or its keys are all equal: two turns as a rule.
+template <int W>
+__device__ __forceinline__ void choose(ChoiceLds<W> &l, const SelectArgs &a, const Span &sp, int b,
+                                       int h, const uint32_t *keys)
 {
-    __shared__ uint32_t count[256], scan[SEL_WAVES];
-    __shared__ int hit;
-    __shared__ uint32_t before_hit;
+    constexpr int THREADS = 64 * W, SUBS = THREADS, LOG_SUBS = W == 16 ? 10 : (W == 8 ? 9 : 8);
+    static_assert(1 << LOG_SUBS == SUBS, "");
     const int tid = threadIdx.x;
-    const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
-    const Span sp = span_of(a, b);
     const int32_t *table = a.table + b * a.table_stride;
-    const uint32_t *keys = all_keys + (int64_t)blockIdx.x * a.table_pages;
     int32_t *out = a.out + ((int64_t)b * a.kv_heads + h) * a.width;
     const int cand = sp.tail - sp.first;
-    uint32_t key = 0, need = sp.keep;            // pages with larger keys, and `need` of this key
+    // kept: keys of lo and more but the last `drop` of those equal to lo
+    uint32_t lo = 0, need = sp.keep, ties = 0;
     if (sp.keep < cand && sp.keep > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256)
-                count[tid] = 0;
+        if (tid == 0) {
+            l.least = ~0u;
+            l.most = 0;
+        }
+        __syncthreads();
+        uint32_t least = ~0u, most = 0;
+        for (int i = sp.first + tid; i < sp.tail; i += THREADS) {
+            least = min(least, keys[i]);
+            most = max(most, keys[i]);
+        }
+        for (int d = 1; d < 64; d <<= 1) {
+            least = min(least, (uint32_t)__shfl_xor(least, d));
+            most = max(most, (uint32_t)__shfl_xor(most, d));
+        }
+        if ((tid & 63) == 0) {
+            atomicMin(&l.least, least);
+            atomicMax(&l.most, most);
+        }
+        __syncthreads();
+        lo = l.least;
+        most = l.most;                           // keys lo .. most are in question
+        for (;;) {
+            const uint32_t span = most - lo;
+            const int shift = max(32 - __builtin_clz(span | 1) - LOG_SUBS, 0);
+            l.count[tid] = 0;
             __syncthreads();
-            for (int i = sp.first + tid; i < sp.tail; i += SEL_THREADS) {
+            for (int i = sp.first + tid; i < sp.tail; i += THREADS) {
                 const uint32_t k = keys[i];
-                if (shift == 24 || (k >> (shift + 8)) == key >> (shift + 8))
-                    atomicAdd(&count[(k >> shift) & 255], 1u);
+                if (k >= lo && k <= most)
+                    atomicAdd(&l.count[(k - lo) >> shift], 1u);
             }
             __syncthreads();
-            const uint32_t own = tid < 256 ? count[255 - tid] : 0;
+            // from the highest sub-bin down, one a thread
+            const uint32_t own = l.count[SUBS - 1 - tid];
             uint32_t all;
-            const uint32_t before = scan_before<SEL_WAVES>(own, scan, all);
+            const uint32_t before = scan_before<W>(own, l.scan[0], all);
             if (before < need && before + own >= need) {
-                hit = 255 - tid;
-                before_hit = before;
+                l.sub = SUBS - 1 - tid;
+                l.before = before;
+                l.own = own;
             }
             __syncthreads();
-            key |= (uint32_t)hit << shift;
-            need -= before_hit;
+            need -= l.before;
+            lo += (uint32_t)l.sub << shift;
+            ties = l.own;
+            const bool done = shift == 0 || ties == need;
+            most = shift == 0 ? lo : min(most, lo + ((1u << shift) - 1));
             __syncthreads();
+            if (done)
+                break;
         }
     }
-    // pages in order: all up to `first` and from `tail` on
-    uint32_t written = 0, ties = 0;
-    for (int base = 0; base < sp.total; base += SEL_THREADS) {
+    // with ties: keys above `most` are kept, of those in lo .. most (all equal, or
+    // all kept) the first `need`
+    const bool partly = ties != need;
+    uint32_t written = 0, met = 0;
+    for (int base = 0; base < sp.total; base += THREADS) {
         const int i = base + tid;
         bool take = i < sp.total;
         uint32_t tie = 0;
         if (take && i >= sp.first && i < sp.tail && sp.keep < cand) {
-            const uint32_t k = keys[i];
-            tie = sp.keep > 0 && k == key;
-            take = sp.keep > 0 && k > key;
+            const uint32_t k = sp.keep > 0 ? keys[i] : 0;
+            take = sp.keep > 0 && k >= lo;
+            tie = take && partly && k == lo;
         }
         uint32_t all;
-        const uint32_t tb = ties + scan_before<SEL_WAVES>(tie, scan, all);
-        ties += all;
-        __syncthreads();
-        take = take || (tie && tb < need);
-        const uint32_t at = written + scan_before<SEL_WAVES>((uint32_t)take, scan, all);
+        if (partly) {
+            const uint32_t rank = met + scan_before<W>(tie, l.scan[0], all);
+            met += all;
+            take = take && (!tie || rank < need);
+        }
+        const uint32_t at = written + scan_before<W>((uint32_t)take, l.scan[1], all);
         written += all;
-        __syncthreads();
         if (take && at < (uint32_t)a.width)
             out[at] = table[i];
+        __syncthreads();
     }
-    for (int i = written + tid; i < a.width; i += SEL_THREADS)
+    for (int i = written + tid; i < a.width; i += THREADS)
         out[i] = -1;
     if (h == 0 && tid == 0)
         a.ctx_out[b] = sp.ctx - (int)((int64_t)(cand - sp.keep) << a.log_page);
+}
+
+// A workgroup for each sequence and key head scores its pages and chooses; their
+// keys stay in LDS.
+template <int DT, int D>
+__global__ __launch_bounds__(SEL_THREADS) void k_select(SelectArgs a)
+{
+    __shared__ QueryLds<D> q;
+    __shared__ uint32_t keys[MOST_KEYS];
+    __shared__ ChoiceLds<SEL_WAVES> l;
+    const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
+    const Span sp = span_of(a, b);
+    if (sp.keep < sp.tail - sp.first && sp.keep > 0)
+        score_pages<DT, D, SEL_WAVES, true>(q, a, sp, h, sp.first, sp.tail, keys);
+    choose<SEL_WAVES>(l, a, sp, b, h, keys);
+}
+
+// The same in two launches: a head's pages spread over gridDim.y workgroups, then
+// the choice.
+template <int DT, int D>
+__global__ __launch_bounds__(SCORE_THREADS) void k_scores(SelectArgs a, uint32_t *keys)
+{
+    __shared__ QueryLds<D> q;
+    const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
+    const Span sp = span_of(a, b);
+    const int cand = sp.tail - sp.first;
+    if (sp.keep == cand || sp.keep == 0)
+        return;
+    // whole turns of 16 pages a wave
+    const int turns = (cand + SCORE_WAVES * 16 - 1) / (SCORE_WAVES * 16);
+    const int each = (turns + gridDim.y - 1) / gridDim.y * (SCORE_WAVES * 16);
+    const int64_t begin = sp.first + (int64_t)blockIdx.y * each;
+    if (begin < sp.tail)
+        score_pages<DT, D, SCORE_WAVES, true>(q, a, sp, h, (int)begin,
+                                              (int)min(begin + each, (int64_t)sp.tail),
+                                              keys + (int64_t)blockIdx.x * a.table_pages);
+}
+
+__global__ __launch_bounds__(64 * CHOOSE_WAVES) void k_choose(SelectArgs a, const uint32_t *keys)
+{
+    __shared__ ChoiceLds<CHOOSE_WAVES> l;
+    const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
+    choose<CHOOSE_WAVES>(l, a, span_of(a, b), b, h, keys + (int64_t)blockIdx.x * a.table_pages);
 }
 
 template <int CT>
@@ -306,16 +430,31 @@ hipError_t bounds_d(int D, dim3 grid, const BoundsArgs &a, int pages, hipStream_
     return hipGetLastError();
 }
 
-template <int DT> hipError_t scores_d(int D, dim3 grid, const SelectArgs &a, uint32_t *keys, hipStream_t s)
+// keys: in scratch, or null for the form in one launch.
+template <int DT, int D>
+hipError_t select_dd(const SelectArgs &a, int64_t pages, uint32_t *keys, hipStream_t s)
+{
+    const dim3 units((unsigned)(a.batch * a.kv_heads));
+    if (!keys) {
+        k_select<DT, D><<<units, SEL_THREADS, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    const int64_t y = std::min<int64_t>((pages + SCORE_WAVES * 16 - 1) / (SCORE_WAVES * 16), 65535);
+    k_scores<DT, D><<<dim3(units.x, (unsigned)y), SCORE_THREADS, 0, s>>>(a, keys);
+    k_choose<<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t select_d(int D, const SelectArgs &a, int64_t pages, uint32_t *keys, hipStream_t s)
 {
     switch (D) {
-    case 64: k_scores<DT, 64><<<grid, THREADS, 0, s>>>(a, keys); break;
-    case 96: k_scores<DT, 96><<<grid, THREADS, 0, s>>>(a, keys); break;
-    case 128: k_scores<DT, 128><<<grid, THREADS, 0, s>>>(a, keys); break;
-    case 256: k_scores<DT, 256><<<grid, THREADS, 0, s>>>(a, keys); break;
-    default: return hipErrorInvalidValue;
+    case 64: return select_dd<DT, 64>(a, pages, keys, s);
+    case 96: return select_dd<DT, 96>(a, pages, keys, s);
+    case 128: return select_dd<DT, 128>(a, pages, keys, s);
+    case 256: return select_dd<DT, 256>(a, pages, keys, s);
     }
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -341,17 +480,15 @@ size_t select_scratch_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages
 hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, void *scratch, hipStream_t s)
 {
     const int64_t units = (int64_t)a.batch * a.kv_heads;
-    const int64_t pages = std::min<int64_t>((max_ctx >> a.log_page) + 1, a.table_pages);
-    const int64_t y = std::min<int64_t>((pages + 16 * WAVES - 1) / (16 * WAVES), 65535);
-    if (!grid_fits(units, SEL_THREADS))
+    if (!grid_fits(units, 64 * CHOOSE_WAVES))
         return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)units, (unsigned)y);
-    hipError_t e = a.dtype == TQ_BF16 ? scores_d<TQ_BF16>(D, grid, a, (uint32_t *)scratch, s)
-                                      : scores_d<TQ_F16>(D, grid, a, (uint32_t *)scratch, s);
-    if (e != hipSuccess)
-        return e;
-    k_select<<<dim3((unsigned)units), SEL_THREADS, 0, s>>>(a, (const uint32_t *)scratch);
-    return hipGetLastError();
+    const int64_t pages = std::min<int64_t>((max_ctx >> a.log_page) + 1, a.table_pages);
+    const int64_t turns = (pages + SEL_WAVES * 16 - 1) / (SEL_WAVES * 16) *
+                          (((int64_t)a.max_nodes * a.group + 15) / 16);
+    const bool alone = a.table_pages <= MOST_KEYS && (turns <= SPREAD_TURNS || units >= SPREAD_UNITS);
+    uint32_t *keys = alone ? nullptr : (uint32_t *)scratch;
+    return a.dtype == TQ_BF16 ? select_d<TQ_BF16>(D, a, pages, keys, s)
+                              : select_d<TQ_F16>(D, a, pages, keys, s);
 }
 
 }  // namespace tq

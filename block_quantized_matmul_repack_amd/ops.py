@@ -234,7 +234,7 @@ _turns = {}
 def _with_workspace(entry, device, st, need, *args):
     """entry(*args, workspace, its bytes, stream): its status."""
     if not need:
-        return entry(*args, None, 0, st)
+        return entry(*args, 0, 0, st)
     turn = _turns.get(st)
     if turn is None:
         turn = _turns.setdefault(st, threading.Lock())
@@ -660,8 +660,7 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
     _check_index(name, "ctx_lens", ctx_lens, B, dev)
     _check_index(name, "starts", starts, B + 1, dev)
     n_pages = _cache_pages(name, ctype, k_cache, v_cache, page_size, kv_heads, D, dev)
-    words = stride = 0
-    mp = None
+    words = stride = mp = 0
     if mask is not None:
         if mask.dim() != 2 or mask.dtype is not torch.int32 or mask.shape[0] < T or \
                 mask.get_device() != dev or (mask.shape[1] > 1 and mask.stride(1) != 1):
@@ -767,20 +766,19 @@ def plan_step(lens, new_tokens, owned, page_table, free_pages, free_count, page_
         _check_index(name, what, t, n, dev)
     if not 0 <= tokens <= 1 << 20:
         raise TiledqError(f"{name}: tokens must be in 0 .. 2^20, got {tokens}")
-    # one allocation; parts begin at multiples of four elements
-    sizes = (B + 1, tokens, tokens, B, B, 1)
-    at = [0]
-    for n in sizes:
-        at.append(at[-1] + (n + 3 & ~3))
-    buf = torch.empty(at[-1], dtype=torch.int32, device=page_table.device)
+    # one allocation, in parts
+    buf = torch.empty(3 * B + 2 * tokens + 2, dtype=torch.int32, device=page_table.device)
     base = buf.data_ptr()
+    rows, slots = base + 4 * (B + 1), base + 4 * (B + 1 + tokens)
+    state = slots + 4 * tokens
     status = lib().tq_plan_step(
         B, lens.data_ptr(), new_tokens.data_ptr(), owned.data_ptr(), page_table.data_ptr(),
-        strides[0], width, page_size, free_pages.data_ptr(), free_pages.shape[0],
-        free_count.data_ptr(), tokens, *(base + 4 * a for a in at[:-1]), _stream_of(dev))
+        strides[0], width, page_size, free_pages.data_ptr(), free_pages.numel(),
+        free_count.data_ptr(), tokens, base, rows, slots, state, state + 4 * B, state + 8 * B,
+        _stream_of(dev))
     if status:
         check(status, name)
-    return tuple(buf[a:a + n] for a, n in zip(at, sizes))
+    return buf.split((B + 1, tokens, tokens, B, B, 1))
 
 
 def release_pages(done, owned, page_table, free_pages, free_count):
@@ -836,7 +834,7 @@ def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0,
         _refuse(name, "y", f"{tuple(shape)} fp32, bf16 or fp16", y)
     y_ts = _rows_of(name, "y", y, shape, y.dtype, dev)
     wtype = None
-    ptr = [None, None, None]
+    ptr = [0, 0, 0]
     for i, (what, w) in enumerate((("post_weight", post_weight), ("pre_weight", pre_weight),
                                    ("gate", gate))):
         if w is None:
@@ -861,8 +859,7 @@ def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0,
         xo_ts = N
     else:
         xo_ts = _rows_of(name, "x_out", x_out, shape, x.dtype, dev)
-    zp = qp = dp = None
-    z_ts = 0
+    zp = qp = dp = z_ts = 0
     if quantize:
         if z_out is None:
             z_out = (torch.empty(shape, dtype=torch.int8, device=x.device),
@@ -907,7 +904,7 @@ def _sample_args(name, logits, settings):
         if t is not None and (t.dtype is not dtype or t.dim() != 1 or t.shape[0] < N or
                               t.get_device() != dev or not t.is_contiguous()):
             _refuse(name, what, f"contiguous {dtype}, 1-D, >= {N} elements, on device {dev}", t)
-        ptr.append(None if t is None else t.data_ptr())
+        ptr.append(0 if t is None else t.data_ptr())
     return code, dev, N, V, ptr
 
 

@@ -715,6 +715,17 @@ int tq_tree_attention_heads(int type, int dtype, const void *q, int64_t q_ts, in
                             int64_t max_ctx, float scale, void *out, int64_t o_ts, int64_t o_hs,
                             void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* The calls above for bindings that pay for every argument of a foreign call: args
+ * holds the named entry point's arguments in order, each in 8 bytes (integers and
+ * addresses sign-extended, a float's bits in the low 4), read before it returns.
+ * Unknown `which`: TQ_E_TYPE. */
+typedef enum {
+    TQ_CALL_TREE_ATTENTION = 0, TQ_CALL_TREE_ATTENTION_HEADS = 1, TQ_CALL_PLAN_STEP = 2,
+    TQ_CALL_RELEASE_PAGES = 3, TQ_CALL_RESIDUAL_NORM = 4, TQ_CALL_SAMPLE = 5,
+    TQ_CALL_SAMPLE_PROBS = 6, TQ_CALL_CACHE_BOUNDS = 7, TQ_CALL_SELECT_PAGES = 8
+} tq_call;
+int tq_packed(int which, const int64_t *args);
+
 /* Which HIP graph capture `stream` is part of: *id becomes 0 outside one, else
  * a number that no other capture of the process has.  For callers that keep a
  * workspace: one allocated and cleared inside a capture belongs to its graph,
