@@ -390,15 +390,15 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 // k_probs writes the distribution instead.
 // A vocabulary of one tile takes one launch (k_one) and no scratch.  Rows that the
 // grid does not suit (logits far above the temperature) or whose list does not fit
-// (thousands of equal logits) are left to the search through the whole row, by
-// k_cut's workgroup.
+// (tens of thousands of logits within 2 %, or thousands of equal ones) are left to
+// the search through the whole row, by k_cut's workgroup: 0.4 ms for 128001.
 
 // 32 in the exponent and more weigh nothing (2^-46); a bin more for the grid.
 constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int MASS_BITS = 17;                    // of a bin's first weight: 16384 elements fit 32 bits
 constexpr int MOST_TILES = 64;
-constexpr int LIST = 4096, SHORT = 128, SUBS = THREADS;
-constexpr int MOST_ROWS = 4096;                  // of one launch; more take several
+constexpr int LIST = 32768, TILE_LIST = 8192;    // entries of a row, and of a tile of it
+constexpr int SHORT = 128, SUBS = THREADS, MOST_ALIKE = 4096;
 
 // Exact weights: kept: surely, and heavy enough for min-p; below: surely inside
 // top-p, were there no min-p; limit: what top-p is a part of.  All without the list.
@@ -778,7 +778,7 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
 template <int PER, int DT>
 __global__ __launch_bounds__(THREADS, 8) void k_gather(SampleArgs a, RowScratch *scratch)
 {
-    __shared__ uint64_t list[LIST], sums[3][WAVES];
+    __shared__ uint64_t list[TILE_LIST], sums[3][WAVES];
     __shared__ uint32_t listed, base;
     const int tid = threadIdx.x, tile = blockIdx.x;
     const int64_t row = blockIdx.y, i0 = ((int64_t)tile * THREADS + tid) * PER;
@@ -793,25 +793,27 @@ __global__ __launch_bounds__(THREADS, 8) void k_gather(SampleArgs a, RowScratch 
     if (tid == 0)
         listed = 0;
     __syncthreads();
-    const Sums all = sum_up(gather(x, i0, top, s, g, list, LIST, &listed), sums);
+    const Sums all = sum_up(gather(x, i0, top, s, g, list, TILE_LIST, &listed), sums);
     const uint32_t n = listed;
     if (tid == 0) {
         r.sums[tile] = all;
+        // more than fit here do not fit there
         if (n)
-            base = atomicAdd(&r.listed, n);
+            base = atomicAdd(&r.listed, n > TILE_LIST ? LIST + 1 : n);
     }
     if (n) {
         __syncthreads();
-        for (uint32_t i = tid; i < min(n, (uint32_t)LIST) && base + i < LIST; i += THREADS)
+        for (uint32_t i = tid; i < min(n, (uint32_t)TILE_LIST) && base + i < LIST; i += THREADS)
             r.list[base + i] = list[i];
     }
 }
 
 struct CutLds {
-    uint64_t list[LIST], weight[LIST];
+    uint64_t list[THREADS];                      // the first entries
+    uint64_t weight[SHORT];
     uint32_t sub_count[SUBS];
     uint64_t sub_mass[SUBS];
-    uint64_t in_sub[LIST];                       // those of one sub-bin
+    uint64_t in_sub[MOST_ALIKE];                 // those of one sub-bin
     uint64_t tile_kept[MOST_TILES];
     uint64_t scan[WAVES];
     uint32_t scan32[WAVES];
@@ -828,39 +830,62 @@ struct Ranked {
     uint64_t before;
 };
 
-// Entries of sub-bin `sub` and, for each that a thread has (list[tid + ...]), how
-// many and how much of them come before it.
+// The entries of sub-bin `sub`, each with how many and how much of the list come
+// before it; false (nothing done) if they do not fit.
 template <typename F>
-__device__ __forceinline__ void rank_in(CutLds &l, uint32_t n, int sub, uint32_t least, int shift,
-                                        float top, const Setting &s, F f)
+__device__ __forceinline__ bool rank_in(CutLds &l, const uint64_t *list, uint32_t n, int sub,
+                                        uint32_t least, int shift, float top, const Setting &s, F f)
 {
     const int tid = threadIdx.x;
     if (tid == 0)
         l.n_in = 0;
     __syncthreads();
-    for (uint32_t i = tid; i < n; i += THREADS)
-        if ((int)(((uint32_t)(l.list[i] >> 32) - least) >> shift) == sub)
-            l.in_sub[atomicAdd(&l.n_in, 1u)] = l.list[i];
+    for (uint32_t i = tid; i < n; i += THREADS) {
+        const uint64_t e = list[i];
+        if ((int)(((uint32_t)(e >> 32) - least) >> shift) == sub) {
+            const uint32_t at = atomicAdd(&l.n_in, 1u);
+            if (at < MOST_ALIKE)
+                l.in_sub[at] = e;
+        }
+    }
     __syncthreads();
     const uint32_t m = l.n_in, rank0 = l.sub_before;
     const uint64_t before0 = l.sub_mass_before;
-    for (uint32_t i = tid; i < m; i += THREADS) {
-        const uint64_t e = l.in_sub[i];
-        uint32_t rank = rank0, same = 0;
-        uint64_t before = before0;
-        for (uint32_t j = 0; j < m; j++) {
-            const uint64_t o = l.in_sub[j];
-            const bool ahead = o < e;
-            rank += ahead;
-            // equal logits weigh alike; the others are looked up
-            const bool alike = (uint32_t)(o >> 32) == (uint32_t)(e >> 32);
-            same += ahead && alike;
-            if (ahead && !alike)
-                before += weight(entry_value(o), top, s);
+    if (m > MOST_ALIKE)
+        return false;
+    // sorted by exchanges: each stretch of k entries is made a rising or falling one of
+    // two halves that are (1024 equal logits: 20 us; counting for each what comes
+    // before it takes 100)
+    uint32_t P = 1;
+    while (P < m)
+        P *= 2;
+    for (uint32_t i = m + tid; i < P; i += THREADS)
+        l.in_sub[i] = ~uint64_t(0);
+    for (uint32_t k = 2; k <= P; k *= 2)
+        for (uint32_t j = k / 2; j; j /= 2) {
+            __syncthreads();
+            for (uint32_t t = tid; t < P / 2; t += THREADS) {
+                const uint32_t i = 2 * t - (t & (j - 1));
+                const uint64_t x = l.in_sub[i], y = l.in_sub[i + j];
+                if ((x > y) == ((i & k) == 0)) {
+                    l.in_sub[i] = y;
+                    l.in_sub[i + j] = x;
+                }
+            }
         }
-        const uint64_t w = weight(entry_value(e), top, s);
-        f(e, w, Ranked{rank, before + same * w});
+    __syncthreads();
+    const uint32_t each = (P + THREADS - 1) / THREADS;
+    uint64_t own = 0, sum;
+    for (uint32_t i = tid * each; i < min((tid + 1) * each, m); i++)
+        own += weight(entry_value(l.in_sub[i]), top, s);
+    uint64_t before = before0 + scan_before<WAVES>(own, l.scan, sum);
+    for (uint32_t i = tid * each; i < min((tid + 1) * each, m); i++) {
+        const uint64_t e = l.in_sub[i], w = weight(entry_value(e), top, s);
+        f(e, w, Ranked{rank0 + i, before});
+        before += w;
     }
+    __syncthreads();
+    return true;
 }
 
 // What a short list's cut is: threads in a row share an entry and count what comes
@@ -922,11 +947,12 @@ __device__ __forceinline__ Cut rank_short(CutLds &l, const Setting &s, const Ran
     return Cut{~(uint32_t)(l.cut >> 32), (int64_t)(uint32_t)l.cut};
 }
 
-// The cut, from the list in LDS (n entries); adds what is kept of it to the tiles'
-// sums.  Sub-bins of the list's own range, in falling order, bring it down to the
-// few elements around a cut; those are ranked one by one.
-__device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Range &g, uint32_t n,
-                                         const Sums &all, float top, int tile_size)
+// The cut, from the list (n entries); adds what is kept of it to the tiles' sums.
+// Sub-bins of the list's own range, in falling order, bring it down to the few
+// elements around a cut; those are ranked one by one.  false: too many are alike.
+__device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Range &g,
+                                          const uint64_t *list, uint32_t n, const Sums &all, float top,
+                                          int tile_size, Cut &c)
 {
     const int tid = threadIdx.x;
     const float rate = s.grid, place = floorf(top * rate);
@@ -943,15 +969,13 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
     uint32_t least = ~0u, most = 0, low = 0;
     uint64_t low_mass = 0;
     for (uint32_t i = tid; i < n; i += THREADS) {
-        const uint32_t k = (uint32_t)(l.list[i] >> 32);
-        const float x = key_value(~k);
-        const uint64_t w = weight(x, top, s);
-        l.weight[i] = w;
+        const uint32_t k = (uint32_t)(list[i] >> 32);
         least = min(least, k);
         most = max(most, k);
+        const float x = key_value(~k);
         if (k_cuts && bin_of(x, place, rate) < g.kbin) {
             low++;
-            low_mass += w;
+            low_mass += weight(x, top, s);
         }
     }
     for (int d = 1; d < 64; d <<= 1) {
@@ -963,17 +987,21 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
     if ((tid & 63) == 0) {
         atomicMin(&l.least, least);
         atomicMax(&l.most, most);
-        atomicAdd(&l.low, low);
-        atomicAdd(&l.low_mass, (unsigned long long)low_mass);
+        if (low) {
+            atomicAdd(&l.low, low);
+            atomicAdd(&l.low_mass, (unsigned long long)low_mass);
+        }
     }
     __syncthreads();
     least = l.least;
     const uint32_t span = l.most - least;
     const int shift = max(32 - __builtin_clz(span | 1) - 10, 0);     // SUBS = 2^10
     for (uint32_t i = tid; i < n; i += THREADS) {
-        const int sub = (int)(((uint32_t)(l.list[i] >> 32) - least) >> shift);
+        const uint64_t e = list[i];
+        const int sub = (int)(((uint32_t)(e >> 32) - least) >> shift);
         atomicAdd(&l.sub_count[sub], 1u);
-        atomicAdd((unsigned long long *)&l.sub_mass[sub], (unsigned long long)l.weight[i]);
+        atomicAdd((unsigned long long *)&l.sub_mass[sub],
+                  (unsigned long long)weight(entry_value(e), top, s));
     }
     __syncthreads();
     const uint32_t count = l.sub_count[tid];
@@ -985,61 +1013,69 @@ __device__ __forceinline__ Cut rank_list(CutLds &l, const Setting &s, const Rang
     // top-k keeps k_rank entries of the list: those above kbin and some in it
     const uint32_t k_rank = k_cuts ? (uint32_t)s.k - g.k_before + l.low : ~0u;
     uint64_t total = all.limit;
-    if (k_cuts) {
-        if (count && before < k_rank)
-            atomicMax(&l.k_sub, tid);
+    if (k_cuts && s.p < 1.0) {
+        note_last(count && before < k_rank, tid, &l.k_sub);
         __syncthreads();
         if (tid == l.k_sub) {
             l.sub_before = before;
             l.sub_mass_before = mass_before;
         }
-        if (s.p < 1.0) {
-            rank_in(l, n, l.k_sub, least, shift, top, s, [&](uint64_t, uint64_t w, const Ranked &r) {
-                if (r.rank < k_rank)
-                    atomicAdd(&l.part, (unsigned long long)w);
-            });
-            __syncthreads();
-            total += l.sub_mass_before + l.part - l.low_mass;
-        }
+        if (!rank_in(l, list, n, l.k_sub, least, shift, top, s,
+                     [&](uint64_t, uint64_t w, const Ranked &r) {
+                         if (r.rank < k_rank)
+                             atomicAdd(&l.part, (unsigned long long)w);
+                     }))
+            return false;
+        total += l.sub_mass_before + l.part - l.low_mass;
     }
-    if (count && before < k_rank && inside(all.below + mass_before, s.p, total))
-        atomicMax(&l.p_sub, tid);
+    note_last(count && before < k_rank && inside(all.below + mass_before, s.p, total), tid, &l.p_sub);
     __syncthreads();
     if (tid == l.p_sub) {
         l.sub_before = before;
         l.sub_mass_before = mass_before;
     }
-    rank_in(l, n, l.p_sub, least, shift, top, s, [&](uint64_t e, uint64_t, const Ranked &r) {
-        if (r.rank < k_rank && inside(all.below + r.before, s.p, total))
-            atomicMax(&l.cut, (unsigned long long)e);
-    });
-    __syncthreads();
+    if (!rank_in(l, list, n, l.p_sub, least, shift, top, s,
+                 [&](uint64_t e, uint64_t, const Ranked &r) {
+                     if (r.rank < k_rank && inside(all.below + r.before, s.p, total))
+                         atomicMax(&l.cut, (unsigned long long)e);
+                 }))
+        return false;
     const uint64_t cut = l.cut;
-    for (uint32_t i = tid; i < n; i += THREADS)
-        if (l.list[i] <= cut && l.weight[i] >= s.min_w)
-            atomicAdd((unsigned long long *)&l.tile_kept[(uint32_t)l.list[i] / tile_size],
-                      (unsigned long long)l.weight[i]);
+    for (uint32_t i = tid; i < n; i += THREADS) {
+        const uint64_t e = list[i];
+        const uint64_t w = e <= cut ? weight(entry_value(e), top, s) : 0;
+        if (w && w >= s.min_w)
+            atomicAdd((unsigned long long *)&l.tile_kept[(uint32_t)e / tile_size],
+                      (unsigned long long)w);
+    }
     __syncthreads();
-    return Cut{~(uint32_t)(cut >> 32), (int64_t)(uint32_t)cut};
+    c = Cut{~(uint32_t)(cut >> 32), (int64_t)(uint32_t)cut};
+    return true;
 }
 
-// A row's end: from the sums (in tile_kept, too) and the list in LDS to its token, or
-// to its cut and the sum of what is kept.  x: tile `mine`'s elements, or none (-1).
+// A row's end: from the sums (in tile_kept, too) and the list (its first entries in
+// LDS, too) to its token, or to its cut and the sum of what is kept.  x: tile
+// `mine`'s elements, or none (-1).
 template <int PER, int DT>
 __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, CutLds &l, RowLds &rl,
                                            const Setting &s, const Range &g, const Sums &all,
-                                           uint32_t n, float top, int tiles, Cut &c,
+                                           const uint64_t *list, uint32_t n, uint32_t most,
+                                           float top, int tiles, Cut &c,
                                            float (&x)[PER], int mine)
 {
     const int tid = threadIdx.x, lane = tid & 63;
-    if (g.odd || n > LIST) {
+    bool ranked = !g.odd && n <= most;
+    if (ranked && n) {
+        if (n <= SHORT)
+            c = rank_short(l, s, g, n, all, top, PER * THREADS);
+        else
+            ranked = rank_list(l, s, g, n <= THREADS ? l.list : list, n, all, top, PER * THREADS, c);
+    }
+    if (!ranked) {
         const Walker walker{a.logits, row * a.stride, a.vocab, a.dtype, top};
         c = find_cut(walker, s, rl);
         return walk_row(a, walker, s, c, row, rl);
     }
-    if (n)
-        c = n <= SHORT ? rank_short(l, s, g, n, all, top, PER * THREADS)
-                       : rank_list(l, s, g, n, all, top, PER * THREADS);
     // the tile, then the element in it, where the running sum passes u
     const uint64_t v = lane < tiles ? l.tile_kept[lane] : 0, run = scan_wave(v);
     const uint64_t sum = lane_value(run, 63), thr = place_in(s.u, sum);
@@ -1109,11 +1145,9 @@ __global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scrat
             l.tile_kept[tid] = v.kept;
         }
         l.list[tid] = e0;
-        for (uint32_t i = THREADS + tid; i < min(n, (uint32_t)LIST); i += THREADS)
-            l.list[i] = r.list[i];
         const Sums all = sum_up(v, sums);
         float x[PER];
-        sum = finish<PER, DT>(a, row, l, rl, s, g, all, n, top, tiles, c, x, -1);
+        sum = finish<PER, DT>(a, row, l, rl, s, g, all, r.list, n, LIST, top, tiles, c, x, -1);
     }
     if (a.probs && tid == 0) {
         r.key = c.key;
@@ -1178,7 +1212,7 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
     __shared__ CutLds l;
     __shared__ RowLds rl;
     __shared__ RangeLds range;
-    __shared__ uint64_t bins[BINS], sums[3][WAVES];
+    __shared__ uint64_t bins[BINS], sums[3][WAVES], list[PER * THREADS];
     __shared__ int first;
     __shared__ uint32_t listed;
     const int tid = threadIdx.x;
@@ -1227,12 +1261,14 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
                 g.odd = 1;
             }
         }
-        const Sums all = sum_up(gather(x, i0, top, s, g, l.list, LIST, &listed), sums);
+        const Sums all = sum_up(gather(x, i0, top, s, g, list, PER * THREADS, &listed), sums);
         const uint32_t n = listed;
-        if (tid == 0)
-            l.tile_kept[0] = all.kept;
+        if (tid < MOST_TILES)
+            l.tile_kept[tid] = tid ? 0 : all.kept;
+        if (tid < n)
+            l.list[tid] = list[tid];
         __syncthreads();
-        sum = finish<PER, DT>(a, row, l, rl, s, g, all, n, top, 1, c, x, 0);
+        sum = finish<PER, DT>(a, row, l, rl, s, g, all, list, n, PER * THREADS, top, 1, c, x, 0);
     }
     if (a.probs)
         write_probs(a, row, i0, x, top, s, c, sum);
@@ -1248,14 +1284,22 @@ int64_t tiles_of(int64_t vocab)
     return (vocab + size - 1) / size;
 }
 
+// Rows of one launch: those whose scratch takes up to 256 MiB (several hundred).
+size_t row_bytes(int64_t tiles) { return sizeof(RowScratch) + tiles * BINS * sizeof(uint64_t); }
+
+int64_t rows_a_launch(int64_t rows, int64_t tiles)
+{
+    return std::min<int64_t>(rows, std::max<int64_t>(1, (int64_t(256) << 20) / row_bytes(tiles)));
+}
+
 template <int PER, int DT>
 hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t s)
 {
+    const int64_t rows = a.rows, most = rows_a_launch(rows, tiles), size = DT == TQ_F32 ? 4 : 2;
     RowScratch *r = (RowScratch *)scratch;
-    uint64_t *planes = (uint64_t *)(r + std::min<int64_t>(a.rows, MOST_ROWS));
-    const int64_t rows = a.rows, size = DT == TQ_F32 ? 4 : 2;
-    for (int64_t at = 0; at < rows; at += MOST_ROWS) {
-        const int64_t n = std::min<int64_t>(rows - at, MOST_ROWS);
+    uint64_t *planes = (uint64_t *)(r + most);
+    for (int64_t at = 0; at < rows; at += most) {
+        const int64_t n = std::min(rows - at, most);
         const dim3 grid((unsigned)tiles, (unsigned)n);
         k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
         k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)tiles);
@@ -1266,14 +1310,14 @@ hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        a.logits = (const uint8_t *)a.logits + MOST_ROWS * a.stride * size;
-        a.temperature += a.temperature ? MOST_ROWS : 0;
-        a.top_k += a.top_k ? MOST_ROWS : 0;
-        a.top_p += a.top_p ? MOST_ROWS : 0;
-        a.min_p += a.min_p ? MOST_ROWS : 0;
-        a.u += a.u ? MOST_ROWS : 0;
-        a.tokens += a.tokens ? MOST_ROWS : 0;
-        a.probs += a.probs ? MOST_ROWS * a.probs_stride : 0;
+        a.logits = (const uint8_t *)a.logits + most * a.stride * size;
+        a.temperature += a.temperature ? most : 0;
+        a.top_k += a.top_k ? most : 0;
+        a.top_p += a.top_p ? most : 0;
+        a.min_p += a.min_p ? most : 0;
+        a.u += a.u ? most : 0;
+        a.tokens += a.tokens ? most : 0;
+        a.probs += a.probs ? most * a.probs_stride : 0;
     }
     return hipSuccess;
 }
@@ -1297,10 +1341,8 @@ template <int DT> hipError_t launch_dt(const SampleArgs &a, void *scratch, hipSt
 
 size_t sample_scratch_bytes(int64_t rows, int64_t vocab)
 {
-    const int64_t tiles = tiles_of(vocab), n = std::min<int64_t>(rows, MOST_ROWS);
-    return tiles == 1 || tiles > MOST_TILES
-               ? 0
-               : (size_t)n * (sizeof(RowScratch) + tiles * BINS * sizeof(uint64_t));
+    const int64_t tiles = tiles_of(vocab);
+    return tiles == 1 || tiles > MOST_TILES ? 0 : rows_a_launch(rows, tiles) * row_bytes(tiles);
 }
 
 hipError_t launch_sample(const SampleArgs &a, void *scratch, hipStream_t s)

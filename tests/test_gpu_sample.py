@@ -187,3 +187,19 @@ def test_refusals():
             tq().sample(**{**dict(logits=x, uniforms=u), **bad})
     with pytest.raises(tq().TiledqError):
         tq().sample_probs(x, out=x[:2])
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 0.02, 0.1, 0.5])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_nearly_even_rows(scale, dtype):
+    """Thousands to all of a long row's elements near the cut."""
+    x, u = rows(5, 60001, dtype, scale)
+    check(x, u, [1.0, 2.0, 0.5, 3.0, 1.0], [0, 0, 30000, 7, 0], [0.95, 0.5, 0.9, 1.0, 0.02])
+
+
+def test_more_rows_than_a_launch_takes():
+    """Hundreds of rows of several tiles, their settings each their own."""
+    x, u = rows(700, 17000)
+    k = [(i * 7) % 50 for i in range(700)]
+    p = [0.5 + 0.0007 * i for i in range(700)]
+    check(x, u, [0.5 + 0.001 * i for i in range(700)], k, p)
