@@ -27,15 +27,22 @@ template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_bits(double 
     return __builtin_bit_cast(double, dpp_bits<CTRL, ROWS>(__builtin_bit_cast(uint64_t, x)));
 }
 
-// Running sum over the lanes of a wave: shifts by 1, 2, 4, 8 in each row of 16
-// lanes, then the last lane of a row added to the rows behind it.  Lanes that a
-// step brings nothing to add 0.
-template <typename T> __device__ __forceinline__ T scan_wave(T v)
+// Running sum over each row of 16 lanes: shifts by 1, 2, 4, 8.  Lanes that a step
+// brings nothing to add 0.
+template <typename T> __device__ __forceinline__ T scan_row(T v)
 {
     v += dpp_bits<0x111, 0xF>(v);
     v += dpp_bits<0x112, 0xF>(v);
     v += dpp_bits<0x114, 0xF>(v);
     v += dpp_bits<0x118, 0xF>(v);
+    return v;
+}
+
+// Running sum over the lanes of a wave: in rows, then the last lane of a row added to
+// the rows behind it.
+template <typename T> __device__ __forceinline__ T scan_wave(T v)
+{
+    v = scan_row(v);
     v += dpp_bits<0x142, 0xA>(v);
     v += dpp_bits<0x143, 0xC>(v);
     return v;
@@ -81,20 +88,23 @@ __device__ __forceinline__ float wave_max(float v)
 template <int WAVES, typename T>
 __device__ __forceinline__ T scan_before(T v, T *lds, T &all)
 {
+    static_assert(WAVES <= 16, "");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const T run = scan_wave(v);
     if (lane == 63)
         lds[wave] = run;
     __syncthreads();
-    T before = 0;
-    all = 0;
-#pragma unroll
-    for (int i = 0; i < WAVES; i++) {
-        const T x = lds[i];
-        before += i < wave ? x : T(0);
-        all += x;
-    }
-    return before + run - v;
+    // the waves' sums by lanes: fewer instructions than reading all of them in turn
+    const T upto = scan_row(lane < WAVES ? lds[lane] : T(0));
+    all = lane_value(upto, WAVES - 1);
+    const int w = __builtin_amdgcn_readfirstlane(wave);
+    return (w ? lane_value(upto, w - 1) : T(0)) + run - v;
+}
+
+// The sum of what lanes 0 .. n - 1 hold, n up to 16, in every lane.
+template <typename T> __device__ __forceinline__ T sum_lanes(T v, int n)
+{
+    return lane_value(scan_row((int)(threadIdx.x & 63) < n ? v : T(0)), 15);
 }
 
 // Unsigned numbers in the order of the floats; a NaN counts as -infinity, -0 as 0.

@@ -79,11 +79,8 @@ template <int WAVES> __device__ __forceinline__ float sum_all(float v, float *ld
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    float all = 0.0f;
-#pragma unroll
-    for (int i = 0; i < WAVES; i++)
-        all += lds[i];
-    return all;
+    const int lane = threadIdx.x & 63;
+    return sum_lanes(lane < WAVES ? lds[lane] : 0.0f, WAVES);
 }
 
 // WAVES waves hold a token, U units of eight elements a lane.

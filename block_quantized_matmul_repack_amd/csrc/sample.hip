@@ -58,19 +58,22 @@ __device__ __forceinline__ Setting setting_of(const SampleArgs &a, int64_t row)
 // for 2^f, |f| <= 1/2 (interpolated in Chebyshev's points, off by 2^-51).
 __device__ __forceinline__ double whole_exp2(double t)
 {
-    const double n = rint(t), f = t - n;
-    double p = 7.072585949269223e-09;
-    p = fma(p, f, 1.0208690299958306e-07);
-    p = fma(p, f, 1.321544258792169e-06);
-    p = fma(p, f, 1.5252657260200837e-05);
-    p = fma(p, f, 0.0001540353044173605);
-    p = fma(p, f, 0.0013333558230164974);
-    p = fma(p, f, 0.009618129107606888);
-    p = fma(p, f, 0.05550410866444772);
-    p = fma(p, f, 0.24022650695910097);
-    p = fma(p, f, 0.69314718055995);
+    // the coefficients in scalar registers: as literals each takes two moves
+    double c[10] = {7.072585949269223e-09, 1.0208690299958306e-07, 1.321544258792169e-06, 1.5252657260200837e-05,
+                    0.0001540353044173605, 0.0013333558230164974, 0.009618129107606888,
+                    0.05550410866444772, 0.24022650695910097, 0.69314718055995};
+#pragma unroll
+    for (int i = 0; i < 10; i++)
+        asm("" : "+s"(c[i]));
+    // with 1.5 * 2^52 added the whole part is in the low bits: no conversion
+    const double near = t + 0x1.8p52, f = t - (near - 0x1.8p52);
+    const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, near);
+    double p = c[0];
+#pragma unroll
+    for (int i = 1; i < 10; i++)
+        p = fma(p, f, c[i]);
     p = fma(p, f, 1.0);
-    const uint64_t scaled = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(uint32_t)(int)n << 52);
+    const uint64_t scaled = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(uint32_t)n << 52);
     return __builtin_bit_cast(double, scaled) + 0x1p52;
 }
 
@@ -334,8 +337,9 @@ __device__ __forceinline__ float max_all(float v, float *lds)
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    for (int i = 0; i < WAVES; i++)
-        v = fmaxf(v, lds[i]);
+    v = lds[threadIdx.x & (WAVES - 1)];
+    for (int m = 1; m < WAVES; m <<= 1)
+        v = fmaxf(v, __shfl_xor(v, m));
     return v;
 }
 
@@ -397,7 +401,8 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int MASS_BITS = 17;                    // of a bin's first weight: 16384 elements fit 32 bits
 constexpr int MOST_TILES = 64;
-constexpr int LIST = 32768, TILE_LIST = 8192;    // entries of a row, and of a tile of it
+constexpr int LIST = 32768;                      // entries of a row
+constexpr int GATHER_THREADS = 256;
 constexpr int SHORT = 128, SUBS = THREADS, MOST_ALIKE = 4096;
 
 // Exact weights: kept: surely, and heavy enough for min-p; below: surely inside
@@ -691,6 +696,8 @@ __global__ __launch_bounds__(THREADS) void k_range(SampleArgs a, RowScratch *scr
             g.odd = 1;
         }
     }
+    if (tid < tiles)
+        r.sums[tid] = Sums{0, 0, 0};
     if (tid == 0) {
         r.setting = s;
         r.range = g;
@@ -702,21 +709,16 @@ __global__ __launch_bounds__(THREADS) void k_range(SampleArgs a, RowScratch *scr
 // A workgroup's sums, to all of its threads.
 __device__ __forceinline__ Sums sum_up(Sums v, uint64_t (&lds)[3][WAVES])
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     v = {wave_sum(v.kept), wave_sum(v.below), wave_sum(v.limit)};
     if (lane == 0) {
-        lds[0][wave] = v.kept;
-        lds[1][wave] = v.below;
-        lds[2][wave] = v.limit;
+        lds[0][threadIdx.x >> 6] = v.kept;
+        lds[1][threadIdx.x >> 6] = v.below;
+        lds[2][threadIdx.x >> 6] = v.limit;
     }
     __syncthreads();
-    Sums all{0, 0, 0};
-    for (int i = 0; i < WAVES; i++) {
-        all.kept += lds[0][i];
-        all.below += lds[1][i];
-        all.limit += lds[2][i];
-    }
-    return all;
+    const int i = lane & (WAVES - 1);
+    return {sum_lanes(lds[0][i], WAVES), sum_lanes(lds[1][i], WAVES), sum_lanes(lds[2][i], WAVES)};
 }
 
 // Sums of a tile's elements by the range, and the list of those in question (of
@@ -753,14 +755,35 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
     const double min_w = (double)s.min_w;
     double kept = 0.0, below = 0.0, limit = 0.0;
     uint32_t question = 0;
+    if (g.kbin < BINS) {                         // top-k leaves few
 #pragma unroll
-    for (int e = 0; e < PER; e++) {
-        const double w = d[e] < end ? weight_in_bin(x[e], top, s) : 0.0;
-        limit += d[e] < kbin ? w : 0.0;
-        const double b = d[e] < lo ? w : 0.0;
-        below += b;
-        kept += b >= min_w ? b : 0.0;
-        question |= w > 0.0 && ((d[e] >= lo && d[e] <= hi) || d[e] == kbin) ? 1u << e : 0u;
+        for (int e = 0; e < PER; e++)
+            if (d[e] < end) {
+                const double w = weight_in_bin(x[e], top, s), b = d[e] < lo ? w : 0.0;
+                limit += d[e] < kbin ? w : 0.0;
+                below += b;
+                kept += b >= min_w ? b : 0.0;
+                question |= w > 0.0 && ((d[e] >= lo && d[e] <= hi) || d[e] == kbin) ? 1u << e : 0u;
+            }
+    } else {
+        // the weights of all without branches, for their instructions to overlap
+        double b[PER];
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            double w = weight_in_bin(x[e], top, s);
+            w = d[e] < end ? w : 0.0;
+            b[e] = d[e] < lo ? w : 0.0;
+            limit += w;
+            below += b[e];
+            question |= w > 0.0 && d[e] >= lo && d[e] <= hi ? 1u << e : 0u;
+        }
+        kept = below;
+        if (s.min_w) {
+            kept = 0.0;
+#pragma unroll
+            for (int e = 0; e < PER; e++)
+                kept += b[e] >= min_w ? b[e] : 0.0;
+        }
     }
     if (question) {
         uint32_t at = atomicAdd(listed, (uint32_t)__builtin_popcount(question));
@@ -775,13 +798,17 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
     return Sums{(uint64_t)kept, (uint64_t)below, (uint64_t)limit};
 }
 
+// Small workgroups, four for a tile, so that some load while others compute (64
+// rows of 128001, top-k and top-p: 6.6 us, one for a tile 8.5; top-p alone 18.8).
 template <int PER, int DT>
-__global__ __launch_bounds__(THREADS, 8) void k_gather(SampleArgs a, RowScratch *scratch)
+__global__ __launch_bounds__(GATHER_THREADS, PER == 8 ? 8 : 4) void k_gather(SampleArgs a, RowScratch *scratch)
 {
-    __shared__ uint64_t list[TILE_LIST], sums[3][WAVES];
+    constexpr int MOST = PER * GATHER_THREADS;
+    __shared__ uint64_t list[MOST];
+    __shared__ Sums sums[GATHER_THREADS / 64];
     __shared__ uint32_t listed, base;
-    const int tid = threadIdx.x, tile = blockIdx.x;
-    const int64_t row = blockIdx.y, i0 = ((int64_t)tile * THREADS + tid) * PER;
+    const int tid = threadIdx.x, tile = blockIdx.x / (THREADS / GATHER_THREADS);
+    const int64_t row = blockIdx.y, i0 = ((int64_t)blockIdx.x * GATHER_THREADS + tid) * PER;
     RowScratch &r = scratch[row];
     float x[PER];
     load_tile<PER, DT>(x, a, row, i0);
@@ -793,19 +820,31 @@ __global__ __launch_bounds__(THREADS, 8) void k_gather(SampleArgs a, RowScratch 
     if (tid == 0)
         listed = 0;
     __syncthreads();
-    const Sums all = sum_up(gather(x, i0, top, s, g, list, TILE_LIST, &listed), sums);
+    Sums v = gather(x, i0, top, s, g, list, MOST, &listed);
+    v = {wave_sum(v.kept), wave_sum(v.below), wave_sum(v.limit)};
+    if ((tid & 63) == 0)
+        sums[tid >> 6] = v;
+    __syncthreads();
     const uint32_t n = listed;
     if (tid == 0) {
-        r.sums[tile] = all;
-        // more than fit here do not fit there
-        if (n)
-            base = atomicAdd(&r.listed, n > TILE_LIST ? LIST + 1 : n);
+        for (int i = 1; i < GATHER_THREADS / 64; i++)
+            v = {v.kept + sums[i].kept, v.below + sums[i].below, v.limit + sums[i].limit};
+        // whole numbers: the order of the adds does not show
+        Sums &sum = r.sums[tile];
+        if (v.kept)
+            atomicAdd((unsigned long long *)&sum.kept, (unsigned long long)v.kept);
+        if (v.below)
+            atomicAdd((unsigned long long *)&sum.below, (unsigned long long)v.below);
+        if (v.limit)
+            atomicAdd((unsigned long long *)&sum.limit, (unsigned long long)v.limit);
     }
-    if (n) {
-        __syncthreads();
-        for (uint32_t i = tid; i < min(n, (uint32_t)TILE_LIST) && base + i < LIST; i += THREADS)
-            r.list[base + i] = list[i];
-    }
+    if (n == 0)
+        return;
+    if (tid == 0)
+        base = atomicAdd(&r.listed, n);
+    __syncthreads();
+    for (uint32_t i = tid; i < n && base + i < LIST; i += GATHER_THREADS)
+        r.list[base + i] = list[i];
 }
 
 struct CutLds {
@@ -1085,12 +1124,18 @@ __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, Cut
     const int64_t j0 = ((int64_t)tile * THREADS + tid) * PER;
     if (tile != mine)
         load_tile<PER, DT>(x, a, row, j0);
-    uint64_t w[PER], own = 0, whole;
+    uint64_t w[PER] = {}, own = 0, whole;
+    uint32_t in = 0;
 #pragma unroll
-    for (int e = 0; e < PER; e++) {
-        w[e] = kept(c, order_key(x[e]), j0 + e) ? weight(x[e], top, s) : 0;
-        w[e] = w[e] >= s.min_w ? w[e] : 0;
-        own += w[e];
+    for (int e = 0; e < PER; e++)
+        in |= kept(c, order_key(x[e]), j0 + e) ? 1u << e : 0u;
+    if (__any(in)) {
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            w[e] = weight(x[e], top, s);
+            w[e] = (in >> e & 1) && w[e] >= s.min_w ? w[e] : 0;
+            own += w[e];
+        }
     }
     __syncthreads();
     uint64_t at = lane_value(run - v, tile) + scan_before<WAVES>(own, l.scan, whole);
@@ -1303,7 +1348,8 @@ hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t 
         const dim3 grid((unsigned)tiles, (unsigned)n);
         k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
         k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)tiles);
-        k_gather<PER, DT><<<grid, THREADS, 0, s>>>(a, r);
+        k_gather<PER, DT><<<dim3((unsigned)(tiles * (THREADS / GATHER_THREADS)), (unsigned)n),
+                            GATHER_THREADS, 0, s>>>(a, r);
         k_cut<PER, DT><<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, (int)tiles);
         if (a.probs)
             k_probs<PER, DT><<<grid, THREADS, 0, s>>>(a, r);

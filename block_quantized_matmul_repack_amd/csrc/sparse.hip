@@ -410,11 +410,23 @@ __global__ __launch_bounds__(SCORE_THREADS) void k_scores(SelectArgs a, uint32_t
                                               keys + (int64_t)blockIdx.x * a.table_pages);
 }
 
+// IN_LDS: the keys are brought there first, for the turns over them.
+template <bool IN_LDS>
 __global__ __launch_bounds__(64 * CHOOSE_WAVES) void k_choose(SelectArgs a, const uint32_t *keys)
 {
     __shared__ ChoiceLds<CHOOSE_WAVES> l;
+    __shared__ uint32_t own[IN_LDS ? MOST_KEYS : 1];
     const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
-    choose<CHOOSE_WAVES>(l, a, span_of(a, b), b, h, keys + (int64_t)blockIdx.x * a.table_pages);
+    const Span sp = span_of(a, b);
+    const uint32_t *from = keys + (int64_t)blockIdx.x * a.table_pages;
+    if constexpr (IN_LDS) {
+        if (sp.keep < sp.tail - sp.first && sp.keep > 0)
+            for (int i = sp.first + threadIdx.x; i < sp.tail; i += 64 * CHOOSE_WAVES)
+                own[i] = from[i];
+        choose<CHOOSE_WAVES>(l, a, sp, b, h, own);
+    } else {
+        choose<CHOOSE_WAVES>(l, a, sp, b, h, from);
+    }
 }
 
 template <int CT>
@@ -441,7 +453,10 @@ hipError_t select_dd(const SelectArgs &a, int64_t pages, uint32_t *keys, hipStre
     }
     const int64_t y = std::min<int64_t>((pages + SCORE_WAVES * 16 - 1) / (SCORE_WAVES * 16), 65535);
     k_scores<DT, D><<<dim3(units.x, (unsigned)y), SCORE_THREADS, 0, s>>>(a, keys);
-    k_choose<<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
+    if (a.table_pages <= MOST_KEYS)
+        k_choose<true><<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
+    else
+        k_choose<false><<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
     return hipGetLastError();
 }
 

@@ -503,11 +503,20 @@ def _heads_of(name, what, t, dtypes):
     return shape, ts, hs, dev, code
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_of(dev):
     """The current HIP stream of GPU number dev, as an int handle."""
     if _raw_stream is not None:
-        return _raw_stream(dev)
-    return torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
+    else:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if not stream and _current_device() != dev:
+        # the null handle names the default stream of whichever device is current
+        raise TiledqError(f"the tensors are on device {dev} and its default stream is asked for: "
+                          "make that device the current one")
+    return stream
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
@@ -814,6 +823,14 @@ def _rows_of(name, what, t, shape, dtype, dev):
     return t.stride(0)
 
 
+def _norm_weight(name, what, w, N, dtype, dev):
+    if w.dtype is not dtype or dtype not in _DTYPES or w.get_device() != dev or w.dim() != 1 or \
+            w.numel() != N or not w.is_contiguous():
+        _refuse(name, what, f"contiguous fp32, bf16 or fp16 [{N}], the weights and the gate of one "
+                            f"type, on device {dev}", w)
+    return w.data_ptr()
+
+
 def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6,
                   quantize=False, x_out=None, z_out=None):
     """x' = scale * x + gate * p and z, in one pass: p is y [T, N] (fp32 / bf16 /
@@ -823,66 +840,67 @@ def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0,
     gate: [N], [T, N], [T, 1] or [1], of the weights' type.  x_out may be x.
     Returns (x', z) or (x', (q, d))."""
     name = "tq_residual_norm"
-    code = _DTYPES.get(x.dtype)
-    dev = x.get_device()
-    if x.dim() != 2 or code is None or dev < 0 or (x.shape[1] > 1 and x.stride(1) != 1):
-        _refuse(name, "x", "[tokens, N] fp32, bf16 or fp16 with contiguous rows", x)
-    shape = x.shape
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    code = _DTYPES.get(dtype)
+    if len(shape) != 2 or code is None or dev < 0:
+        _refuse(name, "x", "[tokens, N] fp32, bf16 or fp16", x)
     T, N = shape
+    x_ts, es = x.stride()
     ycode = _DTYPES.get(y.dtype)
-    if ycode is None or y.dim() != 2:
-        _refuse(name, "y", f"{tuple(shape)} fp32, bf16 or fp16", y)
+    if (es != 1 and N > 1) or ycode is None:
+        _refuse(name, "x", "of contiguous rows, y of fp32, bf16 or fp16", y if ycode is None else x)
     y_ts = _rows_of(name, "y", y, shape, y.dtype, dev)
     wtype = None
-    ptr = [0, 0, 0]
-    for i, (what, w) in enumerate((("post_weight", post_weight), ("pre_weight", pre_weight),
-                                   ("gate", gate))):
-        if w is None:
-            continue
-        if wtype is None:
-            wtype = w.dtype
-        if w.dtype is not wtype or wtype not in _DTYPES or w.get_device() != dev or \
-                (i < 2 and (w.dim() != 1 or w.shape[0] != N or not w.is_contiguous())):
-            _refuse(name, what, f"contiguous fp32, bf16 or fp16 [{N}], the weights and the gate of "
-                                f"one type, on device {dev}", w)
-        ptr[i] = w.data_ptr()
-    gate_ts = gate_es = 0
+    post = pre = gp = gate_ts = gate_es = 0
+    if post_weight is not None:
+        wtype = post_weight.dtype
+        post = _norm_weight(name, "post_weight", post_weight, N, wtype, dev)
+    if pre_weight is not None:
+        wtype = wtype or pre_weight.dtype
+        pre = _norm_weight(name, "pre_weight", pre_weight, N, wtype, dev)
     if gate is not None:
+        wtype = wtype or gate.dtype
         dims, gs = gate.dim(), gate.shape
         if dims not in (1, 2) or gs[-1] not in (1, N) or (dims == 2 and gs[0] not in (1, T)) or \
-                (gs[-1] > 1 and gate.stride(-1) not in (0, 1)):
-            _refuse(name, "gate", f"[{N}], [{T}, {N}], [{T}, 1] or [1] with contiguous rows", gate)
+                (gs[-1] > 1 and gate.stride(-1) not in (0, 1)) or gate.dtype is not wtype or \
+                wtype not in _DTYPES or gate.get_device() != dev:
+            _refuse(name, "gate", f"[{N}], [{T}, {N}], [{T}, 1] or [1] with contiguous rows, of the "
+                                  f"weights' type, on device {dev}", gate)
         gate_es = gate.stride(-1) if gs[-1] > 1 else 0
         gate_ts = gate.stride(0) if dims == 2 and gs[0] > 1 else 0
+        gp = gate.data_ptr()
     if x_out is None:
-        x_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        x_out = torch.empty(shape, dtype=dtype, device=x.device)
         xo_ts = N
     else:
-        xo_ts = _rows_of(name, "x_out", x_out, shape, x.dtype, dev)
+        xo_ts = _rows_of(name, "x_out", x_out, shape, dtype, dev)
     zp = qp = dp = z_ts = 0
     if quantize:
         if z_out is None:
-            z_out = (torch.empty(shape, dtype=torch.int8, device=x.device),
-                     torch.empty((T, N // 32), dtype=torch.float16, device=x.device))
-        q, d = z_out
-        if q.shape != shape or q.dtype is not torch.int8 or q.get_device() != dev or \
-                not q.is_contiguous():
-            _refuse(name, "q", f"contiguous int8 {tuple(shape)} on device {dev}", q)
-        if d.shape != (T, N // 32) or d.dtype is not torch.float16 or d.get_device() != dev or \
-                not d.is_contiguous():
-            _refuse(name, "d", f"contiguous float16 {(T, N // 32)} on device {dev}", d)
+            device = x.device
+            q = torch.empty(shape, dtype=torch.int8, device=device)
+            d = torch.empty((T, N // 32), dtype=torch.float16, device=device)
+            z_out = q, d
+        else:
+            q, d = z_out
+            if q.shape != shape or q.dtype is not torch.int8 or q.get_device() != dev or \
+                    not q.is_contiguous():
+                _refuse(name, "q", f"contiguous int8 {tuple(shape)} on device {dev}", q)
+            if d.shape != (T, N // 32) or d.dtype is not torch.float16 or \
+                    d.get_device() != dev or not d.is_contiguous():
+                _refuse(name, "d", f"contiguous float16 {(T, N // 32)} on device {dev}", d)
         qp, dp = q.data_ptr(), d.data_ptr()
     else:
         if z_out is None:
-            z_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+            z_out = torch.empty(shape, dtype=dtype, device=x.device)
             z_ts = N
         else:
-            z_ts = _rows_of(name, "z_out", z_out, shape, x.dtype, dev)
+            z_ts = _rows_of(name, "z_out", z_out, shape, dtype, dev)
         zp = z_out.data_ptr()
     status = lib().tq_residual_norm(
-        code, ycode, y.data_ptr(), y_ts, x.data_ptr(), x.stride(0), T, N,
-        _DTYPES.get(wtype, code), *ptr, gate_ts, gate_es, scale, eps, x_out.data_ptr(), xo_ts, zp,
-        z_ts, qp, dp, _stream_of(dev))
+        code, ycode, y.data_ptr(), y_ts, x.data_ptr(), x_ts, T, N,
+        code if wtype is None else _DTYPES[wtype], post, pre, gp, gate_ts, gate_es, scale, eps,
+        x_out.data_ptr(), xo_ts, zp, z_ts, qp, dp, _stream_of(dev))
     if status:
         check(status, name)
     return x_out, z_out
