@@ -96,7 +96,7 @@ size_t tq_tree_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t k
         !within(max_nodes, 1, MAX_TOKENS) || !within(max_ctx, 0, MAX_POSITIONS))
         return 0;
     const tq::AttnPlan p = tq::attn_plan((int)D, batch, heads, kv_heads, max_nodes,
-                                         max_ctx + max_nodes);
+                                         max_ctx + max_nodes, false);
     const size_t n = tq::attn_scratch_bytes(p, (int)D, batch, kv_heads);
     return n ? TQ_NOALLOC_SCRATCH_BYTES + n : 0;
 }
@@ -135,7 +135,7 @@ int attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs, in
         !aligned(mask, 4))
         return TQ_E_ALIGN;
     const tq::AttnPlan p = tq::attn_plan((int)D, batch, heads, kv_heads, max_nodes,
-                                         max_ctx + max_nodes);
+                                         max_ctx + max_nodes, table_head_stride != 0);
     uint32_t *counters;                          // unused: the layout that all calls share
     void *scratch;
     const int st = scratch_of(

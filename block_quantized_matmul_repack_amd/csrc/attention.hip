@@ -85,6 +85,9 @@ constexpr int FEW_UNITS = 256;
 // From OWN_UNITS on the chip is filled four times over by a workgroup for each,
 // and nothing is to be joined.
 constexpr int OWN_UNITS = 2048;
+// Of selected pages heads have about as many each: once they fill the chip
+// (two workgroups a unit) each takes a workgroup, too.
+constexpr int EVEN_UNITS = 512;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -1420,7 +1423,7 @@ hipError_t launch_c(int D, const AttnArgs &a, const AttnPlan &p, void *scratch, 
 }  // namespace
 
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
-                   int64_t max_keys)
+                   int64_t max_keys, bool even)
 {
     AttnPlan p{};
     const int64_t rows = max_nodes * (heads / kv_heads);
@@ -1448,7 +1451,7 @@ AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_
     p.waves = p.row_groups > 1 && D <= 128 && units <= FEW_UNITS ? 8 : 4;
     const int keys = p.waves * (p.row_groups > 1 ? 16 : STEP), least = MIN_KEYS / keys;
     const int64_t line = units * ((max_keys + keys - 1) / keys + least);
-    p.groups = units >= OWN_UNITS
+    p.groups = units >= (even ? EVEN_UNITS : OWN_UNITS)
                    ? 0
                    : (int)std::min<int64_t>(D > 128 || p.waves == 8 ? 256 : 512,
                                             std::max<int64_t>(1, line / least));

@@ -441,8 +441,9 @@ struct AttnArgs {
 struct AttnPlan {
     int waves, tiles, row_groups, row_blocks, groups, by_rows;
 };
+// even: sequences of about the same length are expected.
 AttnPlan attn_plan(int D, int64_t batch, int64_t heads, int64_t kv_heads, int64_t max_nodes,
-                   int64_t max_keys);
+                   int64_t max_keys, bool even);
 size_t attn_scratch_bytes(const AttnPlan &p, int D, int64_t batch, int64_t kv_heads);
 hipError_t launch_attention(int cache_type, int D, const AttnArgs &a, const AttnPlan &p,
                             void *scratch, hipStream_t s);
