@@ -88,6 +88,30 @@ def test_forms(gate, post, pre):
         check(y, x, wp, wq, g, -0.5, *tq().residual_norm(y, x, wq, wp, g, -0.5, EPS))
 
 
+@pytest.mark.parametrize("T,N", [(6200, 513), (4099, 1504), (1100, 4100), (1031, 5120), (520, 8192),
+                                 (513, 7993), (3001, 2048)])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "row"])
+def test_many_tokens(T, N, gate):
+    """Workgroups that go through several tokens; the same bits as a few at a time."""
+    dts = {"none": ("fp32", "bf16"), "channel": ("bf16", "fp16"), "token": ("fp16", "fp32"),
+           "row": ("bf16", "bf16")}[gate]
+    y, x, post, pre, g = inputs(T, N, *dts, "bf16", gate != "row", gate != "none", gate)
+    xo, z = tq().residual_norm(y, x, pre, post, g, 0.7, EPS)
+    check(y, x, post, pre, g, 0.7, xo, z)
+    for a in range(0, T, 200):
+        part = slice(a, a + 200)
+        gp = g[part] if gate in ("token", "row") else g
+        few = tq().residual_norm(y[part], x[part], pre, post, gp, 0.7, EPS)
+        assert torch.equal(few[0], xo[part]) and torch.equal(few[1], z[part]), a
+    if N % 32 == 0:
+        xq, (q, d) = tq().residual_norm(y, x, pre, post, g, 0.7, EPS, quantize=True)
+        assert torch.equal(xq, xo)
+        check(y, x, post, pre, g, 0.7, xq, (q, d))
+    own = x.clone()
+    tq().residual_norm(y, own, pre, post, g, 0.7, EPS, x_out=own)
+    assert torch.equal(own, xo)
+
+
 @pytest.mark.parametrize("N", [32, 64, 96, 512, 544, 2048, 4096, 5120, 8224, 32768])
 def test_quantized_as_the_products_do(N):
     """q and d are tq_quantize_act's of the fp32 z, bit for bit."""
