@@ -265,7 +265,7 @@ int tq_select_pages(int dtype, const void *q, int64_t q_ts, int64_t q_hs, int64_
                            ctx_lens, starts, (int)table_pages, tq::log2_of(page_size), (int)batch,
                            (int)kv_heads, (int)(heads / kv_heads), (int)max_nodes, dtype,
                            (int)first, (int)last, (int)keep, (int)width, tables, ctx_out};
-    return launch_status(tq::launch_select((int)D, a, max_ctx, scratch, stream));
+    return launch_status(tq::launch_select((int)D, a, max_ctx, counters, scratch, stream));
 }
 
 }  // extern "C"

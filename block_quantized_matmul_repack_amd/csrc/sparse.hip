@@ -26,9 +26,9 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 constexpr int WAVES = 4, THREADS = 64 * WAVES;
 constexpr int SEL_WAVES = 8, SEL_THREADS = 64 * SEL_WAVES;
 constexpr int CHOOSE_WAVES = 16;
-constexpr int SCORE_WAVES = 8, SCORE_THREADS = 64 * SCORE_WAVES;
 constexpr int MOST_KEYS = 8192;                  // pages whose keys LDS holds
 constexpr int SPREAD_TURNS = 2, SPREAD_UNITS = 128;
+constexpr int COUNTER_STRIDE = 64;               // words: a cache line for each head
 
 // ---- bounds ----------------------------------------------------------------
 
@@ -207,11 +207,12 @@ __device__ __forceinline__ void load_bounds(PageBounds<D> &p, const SelectArgs &
     }
 }
 
-// Scores of pages [begin, end), 16 a wave and turn, as order keys into keys[page].
-// With AHEAD the next turn's bounds are on their way while this one's are scored.
-template <int DT, int D, int W, bool AHEAD>
+// Scores of pages [begin, end), 16 a wave and turn, as order keys: put(page, key,
+// again), again where the page has one of earlier rows.  The next turn's bounds are
+// on their way while this one's are scored.
+template <int DT, int D, int W, typename F>
 __device__ __forceinline__ void score_pages(QueryLds<D> &l, const SelectArgs &a, const Span &sp, int h,
-                                            int begin, int end, uint32_t *keys)
+                                            int begin, int end, F put)
 {
     constexpr int NB = D / 32, RT = row_tiles(D);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -230,7 +231,7 @@ __device__ __forceinline__ void score_pages(QueryLds<D> &l, const SelectArgs &a,
         __syncthreads();
         for (; p0 < end; p0 += W * 16) {
             const int p1 = p0 + W * 16;
-            if (AHEAD && p1 < end)
+            if (p1 < end)
                 load_bounds<D>(next, a, table[min(p1 + r, end - 1)], h, g);
             double best = -__builtin_inf();
             for (int t = 0; t < tiles; t++) {
@@ -255,13 +256,9 @@ __device__ __forceinline__ void score_pages(QueryLds<D> &l, const SelectArgs &a,
             score = fmaxf(score, __shfl_xor(score, 32));
             if (g == 0 && p0 + r < end) {
                 // a page that is not there comes last
-                const uint32_t key = now.there ? order_key(score) : 0u;
-                keys[p0 + r] = r0 ? max(keys[p0 + r], key) : key;
+                put(p0 + r, now.there ? order_key(score) : 0u, r0 > 0);
             }
-            if (AHEAD)
-                now = next;
-            else if (p1 < end)
-                load_bounds<D>(now, a, table[min(p1 + r, end - 1)], h, g);
+            now = next;
         }
     }
 }
@@ -385,48 +382,76 @@ __global__ __launch_bounds__(SEL_THREADS) void k_select(SelectArgs a)
     const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
     const Span sp = span_of(a, b);
     if (sp.keep < sp.tail - sp.first && sp.keep > 0)
-        score_pages<DT, D, SEL_WAVES, true>(q, a, sp, h, sp.first, sp.tail, keys);
+        score_pages<DT, D, SEL_WAVES>(q, a, sp, h, sp.first, sp.tail,
+                                      [&](int page, uint32_t key, bool again) {
+                                          keys[page] = again ? max(keys[page], key) : key;
+                                      });
     choose<SEL_WAVES>(l, a, sp, b, h, keys);
 }
 
-// The same in two launches: a head's pages spread over gridDim.y workgroups, then
-// the choice.
-template <int DT, int D>
-__global__ __launch_bounds__(SCORE_THREADS) void k_scores(SelectArgs a, uint32_t *keys)
+// A head's pages spread over gridDim.y workgroups.  LAST: the last of them to end
+// chooses; the keys are exchanged into memory (device-scope atomics act there, past
+// the dies' caches) and have come back before the head's count rises, so it reads
+// them whole.  Else k_choose does, in a launch of its own.
+template <int DT, int D, bool LAST>
+__global__ __launch_bounds__(SEL_THREADS) void k_scores(SelectArgs a, uint32_t *all_keys,
+                                                        uint32_t *counters)
 {
     __shared__ QueryLds<D> q;
+    __shared__ uint32_t own[LAST ? MOST_KEYS : 1];
+    __shared__ ChoiceLds<SEL_WAVES> l;
+    __shared__ bool last;
     const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
     const Span sp = span_of(a, b);
     const int cand = sp.tail - sp.first;
-    if (sp.keep == cand || sp.keep == 0)
+    uint32_t *keys = all_keys + (int64_t)blockIdx.x * a.table_pages;
+    if (sp.keep == cand || sp.keep == 0) {       // nothing to compare
+        if constexpr (LAST) {
+            if (blockIdx.y == 0)
+                choose<SEL_WAVES>(l, a, sp, b, h, own);
+        }
         return;
+    }
     // whole turns of 16 pages a wave
-    const int turns = (cand + SCORE_WAVES * 16 - 1) / (SCORE_WAVES * 16);
-    const int each = (turns + gridDim.y - 1) / gridDim.y * (SCORE_WAVES * 16);
-    const int64_t begin = sp.first + (int64_t)blockIdx.y * each;
+    const int turns = (cand + SEL_WAVES * 16 - 1) / (SEL_WAVES * 16);
+    const int64_t each = (int64_t)((turns + gridDim.y - 1) / gridDim.y) * (SEL_WAVES * 16);
+    const int64_t begin = sp.first + blockIdx.y * each;
+    uint32_t was = 0;
     if (begin < sp.tail)
-        score_pages<DT, D, SCORE_WAVES, true>(q, a, sp, h, (int)begin,
-                                              (int)min(begin + each, (int64_t)sp.tail),
-                                              keys + (int64_t)blockIdx.x * a.table_pages);
+        score_pages<DT, D, SEL_WAVES>(
+            q, a, sp, h, (int)begin, (int)min(begin + each, (int64_t)sp.tail),
+            [&](int page, uint32_t key, bool again) {
+                if constexpr (LAST)
+                    was |= again ? __hip_atomic_fetch_max(keys + page, key, __ATOMIC_RELAXED,
+                                                          __HIP_MEMORY_SCOPE_AGENT)
+                                 : __hip_atomic_exchange(keys + page, key, __ATOMIC_RELAXED,
+                                                         __HIP_MEMORY_SCOPE_AGENT);
+                else
+                    keys[page] = again ? max(keys[page], key) : key;
+            });
+    if constexpr (LAST) {
+        asm volatile("s_waitcnt vmcnt(0)" : : "v"(was) : "memory");
+        __syncthreads();
+        uint32_t *count = counters + (int64_t)blockIdx.x * COUNTER_STRIDE;
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.y - 1;
+        __syncthreads();
+        if (!last)
+            return;
+        for (int i = sp.first + threadIdx.x; i < sp.tail; i += SEL_THREADS)
+            own[i] = __hip_atomic_load(keys + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        choose<SEL_WAVES>(l, a, sp, b, h, own);
+        if (threadIdx.x == 0)                    // zero again for the next call
+            __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 }
 
-// IN_LDS: the keys are brought there first, for the turns over them.
-template <bool IN_LDS>
 __global__ __launch_bounds__(64 * CHOOSE_WAVES) void k_choose(SelectArgs a, const uint32_t *keys)
 {
     __shared__ ChoiceLds<CHOOSE_WAVES> l;
-    __shared__ uint32_t own[IN_LDS ? MOST_KEYS : 1];
     const int b = blockIdx.x / a.kv_heads, h = blockIdx.x - b * a.kv_heads;
-    const Span sp = span_of(a, b);
-    const uint32_t *from = keys + (int64_t)blockIdx.x * a.table_pages;
-    if constexpr (IN_LDS) {
-        if (sp.keep < sp.tail - sp.first && sp.keep > 0)
-            for (int i = sp.first + threadIdx.x; i < sp.tail; i += 64 * CHOOSE_WAVES)
-                own[i] = from[i];
-        choose<CHOOSE_WAVES>(l, a, sp, b, h, own);
-    } else {
-        choose<CHOOSE_WAVES>(l, a, sp, b, h, from);
-    }
+    choose<CHOOSE_WAVES>(l, a, span_of(a, b), b, h, keys + (int64_t)blockIdx.x * a.table_pages);
 }
 
 template <int CT>
@@ -442,32 +467,36 @@ hipError_t bounds_d(int D, dim3 grid, const BoundsArgs &a, int pages, hipStream_
     return hipGetLastError();
 }
 
-// keys: in scratch, or null for the form in one launch.
+// How a step's pages are chosen: by a workgroup for each head; by several, of which
+// the last one chooses; or in two launches, where LDS does not hold a head's keys.
+enum Form { ALONE, SPREAD, APART };
+
 template <int DT, int D>
-hipError_t select_dd(const SelectArgs &a, int64_t pages, uint32_t *keys, hipStream_t s)
+hipError_t select_dd(Form form, const SelectArgs &a, int64_t pages, uint32_t *counters,
+                     uint32_t *keys, hipStream_t s)
 {
-    const dim3 units((unsigned)(a.batch * a.kv_heads));
-    if (!keys) {
+    const int64_t y = std::min<int64_t>((pages + SEL_WAVES * 16 - 1) / (SEL_WAVES * 16), 65535);
+    const dim3 units((unsigned)(a.batch * a.kv_heads)), spread(units.x, (unsigned)y);
+    if (form == ALONE) {
         k_select<DT, D><<<units, SEL_THREADS, 0, s>>>(a);
-        return hipGetLastError();
+    } else if (form == SPREAD) {
+        k_scores<DT, D, true><<<spread, SEL_THREADS, 0, s>>>(a, keys, counters);
+    } else {
+        k_scores<DT, D, false><<<spread, SEL_THREADS, 0, s>>>(a, keys, nullptr);
+        k_choose<<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
     }
-    const int64_t y = std::min<int64_t>((pages + SCORE_WAVES * 16 - 1) / (SCORE_WAVES * 16), 65535);
-    k_scores<DT, D><<<dim3(units.x, (unsigned)y), SCORE_THREADS, 0, s>>>(a, keys);
-    if (a.table_pages <= MOST_KEYS)
-        k_choose<true><<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
-    else
-        k_choose<false><<<units, 64 * CHOOSE_WAVES, 0, s>>>(a, keys);
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t select_d(int D, const SelectArgs &a, int64_t pages, uint32_t *keys, hipStream_t s)
+hipError_t select_d(int D, Form form, const SelectArgs &a, int64_t pages, uint32_t *counters,
+                    uint32_t *keys, hipStream_t s)
 {
     switch (D) {
-    case 64: return select_dd<DT, 64>(a, pages, keys, s);
-    case 96: return select_dd<DT, 96>(a, pages, keys, s);
-    case 128: return select_dd<DT, 128>(a, pages, keys, s);
-    case 256: return select_dd<DT, 256>(a, pages, keys, s);
+    case 64: return select_dd<DT, 64>(form, a, pages, counters, keys, s);
+    case 96: return select_dd<DT, 96>(form, a, pages, counters, keys, s);
+    case 128: return select_dd<DT, 128>(form, a, pages, counters, keys, s);
+    case 256: return select_dd<DT, 256>(form, a, pages, counters, keys, s);
     }
     return hipErrorInvalidValue;
 }
@@ -492,7 +521,8 @@ size_t select_scratch_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages
     return (size_t)batch * kv_heads * table_pages * sizeof(uint32_t);
 }
 
-hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, void *scratch, hipStream_t s)
+hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, uint32_t *counters,
+                         void *scratch, hipStream_t s)
 {
     const int64_t units = (int64_t)a.batch * a.kv_heads;
     if (!grid_fits(units, 64 * CHOOSE_WAVES))
@@ -500,10 +530,12 @@ hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, void *scra
     const int64_t pages = std::min<int64_t>((max_ctx >> a.log_page) + 1, a.table_pages);
     const int64_t turns = (pages + SEL_WAVES * 16 - 1) / (SEL_WAVES * 16) *
                           (((int64_t)a.max_nodes * a.group + 15) / 16);
-    const bool alone = a.table_pages <= MOST_KEYS && (turns <= SPREAD_TURNS || units >= SPREAD_UNITS);
-    uint32_t *keys = alone ? nullptr : (uint32_t *)scratch;
-    return a.dtype == TQ_BF16 ? select_d<TQ_BF16>(D, a, pages, keys, s)
-                              : select_d<TQ_F16>(D, a, pages, keys, s);
+    const Form form = a.table_pages > MOST_KEYS                            ? APART
+                      : turns <= SPREAD_TURNS || units >= SPREAD_UNITS ? ALONE
+                                                                           : SPREAD;
+    uint32_t *keys = (uint32_t *)scratch;
+    return a.dtype == TQ_BF16 ? select_d<TQ_BF16>(D, form, a, pages, counters, keys, s)
+                              : select_d<TQ_F16>(D, form, a, pages, counters, keys, s);
 }
 
 }  // namespace tq

@@ -545,6 +545,8 @@ struct SelectArgs {
     int32_t *out, *ctx_out;                      // [batch][kv_heads][width], [batch]
 };
 size_t select_scratch_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages);
-hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, void *scratch, hipStream_t s);
+// counters: zero before and after (the workspace's first TQ_NOALLOC_SCRATCH_BYTES).
+hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, uint32_t *counters,
+                         void *scratch, hipStream_t s);
 
 }  // namespace tq

@@ -176,6 +176,29 @@ def test_select_from_many_pages(pages):
         check_select(c, q, ctx, nodes, keep)
 
 
+@pytest.mark.parametrize("pages,heads", [(8300, 1), (60, 2)])
+def test_select_from_tables_wider_than_a_workgroup_holds(pages, heads):
+    """More than 8192 entries a row: scored and chosen in two launches."""
+    ctx, nodes = [pages * 16 - 5, 100], [3, 1]
+    c = Cache("q4_0", 2, 8320, 16, heads, 64, [ctx[0] + 3, 101], seed=pages)
+    c.bounds([0, 0], c.lens)
+    q = queries(c, nodes, 3, "fp16")
+    for keep in (1, 40):
+        check_select(c, q, ctx, nodes, keep)
+        check_select(c, q, ctx, nodes, keep, max_nodes=3, max_ctx=64)    # a bound too small
+
+
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_select_with_a_bound_too_small(nodes):
+    """max_ctx shapes the launch: the pages past it are scored all the same."""
+    ctx = [1000 * 16 + 7]
+    c = Cache("q8_0", 1, 1100, 16, 2, 64, [ctx[0] + nodes], seed=12)
+    c.bounds([0], c.lens)
+    q = queries(c, [nodes], 4, "bf16")
+    for most in (0, 300, ctx[0]):
+        check_select(c, q, ctx, [nodes], 9, max_nodes=nodes, max_ctx=most)
+
+
 def test_select_takes_the_earlier_of_equal_pages():
     """Equal scores, zero scores, queries of zeros, and pages that are not there."""
     ctx, nodes = [320, 320], [1, 1]
