@@ -61,25 +61,50 @@ __global__ __launch_bounds__(THREADS) void k_bounds(BoundsArgs a, int pages)
         hi[e] = -__builtin_inff();
         lo[e] = __builtin_inff();
     }
-#pragma unroll 4
-    for (int pos = r; pos < n; pos += 16) {
-        const uint8_t *p = chunk + k_offset<CT, D>(pos, s, g);
-        const float d = f16_bits_to_f32(scales[pos * NB + s]);
-        uint2 code;
-        if constexpr (CT == TQ_Q8_0)
-            code = *(const uint2 *)p;
-        else
-            code = make_uint2(*(const uint32_t *)p, 0);
+    // The codes are unsigned: code * d - offset * d, one fma of a value that fp32 holds
+    // (19 bits).  Two tokens at a time, for maxima and minima of three; past the end the
+    // last one again.
+#pragma unroll 2
+    for (int pos = r; pos < n; pos += 32) {
+        uint2 code[2];
+        float d[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int at = pos + 16 * k < n ? pos + 16 * k : pos;
+            const uint8_t *p = chunk + k_offset<CT, D>(at, s, g);
+            d[k] = f16_bits_to_f32(scales[at * NB + s]);
+            if constexpr (CT == TQ_Q8_0) {
+                code[k] = *(const uint2 *)p;
+            } else {
+                const uint32_t w = *(const uint32_t *)p;
+                code[k] = make_uint2(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu);
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            int x;
-            if constexpr (CT == TQ_Q8_0)
-                x = (int)(((e < 4 ? code.x : code.y) >> (8 * (e & 3))) & 255u) - 128;
-            else
-                x = (int)((code.x >> k4_shift(e)) & 15u) - 8;
-            const float v = d * (float)x;        // 19 bits: exact
-            hi[e] = fmaxf(hi[e], v);
-            lo[e] = fminf(lo[e], v);
+            // element of byte e % 4 of the low or high nibbles, or e itself
+            constexpr float offset = CT == TQ_Q8_0 ? 128.0f : 8.0f;
+            const float u = fmaf((float)(((e < 4 ? code[0].x : code[0].y) >> (8 * (e & 3))) & 255u), d[0],
+                                 -offset * d[0]);
+            const float v = fmaf((float)(((e < 4 ? code[1].x : code[1].y) >> (8 * (e & 3))) & 255u), d[1],
+                                 -offset * d[1]);
+            hi[e] = fmaxf(fmaxf(hi[e], u), v);
+            lo[e] = fminf(fminf(lo[e], u), v);
+        }
+    }
+    if constexpr (CT == TQ_Q4_0) {
+        // from the places of the nibbles to the elements
+        float h[8], l[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int at = ((k4_shift(e) & 4) ? 4 : 0) + (k4_shift(e) >> 3);
+            h[e] = hi[at];
+            l[e] = lo[at];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            hi[e] = h[e];
+            lo[e] = l[e];
         }
     }
     float big = 0.0f;
