@@ -33,7 +33,10 @@ constexpr int COUNTER_STRIDE = 64;               // words: a cache line for each
 // ---- bounds ----------------------------------------------------------------
 
 // A wave has one block of one page and head: lane (g, r) the elements 8g ..
-// 8g+7 of every 16th token from r.
+// 8g+7 of every 16th token from r.  Bound: four dependent reads (length, page,
+// scales and codes); 64 sequences' last pages of 64 take 5.8 us, the pages of two
+// prompts of 8191 tokens 11.4, 8 heads of 128 (7.0 and 12.2 with the codes made signed
+// first, a token at a time).
 template <int CT, int D>
 __global__ __launch_bounds__(THREADS) void k_bounds(BoundsArgs a, int pages)
 {
@@ -397,7 +400,8 @@ __device__ __forceinline__ void choose(ChoiceLds<W> &l, const SelectArgs &a, con
 }
 
 // A workgroup for each sequence and key head scores its pages and chooses; their
-// keys stay in LDS.
+// keys stay in LDS.  64 sequences of up to 16384 keys in pages of 64, 8 key heads:
+// 11.9 us for 26 MB of bounds (sixteen waves a workgroup: 16.7).
 template <int DT, int D>
 __global__ __launch_bounds__(SEL_THREADS) void k_select(SelectArgs a)
 {
@@ -417,7 +421,8 @@ __global__ __launch_bounds__(SEL_THREADS) void k_select(SelectArgs a)
 // A head's pages spread over gridDim.y workgroups.  LAST: the last of them to end
 // chooses; the keys are exchanged into memory (device-scope atomics act there, past
 // the dies' caches) and have come back before the head's count rises, so it reads
-// them whole.  Else k_choose does, in a launch of its own.
+// them whole.  Else k_choose does, in a launch of its own.  One sequence of 131000
+// keys: 11.6 us, where scores and choice apart take 7 + 7.
 template <int DT, int D, bool LAST>
 __global__ __launch_bounds__(SEL_THREADS) void k_scores(SelectArgs a, uint32_t *all_keys,
                                                         uint32_t *counters)
