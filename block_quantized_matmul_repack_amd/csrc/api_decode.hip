@@ -145,8 +145,8 @@ int attention(int type, int dtype, const void *q, int64_t q_ts, int64_t q_hs, in
     if (st != TQ_OK)
         return st;
     const tq::AttnArgs a{q, out, q_ts, q_hs, o_ts, o_hs, (const uint8_t *)k_cache,
-                         (const uint8_t *)v_cache, page_table, table_stride, table_head_stride, ctx_lens, starts,
-                         mask, mask_stride, n_pages, tokens, (int)table_pages,
+                         (const uint8_t *)v_cache, page_table, table_stride, table_head_stride,
+                         ctx_lens, starts, mask, mask_stride, n_pages, tokens, (int)table_pages,
                          tq::log2_of(page_size), (int)batch, (int)kv_heads,
                          (int)(heads / kv_heads), (int)max_nodes, (int)mask_words, dtype, scale};
     return launch_status(tq::launch_attention(type, (int)D, a, p, scratch, stream));

@@ -35,6 +35,14 @@ int tq_plan_step(int64_t batch, const int32_t *lens, const int32_t *new_tokens,
         for (const auto &o : out)
             if (overlap(i.p, 4 * i.n, o.p, 4 * o.n))
                 return TQ_E_SHAPE;
+    // the table is read and written: no other array lies in it
+    const int64_t entries = batch ? (batch - 1) * table_stride + table_pages : 0;
+    for (const auto &i : in)
+        if (overlap(i.p, 4 * i.n, page_table, 4 * entries))
+            return TQ_E_SHAPE;
+    for (const auto &o : out)
+        if (overlap(o.p, 4 * o.n, page_table, 4 * entries))
+            return TQ_E_SHAPE;
     const tq::PlanArgs a{lens, new_tokens, owned, page_table, table_stride, table_pages, free_pages,
                          free_count, free_capacity, batch, tokens, tq::log2_of(page_size), starts,
                          positions, slots, new_lens, new_owned, free_left};
@@ -59,6 +67,16 @@ int tq_release_pages(int64_t batch, const int32_t *done, const int32_t *owned, i
         return TQ_E_ALIGN;
     if (overlap(owned, 4 * batch, new_owned, 4 * batch) ||
         overlap(done, 4 * batch, new_owned, 4 * batch) || overlap(free_count, 4, free_left, 4))
+        return TQ_E_SHAPE;
+    // the table and the stack are written: no other array lies in them
+    const int64_t entries = batch ? (batch - 1) * table_stride + table_pages : 0;
+    const struct { const void *p; int64_t n; } others[] = {
+        {done, batch}, {owned, batch}, {free_count, 1}, {new_owned, batch}, {free_left, 1}};
+    for (const auto &o : others)
+        if (overlap(o.p, 4 * o.n, page_table, 4 * entries) ||
+            overlap(o.p, 4 * o.n, free_pages, 4 * free_capacity))
+            return TQ_E_SHAPE;
+    if (overlap(free_pages, 4 * free_capacity, page_table, 4 * entries))
         return TQ_E_SHAPE;
     const tq::ReleaseArgs a{done, owned, page_table, table_stride, table_pages, free_pages,
                             free_count, free_capacity, batch, new_owned, free_left};
@@ -85,6 +103,8 @@ int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const 
         return TQ_OK;
     if (!y || !x || !x_out || !z == !q || !q != !d)
         return TQ_E_NULL;
+    if (x == x_out && x_ts != xo_ts && tokens > 1)
+        return TQ_E_SHAPE;
     const uintptr_t al = size_of(dtype), wal = size_of(w_dtype);
     if (!aligned(y, size_of(y_dtype)) || !aligned(x, al) || !aligned(x_out, al) || !aligned(z, al) ||
         !aligned(post_weight, wal) || !aligned(pre_weight, wal) || !aligned(gate, wal) ||
@@ -251,6 +271,9 @@ int tq_select_pages(int dtype, const void *q, int64_t q_ts, int64_t q_hs, int64_
         !aligned(ctx_lens, 4) || !aligned(starts, 4) || !aligned(tables, 4) || !aligned(ctx_out, 4))
         return TQ_E_ALIGN;
     if (overlap(ctx_lens, 4 * batch, ctx_out, 4 * batch) ||
+        overlap(starts, 4 * (batch + 1), ctx_out, 4 * batch) ||
+        overlap(ctx_lens, 4 * batch, tables, 4 * batch * kv_heads * width) ||
+        overlap(starts, 4 * (batch + 1), tables, 4 * batch * kv_heads * width) ||
         overlap(page_table, 4 * ((batch - 1) * table_stride + table_pages), tables,
                 4 * batch * kv_heads * width))
         return TQ_E_SHAPE;

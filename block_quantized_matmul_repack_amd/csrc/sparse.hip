@@ -548,7 +548,10 @@ hipError_t launch_bounds(int cache_type, int D, const BoundsArgs &a, int64_t max
 
 size_t select_scratch_bytes(int64_t batch, int64_t kv_heads, int64_t table_pages)
 {
-    return (size_t)batch * kv_heads * table_pages * sizeof(uint32_t);
+    // with more units than that a workgroup has each, and the keys in LDS
+    const int64_t units = batch * kv_heads;
+    return (size_t)(table_pages > MOST_KEYS ? units : std::min<int64_t>(units, SPREAD_UNITS)) *
+           table_pages * sizeof(uint32_t);
 }
 
 hipError_t launch_select(int D, const SelectArgs &a, int64_t max_ctx, uint32_t *counters,

@@ -660,7 +660,8 @@ def tree_attention(ctype, q, k_cache, v_cache, page_table, ctx_lens, starts, kv_
     tokens before the new ones.  mask: int32 [T, words], bit j of a row = new
     token j of the sequence is seen (None: the chain, j <= i).  page_table may
     be [B, kv_heads, pages], a table for each key head, as select_pages gives
-    (then with its ctx_lens).  max_nodes and max_ctx bound the new and the cached tokens of a sequence; they default
+    (then with its ctx_lens).  max_nodes and max_ctx bound the new and the
+    cached tokens of a sequence; they default
     to all rows of q and all of the table.  scale defaults to D ** -0.5."""
     name = "tq_tree_attention"
     shape, q_ts, q_hs, dev, code = _heads_of(name, "q", q, _ATTN_DTYPES)

@@ -582,7 +582,8 @@ int tq_verify_draft(int dtype, const void *target, int64_t target_stride,
  *   new_lens  : lens + the new tokens;  new_owned : pages owned now.
  *   free_left : the stack's new count; below 0, as many pages were missing.
  * The state (lens, owned, free_count) is read and the next one written apart,
- * so the two must not overlap (TQ_E_SHAPE).  Numbers below 0 count as 0, lens
+ * so the two must not overlap, nor any array the table or, where that is written, the
+ * stack (TQ_E_SHAPE).  A page is owned by one request.  Numbers below 0 count as 0, lens
  * past 2^30 as 2^30.  A request that gives back cached tokens (drafts that were
  * refused) lowers its length and keeps its pages.
  * tq_release_pages: the pages of requests with done[b] != 0 go back on the stack
@@ -641,7 +642,7 @@ int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const 
  * A logit that is NaN or -infinity weighs nothing; at +infinity all such share the
  * row.  Sums are exact, so results do not depend on any order: deterministic.
  *   logits : of dtype, rows of vocab at row stride `stride` elements (0: one row
- *     for all).
+ *     for all); probs must not overlap them.
  *   workspace : as tq_tree_attention's, tq_sample_workspace_bytes() (0: NULL will
  *     do).
  * Domain: rows 0..2^20, vocab 1..2^27, rows * vocab below 2^34. */
@@ -718,7 +719,7 @@ int tq_tree_attention_heads(int type, int dtype, const void *q, int64_t q_ts, in
 /* The calls above for bindings that pay for every argument of a foreign call: args
  * holds the named entry point's arguments in order, each in 8 bytes (integers and
  * addresses sign-extended, a float's bits in the low 4), read before it returns.
- * Unknown `which`: TQ_E_TYPE. */
+ * TQ_E_NULL without args, TQ_E_TYPE for an unknown `which`. */
 typedef enum {
     TQ_CALL_TREE_ATTENTION = 0, TQ_CALL_TREE_ATTENTION_HEADS = 1, TQ_CALL_PLAN_STEP = 2,
     TQ_CALL_RELEASE_PAGES = 3, TQ_CALL_RESIDUAL_NORM = 4, TQ_CALL_SAMPLE = 5,

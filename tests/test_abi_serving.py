@@ -44,6 +44,11 @@ def test_plan(L):
     for name, other in (("new_lens", 0), ("new_owned", 2), ("left", 5), ("starts", 1), ("slots", 4)):
         assert c(**{name: P(other)}) == SHAPE, name
     assert c(new_lens=ctypes.c_void_p(I32 + 8)) == SHAPE
+    # nothing lies in the table, which is read and written
+    row2 = ctypes.c_void_p(P(3).value + 4 * (2 * 9 + 7))
+    for name in ("lens", "new", "owned", "free", "count", "starts", "positions", "slots", "new_lens",
+                 "new_owned", "left"):
+        assert c(**{name: row2}) == SHAPE, name
 
 
 def release(L):
@@ -61,6 +66,11 @@ def test_release(L):
     for name in ("done", "owned", "table", "free", "count", "new_owned", "left"):
         assert c(**{name: NUL}) == NULL, name
         assert c(**{name: ODD}) == ALIGN, name
+    # nothing lies in the table or the stack, which are written
+    row2, last = ctypes.c_void_p(P(3).value + 4 * (2 * 9 + 7)), ctypes.c_void_p(P(4).value + 4 * 49)
+    for name in ("done", "owned", "count", "new_owned", "left"):
+        assert c(**{name: row2}) == SHAPE and c(**{name: last}) == SHAPE, name
+    assert c(free=row2) == SHAPE
 
 
 def residual(L, **kw):
@@ -80,6 +90,7 @@ def test_residual_norm(L):
                 dict(scale=float("inf")), dict(eps=-1.0), dict(eps=float("nan"))):
         assert c(**bad) == SHAPE, bad
     assert c(tokens=0, y=NUL) == OK
+    assert c(x_ts=0) == SHAPE and c(xo_ts=128) == SHAPE      # in place, at another stride
     for name in ("y", "x", "x_out", "z"):
         assert c(**{name: NUL}) == NULL, name
         assert c(**{name: ODD}) == ALIGN, name
@@ -165,12 +176,16 @@ def test_select(L):
                 dict(batch=-1), dict(batch=65536), dict(batch=65535, kv_heads=64, heads=64),
                 dict(page=20), dict(table_pages=0), dict(table_stride=39), dict(max_nodes=0),
                 dict(max_ctx=-1), dict(first=-1), dict(last=-1), dict(keep=-1), dict(width=7),
-                dict(keep=5), dict(q_ts=-1), dict(ctx_out=P(4)), dict(tables=P(3))):
+                dict(keep=5), dict(q_ts=-1), dict(ctx_out=P(4)), dict(tables=P(3)),
+                dict(ctx_out=P(5)), dict(tables=P(4)), dict(tables=P(5))):
         assert c(**bad) == SHAPE, bad
     assert c(batch=0, table=NUL) == OK
     for name in ("q", "codes", "scales", "table", "ctx", "starts", "tables", "ctx_out"):
         assert c(**{name: NUL}) == NULL, name
         assert c(**{name: ODD}) == ALIGN, name
+    # keys of heads that have a workgroup each stay on the chip
+    assert (L.tq_select_pages_workspace_bytes(64, 8, 256) ==
+            L.tq_select_pages_workspace_bytes(4096, 8, 256) <= (1 << 20) + 128 * 256 * 4)
     need = L.tq_select_pages_workspace_bytes(2, 2, 40)
     assert need > 1 << 20
     assert c(ws=NUL) == NULL and c(ws_bytes=need - 1) == SHAPE and c(ws=A4) == ALIGN
@@ -205,3 +220,59 @@ def test_binding_refuses():
     for call in calls:
         with pytest.raises(tq.TiledqError):
             call()
+
+
+def numbers(args):
+    """Arguments as plain numbers: addresses, and 0 for none."""
+    return [0 if a is None else a.value if isinstance(a, ctypes.c_void_p) else a for a in args]
+
+
+@pytest.mark.parametrize("make", [attention, plan, release, residual, sample, probs, bounds, select])
+def test_packed_is_the_same_call(L, make):
+    """Each argument replaced by one that is refused gives the same status
+    packed and unpacked; so do calls that cannot be packed."""
+    c = make(L)
+    packed = c.fn
+    assert type(packed).__name__ == "_Packed"
+    kinds = dict(zip(c.good, packed.plain.argtypes))
+    seen = set()
+    for name, kind in kinds.items():
+        # (a good call is left out: it would be launched)
+        for bad in ([float("nan"), -1.0, float("inf")] if kind is ctypes.c_float else
+                    [None, ODD] if kind is ctypes.c_void_p else [-1, 1 << 62, 7]):
+            kw = {**c.good, name: bad}
+            if kind is ctypes.c_int and bad == 1 << 62:
+                continue                         # not a number of that type
+            # an output is missing besides, so nothing is ever launched
+            off = next(o for o in ("new_lens", "left", "x_out", "u", "probs", "codes", "tables", "out")
+                       if kinds.get(o) is ctypes.c_void_p)
+            if off != name:
+                kw[off] = None
+            plain = packed.plain(*kw.values())
+            assert plain in (OK, NULL, TYPE, SHAPE, ALIGN)
+            if plain == OK:
+                continue                         # nothing to do
+            assert packed(*numbers(kw.values())) == plain, (name, bad)
+            assert packed(*kw.values()) == plain, (name, bad)
+            seen.add(plain)
+    assert len(seen) > 1
+    assert L.tq_packed(packed.which, None) == NULL
+
+
+def test_packed_refuses_other_calls(L):
+    for which in (-1, 9, 1 << 20):
+        assert L.tq_packed(which, bytes(8 * 40)) == TYPE
+
+
+def test_default_streams_of_other_devices(monkeypatch):
+    """The null stream's handle says nothing of its device: asked for with
+    another device current, the call is refused."""
+    import block_quantized_matmul_repack_amd as tq
+    from block_quantized_matmul_repack_amd import ops
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
+    assert ops._stream_of(0) == 0
+    with pytest.raises(tq.TiledqError, match="current"):
+        ops._stream_of(1)
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 64 + dev)
+    assert ops._stream_of(1) == 65

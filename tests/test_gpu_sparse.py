@@ -188,6 +188,27 @@ def test_select_from_tables_wider_than_a_workgroup_holds(pages, heads):
         check_select(c, q, ctx, nodes, keep, max_nodes=3, max_ctx=64)    # a bound too small
 
 
+@pytest.mark.parametrize("G", [4, 17])
+def test_select_reads_queries_wherever_they_are(G):
+    """Any token and head strides, and rows that begin on an odd element."""
+    ctx, nodes = [700, 30], [2, 3]
+    c = Cache("q8_0", 2, 50, 16, 2, 96, [702, 33], seed=G)
+    c.bounds([0, 0], c.lens)
+    q = queries(c, nodes, G, "bf16")
+    want = check_select(c, q, ctx, nodes, 6)
+    heads = 2 * G
+    wide = torch.full((5, heads, 2 * 96 + 3), float("nan"), dtype=q.dtype, device="cuda")
+    turned = torch.full((heads, 5, 96), float("nan"), dtype=q.dtype, device="cuda")
+    odd = torch.full((5 * heads * 96 + 1,), float("nan"), dtype=q.dtype, device="cuda")
+    for view in (wide[:, :, 1:97], turned.transpose(0, 1), odd[1:].view(5, heads, 96)):
+        view.copy_(q)
+        got = check_select(c, view, ctx, nodes, 6)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # one query row for all
+    one = q[:1, :1].expand(5, heads, 96)
+    check_select(c, one, ctx, nodes, 6)
+
+
 @pytest.mark.parametrize("nodes", [1, 40])
 def test_select_with_a_bound_too_small(nodes):
     """max_ctx shapes the launch: the pages past it are scored all the same."""
