@@ -203,3 +203,13 @@ def test_more_rows_than_a_launch_takes():
     k = [(i * 7) % 50 for i in range(700)]
     p = [0.5 + 0.0007 * i for i in range(700)]
     check(x, u, [0.5 + 0.001 * i for i in range(700)], k, p)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [524288, 524289, 600001, 1048577])
+def test_the_longest_rows(V, dtype):
+    """Tiles twice as large, and rows of more tiles than are kept apart."""
+    x, u = rows(3, V, dtype)
+    x[2, ::3] = -INF
+    check(x, u, [0.8, 1.0, 0.0], [0, 40, 3], [0.95, 1.0, 0.5], [0.0, 0.02, 0.1])
+    check(x[:2], u[:2], [1.0, 0.6], [100000, 0], [0.5, 0.05])
