@@ -21,6 +21,7 @@
 // k_probs 22.0, 4.5 TB/s.  A workgroup for each row that does it all took 418 us for
 // one row and 493 for 64.
 #include <algorithm>
+#include <type_traits>
 
 #include "block_ops.h"
 
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 // weights lie within 2 % of each other.
 // k_range: one workgroup a row adds up its bins and learns in which of them top-k and
 // top-p cut (the masses err by a known margin, so at times two come into question).
-// k_gather: each workgroup sums the exact weights of what is surely kept, and lists
+// k_gather: each workgroup, a quarter of a tile, sums the exact weights of what is surely kept, and lists
 // the elements of the bins in question.
 // k_cut: one workgroup a row ranks the list, which gives the cut, and draws.
 // k_probs writes the distribution instead.
@@ -409,10 +410,15 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 
 // 32 in the exponent and more weigh nothing (2^-46); a bin more for the grid.
 constexpr int BINS = 2048, EACH = BINS / THREADS;
+static_assert(EACH == 2, "a pair of bins a thread");
+// e^(-1 / BIN_RATE): from a bin to the next.
+constexpr float STEP = 0.98347145f;
+constexpr int GUARD = 4, PLANE = GUARD + BINS;   // a tile's bins in scratch, behind entries of nothing
 constexpr int MASS_BITS = 17;                    // of a bin's first weight: 16384 elements fit 32 bits
 constexpr int MOST_TILES = 64;
 constexpr int LIST = 32768;                      // entries of a row
 constexpr int GATHER_THREADS = 256;
+constexpr int PARTS = THREADS / GATHER_THREADS, MOST_PARTS = MOST_TILES * PARTS;    // of a tile, a row
 constexpr int SHORT = 128, SUBS = THREADS, MOST_ALIKE = 4096;
 
 // Exact weights: kept: surely, and heavy enough for min-p; below: surely inside
@@ -440,7 +446,7 @@ struct RowScratch {
     uint64_t sum;
     float top[MOST_TILES];                       // of each tile
     int first[MOST_TILES];                       // its first place
-    Sums sums[MOST_TILES];
+    Sums sums[MOST_PARTS];
     uint64_t list[LIST];                         // entry()
 };
 
@@ -561,11 +567,14 @@ __global__ __launch_bounds__(THREADS) void k_bins(SampleArgs a, RowScratch *scra
         add_bins(x, top, BIN_RATE / t, counted, bins);
         __syncthreads();
         // without counts: 32-bit masses in the first half of its place
-        uint64_t *out = planes + (row * gridDim.x + tile) * BINS;
+        uint64_t *out = planes + (row * gridDim.x + tile) * PLANE;
+        const int at = counted ? GUARD : GUARD / 2;
 #pragma unroll
         for (int i = 0; i < EACH; i++)
             if (counted || i < EACH / 2)
-                out[i * THREADS + tid] = bins[i * THREADS + tid];
+                out[at + i * THREADS + tid] = bins[i * THREADS + tid];
+        if (tid < at)
+            out[tid] = 0;
     }
     if (tid == 0) {
         r.top[tile] = top;
@@ -574,8 +583,8 @@ __global__ __launch_bounds__(THREADS) void k_bins(SampleArgs a, RowScratch *scra
 }
 
 struct RangeLds {
-    uint32_t scan32[EACH][WAVES];
-    float scan[EACH][WAVES];
+    uint32_t scan32[WAVES];
+    float scan[WAVES];
     int lo, hi, kbin;
     uint32_t k_before;
     float mass_k, mass_through;
@@ -589,37 +598,41 @@ __device__ __forceinline__ void note_last(bool is, int number, int *p)
         atomicMax(p, number);
 }
 
-// From the bins of the row (thread t: bins t, t + THREADS, ...) to those that cut.
-__device__ __forceinline__ Range find_range(RangeLds &l, const uint32_t (&count)[EACH],
-                                            const uint64_t (&units)[EACH], const Setting &s, float top)
+// The same of a pair of neighbours.
+__device__ __forceinline__ void note_last(const bool (&is)[2], int number, int *p)
+{
+    note_last(is[0] || is[1], number + is[1], p);
+}
+
+// From the bins of the row (thread t: bins 2t and 2t + 1) to those that cut.
+__device__ __forceinline__ Range find_range(RangeLds &l, const uint32_t (&count)[2],
+                                            const uint64_t (&units)[2], const Setting &s, float top)
 {
     const int tid = threadIdx.x;
     const float place = floorf(top * s.grid);
     Range g{BINS, -1, BINS, 0, 0};
     if (tid == 0)
         l.lo = l.hi = l.kbin = -1;
-    uint32_t all = 0, before[EACH];
-    float total = 0.0f, mass[EACH], ahead[EACH];
-#pragma unroll
-    for (int i = 0; i < EACH; i++) {
-        uint32_t c;
-        float m;
-        mass[i] = (float)units[i] * exp2f((float)(tid + i * THREADS) * (-1.44269504f / BIN_RATE));
-        before[i] = all + scan_before<WAVES>(count[i], l.scan32[i], c);
-        ahead[i] = total + scan_before<WAVES>(mass[i], l.scan[i], m);
-        all += c;
-        total += m;
-    }
+    const int b = 2 * tid;
+    const float first = __builtin_amdgcn_exp2f((float)b * (-1.44269504f / BIN_RATE));
+    const float mass[2] = {(float)units[0] * first, (float)units[1] * (first * STEP)};
+    float total;
+    const float ahead0 = scan_before<WAVES>(mass[0] + mass[1], l.scan, total);
+    const float ahead[2] = {ahead0, ahead0 + mass[0]};
     float least = total, most = total;
+    uint32_t all = 0, before[2] = {};
+    if (s.k > 0) {
+        before[0] = scan_before<WAVES>(count[0] + count[1], l.scan32, all);
+        before[1] = before[0] + count[0];
+    }
     if (s.k > 0 && all > (uint32_t)s.k) {
-#pragma unroll
-        for (int i = 0; i < EACH; i++)
-            note_last(count[i] && before[i] < (uint32_t)s.k, tid + i * THREADS, &l.kbin);
+        note_last({count[0] && before[0] < (uint32_t)s.k, count[1] && before[1] < (uint32_t)s.k}, b,
+                  &l.kbin);
         __syncthreads();
         g.kbin = g.lo = g.hi = l.kbin;
 #pragma unroll
-        for (int i = 0; i < EACH; i++)
-            if (tid + i * THREADS == g.kbin) {
+        for (int i = 0; i < 2; i++)
+            if (b + i == g.kbin) {
                 l.k_before = before[i];
                 l.mass_k = ahead[i];
                 l.mass_through = ahead[i] + mass[i];
@@ -635,12 +648,14 @@ __device__ __forceinline__ Range find_range(RangeLds &l, const uint32_t (&count)
         // of the place, yet the part stays within its bin.
         const float margin = 0x1p-15f + fminf((fabsf(place) + BINS) * 0x1p-23f, 0.02f);
         const float p = (float)s.p, sure = p * least * (1.0f - margin), some = p * most * (1.0f + margin);
+        bool lo[2], hi[2];
 #pragma unroll
-        for (int i = 0; i < EACH; i++) {
-            const int b = tid + i * THREADS;
-            note_last(count[i] && (b == 0 || ahead[i] * (1.0f + margin) < sure), b, &l.lo);
-            note_last(count[i] && (b == 0 || ahead[i] * (1.0f - margin) <= some), b, &l.hi);
+        for (int i = 0; i < 2; i++) {
+            lo[i] = count[i] && (b + i == 0 || ahead[i] * (1.0f + margin) < sure);
+            hi[i] = count[i] && (b + i == 0 || ahead[i] * (1.0f - margin) <= some);
         }
+        note_last(lo, b, &l.lo);
+        note_last(hi, b, &l.hi);
         __syncthreads();
         g.lo = max(l.lo, 0);
         g.hi = min(l.hi, g.kbin);
@@ -648,33 +663,39 @@ __device__ __forceinline__ Range find_range(RangeLds &l, const uint32_t (&count)
     return g;
 }
 
-// COUNTED: the tiles' bins hold counts, too.
+// COUNTED: the tiles' bins hold counts, too; else a count is what is not 0.  shift: of
+// lane's tile, the bins that its own lie behind the row's; before them a pair is read
+// from the guard.
 template <bool COUNTED>
-__device__ __forceinline__ void add_tiles(uint32_t (&count)[EACH], uint64_t (&units)[EACH],
+__device__ __forceinline__ void add_tiles(uint32_t (&count)[2], uint64_t (&units)[2],
                                           const uint64_t *from, int tiles, int shift)
 {
-    const int tid = threadIdx.x;
-    for (int c0 = 0; c0 < tiles; c0 += 8) {
-        uint64_t v[8][EACH];                     // the loads of eight tiles together
+    typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(4)));
+    typedef uint64_t u64x2a __attribute__((ext_vector_type(2), aligned(8)));
+    using T = std::conditional_t<COUNTED, u64x2a, u32x2a>;
+    constexpr int TOGETHER = 8;                  // loads of so many tiles
+    const int b = 2 * (int)threadIdx.x;
+    for (int c0 = 0; c0 < tiles; c0 += TOGETHER) {
+        T v[TOGETHER];
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int c = min(c0 + k, tiles - 1), down = __builtin_amdgcn_readlane(shift, c);
-#pragma unroll
-            for (int i = 0; i < EACH; i++) {
-                const int b = tid + i * THREADS - down;
-                if constexpr (COUNTED)
-                    v[k][i] = from[c * BINS + max(b, 0)];
-                else
-                    v[k][i] = ((const uint32_t *)(from + c * BINS))[max(b, 0)];
-                if (b < 0 || c0 + k >= tiles)
-                    v[k][i] = 0;
-            }
+        for (int k = 0; k < TOGETHER; k++) {
+            // past the last tile the guard of the last one
+            const int c = min(c0 + k, tiles - 1);
+            const int down = c0 + k < tiles ? __builtin_amdgcn_readlane(shift, c) : BINS;
+            const int at = max(b - down, -2) + GUARD;
+            if constexpr (COUNTED)
+                v[k] = *(const T *)(from + c * PLANE + at);
+            else
+                v[k] = *(const T *)((const uint32_t *)(from + c * PLANE) + at);
         }
 #pragma unroll
-        for (int k = 0; k < 8; k++)
+        for (int k = 0; k < TOGETHER; k++)
 #pragma unroll
-            for (int i = 0; i < EACH; i++) {
-                count[i] += (uint32_t)(COUNTED ? v[k][i] >> 32 : v[k][i] != 0);
+            for (int i = 0; i < 2; i++) {
+                if constexpr (COUNTED)
+                    count[i] += (uint32_t)(v[k][i] >> 32);
+                else
+                    count[i] |= v[k][i];
                 units[i] += (uint32_t)v[k][i];
             }
     }
@@ -694,9 +715,9 @@ __global__ __launch_bounds__(THREADS) void k_range(SampleArgs a, RowScratch *scr
     if (top > -__builtin_inff() && s.rate >= 0.0 && cuts(s)) {
         if (on_grid(top, s.grid)) {
             const int shift = bin_of(tile_top, floorf(top * s.grid), s.grid);    // of lane's tile
-            const uint64_t *from = planes + row * tiles * BINS;
-            uint32_t count[EACH] = {};
-            uint64_t units[EACH] = {};
+            const uint64_t *from = planes + row * tiles * PLANE;
+            uint32_t count[2] = {};
+            uint64_t units[2] = {};
             if (s.k > 0)
                 add_tiles<true>(count, units, from, tiles, shift);
             else
@@ -706,8 +727,6 @@ __global__ __launch_bounds__(THREADS) void k_range(SampleArgs a, RowScratch *scr
             g.odd = 1;
         }
     }
-    if (tid < tiles)
-        r.sums[tid] = Sums{0, 0, 0};
     if (tid == 0) {
         r.setting = s;
         r.range = g;
@@ -818,7 +837,7 @@ __global__ __launch_bounds__(GATHER_THREADS, PER == 8 ? 8 : 4) void k_gather(Sam
     __shared__ uint64_t list[MOST];
     __shared__ Sums sums[GATHER_THREADS / 64];
     __shared__ uint32_t listed, base;
-    const int tid = threadIdx.x, tile = blockIdx.x / (THREADS / GATHER_THREADS);
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.y, i0 = ((int64_t)blockIdx.x * GATHER_THREADS + tid) * PER;
     RowScratch &r = scratch[row];
     float x[PER];
@@ -840,14 +859,7 @@ __global__ __launch_bounds__(GATHER_THREADS, PER == 8 ? 8 : 4) void k_gather(Sam
     if (tid == 0) {
         for (int i = 1; i < GATHER_THREADS / 64; i++)
             v = {v.kept + sums[i].kept, v.below + sums[i].below, v.limit + sums[i].limit};
-        // whole numbers: the order of the adds does not show
-        Sums &sum = r.sums[tile];
-        if (v.kept)
-            atomicAdd((unsigned long long *)&sum.kept, (unsigned long long)v.kept);
-        if (v.below)
-            atomicAdd((unsigned long long *)&sum.below, (unsigned long long)v.below);
-        if (v.limit)
-            atomicAdd((unsigned long long *)&sum.limit, (unsigned long long)v.limit);
+        r.sums[blockIdx.x] = v;
     }
     if (n == 0)
         return;
@@ -864,7 +876,7 @@ struct CutLds {
     uint32_t sub_count[SUBS];
     uint64_t sub_mass[SUBS];
     uint64_t in_sub[MOST_ALIKE];                 // those of one sub-bin
-    uint64_t tile_kept[MOST_TILES];
+    uint64_t part_kept[MOST_PARTS];
     uint64_t scan[WAVES];
     uint32_t scan32[WAVES];
     unsigned long long cut, low_mass, part;
@@ -941,7 +953,7 @@ __device__ __forceinline__ bool rank_in(CutLds &l, const uint64_t *list, uint32_
 // What a short list's cut is: threads in a row share an entry and count what comes
 // before it.
 __device__ __forceinline__ Cut rank_short(CutLds &l, const Setting &s, const Range &g, uint32_t n,
-                                          const Sums &all, float top, int tile_size)
+                                          const Sums &all, float top, int part_size)
 {
     const int tid = threadIdx.x;
     const float rate = s.grid, place = floorf(top * rate);
@@ -990,19 +1002,19 @@ __device__ __forceinline__ Cut rank_short(CutLds &l, const Setting &s, const Ran
     if (in && in_k && bin <= g.hi && inside(all.below + before, s.p, total)) {
         atomicMax(&l.cut, (unsigned long long)e);
         if (w >= s.min_w)
-            atomicAdd((unsigned long long *)&l.tile_kept[(uint32_t)e / tile_size],
+            atomicAdd((unsigned long long *)&l.part_kept[(uint32_t)e / part_size],
                       (unsigned long long)w);
     }
     __syncthreads();
     return Cut{~(uint32_t)(l.cut >> 32), (int64_t)(uint32_t)l.cut};
 }
 
-// The cut, from the list (n entries); adds what is kept of it to the tiles' sums.
+// The cut, from the list (n entries); adds what is kept of it to the parts' sums.
 // Sub-bins of the list's own range, in falling order, bring it down to the few
 // elements around a cut; those are ranked one by one.  false: too many are alike.
 __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Range &g,
                                           const uint64_t *list, uint32_t n, const Sums &all, float top,
-                                          int tile_size, Cut &c)
+                                          int part_size, Cut &c)
 {
     const int tid = threadIdx.x;
     const float rate = s.grid, place = floorf(top * rate);
@@ -1095,7 +1107,7 @@ __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Ran
         const uint64_t e = list[i];
         const uint64_t w = e <= cut ? weight(entry_value(e), top, s) : 0;
         if (w && w >= s.min_w)
-            atomicAdd((unsigned long long *)&l.tile_kept[(uint32_t)e / tile_size],
+            atomicAdd((unsigned long long *)&l.part_kept[(uint32_t)e / part_size],
                       (unsigned long long)w);
     }
     __syncthreads();
@@ -1103,57 +1115,72 @@ __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Ran
     return true;
 }
 
-// A row's end: from the sums (in tile_kept, too) and the list (its first entries in
-// LDS, too) to its token, or to its cut and the sum of what is kept.  x: tile
-// `mine`'s elements, or none (-1).
-template <int PER, int DT>
+// A row's end: from the sums of its parts (part_kept, too) and the list (its first
+// entries in LDS, too) to its token, or to its cut and the sum of what is kept.  A
+// part holds E elements a thread; x: the only part's, or not loaded.
+template <int E, int DT>
 __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, CutLds &l, RowLds &rl,
                                            const Setting &s, const Range &g, const Sums &all,
                                            const uint64_t *list, uint32_t n, uint32_t most,
-                                           float top, int tiles, Cut &c,
-                                           float (&x)[PER], int mine)
+                                           float top, int parts, Cut &c, float (&x)[E],
+                                           bool loaded)
 {
     const int tid = threadIdx.x, lane = tid & 63;
     bool ranked = !g.odd && n <= most;
     if (ranked && n) {
         if (n <= SHORT)
-            c = rank_short(l, s, g, n, all, top, PER * THREADS);
+            c = rank_short(l, s, g, n, all, top, E * THREADS);
         else
-            ranked = rank_list(l, s, g, n <= THREADS ? l.list : list, n, all, top, PER * THREADS, c);
+            ranked = rank_list(l, s, g, n <= THREADS ? l.list : list, n, all, top, E * THREADS, c);
     }
     if (!ranked) {
         const Walker walker{a.logits, row * a.stride, a.vocab, a.dtype, top};
         c = find_cut(walker, s, rl);
         return walk_row(a, walker, s, c, row, rl);
     }
-    // the tile, then the element in it, where the running sum passes u
-    const uint64_t v = lane < tiles ? l.tile_kept[lane] : 0, run = scan_wave(v);
+    // the part, then the element in it, where the running sum passes u
+    const int each = (parts + 63) / 64;          // of a lane
+    uint64_t v = 0;
+    for (int i = lane * each; i < min(lane * each + each, parts); i++)
+        v += l.part_kept[i];
+    const uint64_t run = scan_wave(v);
     const uint64_t sum = lane_value(run, 63), thr = place_in(s.u, sum);
     if (a.probs)
         return sum;
-    const int tile = __builtin_ctzll(__ballot(run > thr));
-    const int64_t j0 = ((int64_t)tile * THREADS + tid) * PER;
-    if (tile != mine)
-        load_tile<PER, DT>(x, a, row, j0);
-    uint64_t w[PER] = {}, own = 0, whole;
+    const int at_lane = __builtin_ctzll(__ballot(run > thr));
+    int part = at_lane * each;
+    uint64_t at = lane_value(run - v, at_lane);
+    for (int i = 1; i < each; i++)
+        if (at + l.part_kept[part] <= thr)
+            at += l.part_kept[part++];
+    const int64_t j0 = ((int64_t)part * THREADS + tid) * E;
+    if (!loaded) {
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const float one =
+                j0 + e < a.vocab ? load_one(a.logits, DT, row * a.stride + j0 + e) : -__builtin_inff();
+            x[e] = one != one ? -__builtin_inff() : one;
+        }
+    }
+    uint64_t w[E] = {}, own = 0, whole;
     uint32_t in = 0;
 #pragma unroll
-    for (int e = 0; e < PER; e++)
+    for (int e = 0; e < E; e++)
         in |= kept(c, order_key(x[e]), j0 + e) ? 1u << e : 0u;
     if (__any(in)) {
 #pragma unroll
-        for (int e = 0; e < PER; e++) {
+        for (int e = 0; e < E; e++) {
             w[e] = weight(x[e], top, s);
             w[e] = (in >> e & 1) && w[e] >= s.min_w ? w[e] : 0;
             own += w[e];
         }
     }
     __syncthreads();
-    uint64_t at = lane_value(run - v, tile) + scan_before<WAVES>(own, l.scan, whole);
+    at += scan_before<WAVES>(own, l.scan, whole);
     if (at <= thr && thr < at + own) {
         int hit = 0;
 #pragma unroll
-        for (int e = 0; e < PER; e++) {
+        for (int e = 0; e < E; e++) {
             at += w[e];
             hit += at <= thr;
         }
@@ -1196,14 +1223,15 @@ __global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scrat
         Sums v{0, 0, 0};
         const uint32_t n = r.listed;
         const Range g = r.range;
-        if (tid < tiles) {
+        if (tid < tiles * PARTS) {
             v = r.sums[tid];
-            l.tile_kept[tid] = v.kept;
+            l.part_kept[tid] = v.kept;
         }
         l.list[tid] = e0;
         const Sums all = sum_up(v, sums);
-        float x[PER];
-        sum = finish<PER, DT>(a, row, l, rl, s, g, all, r.list, n, LIST, top, tiles, c, x, -1);
+        float x[PER / PARTS];
+        sum = finish<PER / PARTS, DT>(a, row, l, rl, s, g, all, r.list, n, LIST, top, tiles * PARTS, c,
+                                      x, false);
     }
     if (a.probs && tid == 0) {
         r.key = c.key;
@@ -1304,11 +1332,11 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
                 const bool counted = s.k > 0;
                 add_bins(x, top, s.grid, counted, bins);
                 __syncthreads();
-                uint32_t count[EACH];
-                uint64_t units[EACH];
+                uint32_t count[2];
+                uint64_t units[2];
 #pragma unroll
-                for (int i = 0; i < EACH; i++) {
-                    const int b = tid + i * THREADS;
+                for (int i = 0; i < 2; i++) {
+                    const int b = 2 * tid + i;
                     units[i] = counted ? (uint32_t)bins[b] : ((const uint32_t *)bins)[b];
                     count[i] = counted ? (uint32_t)(bins[b] >> 32) : units[i] != 0;
                 }
@@ -1319,12 +1347,12 @@ template <int PER, int DT> __global__ __launch_bounds__(THREADS) void k_one(Samp
         }
         const Sums all = sum_up(gather(x, i0, top, s, g, list, PER * THREADS, &listed), sums);
         const uint32_t n = listed;
-        if (tid < MOST_TILES)
-            l.tile_kept[tid] = tid ? 0 : all.kept;
+        if (tid == 0)
+            l.part_kept[0] = all.kept;
         if (tid < n)
             l.list[tid] = list[tid];
         __syncthreads();
-        sum = finish<PER, DT>(a, row, l, rl, s, g, all, list, n, PER * THREADS, top, 1, c, x, 0);
+        sum = finish<PER, DT>(a, row, l, rl, s, g, all, list, n, PER * THREADS, top, 1, c, x, true);
     }
     if (a.probs)
         write_probs(a, row, i0, x, top, s, c, sum);
@@ -1341,7 +1369,7 @@ int64_t tiles_of(int64_t vocab)
 }
 
 // Rows of one launch: those whose scratch takes up to 256 MiB (several hundred).
-size_t row_bytes(int64_t tiles) { return sizeof(RowScratch) + tiles * BINS * sizeof(uint64_t); }
+size_t row_bytes(int64_t tiles) { return sizeof(RowScratch) + tiles * PLANE * sizeof(uint64_t); }
 
 int64_t rows_a_launch(int64_t rows, int64_t tiles)
 {
@@ -1359,7 +1387,7 @@ hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t 
         const dim3 grid((unsigned)tiles, (unsigned)n);
         k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
         k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)tiles);
-        k_gather<PER, DT><<<dim3((unsigned)(tiles * (THREADS / GATHER_THREADS)), (unsigned)n),
+        k_gather<PER, DT><<<dim3((unsigned)(tiles * PARTS), (unsigned)n),
                             GATHER_THREADS, 0, s>>>(a, r);
         k_cut<PER, DT><<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, (int)tiles);
         if (a.probs)
