@@ -88,12 +88,20 @@ __device__ __forceinline__ double whole_exp2(double t)
     return __builtin_bit_cast(double, scaled) + 0x1p52;
 }
 
+constexpr uint64_t LOW52 = (uint64_t(1) << 52) - 1;
+
+// w of 2^52 + w.
+__device__ __forceinline__ uint64_t whole_bits(double v)
+{
+    return __builtin_bit_cast(uint64_t, v) & LOW52;
+}
+
 // A weight in units of 2^-bits; 0 for what is no number, or -infinity.
 __device__ __forceinline__ uint64_t weight(float x, float top, const Setting &s)
 {
     const double t = ((double)x - (double)top) * s.rate + (double)s.bits;
     // 1/4 rounds to 0, and so do NaN and what is far below
-    const uint64_t w = __builtin_bit_cast(uint64_t, whole_exp2(fmax(t, -2.0))) & 0xFFFFFFFFFFFFFull;
+    const uint64_t w = whole_bits(whole_exp2(fmax(t, -2.0)));
     const uint64_t got = x > -__builtin_inff() ? w : 0;
     return x == top ? uint64_t(1) << s.bits : got;
 }
@@ -766,25 +774,27 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
         for (int e = 0; e < PER; e++) {
             const uint64_t w = weight(x[e], top, s);
             mine.kept += w >= s.min_w ? w : 0;
+            mine.below += w;
         }
         return mine;
     }
+    const float lo = (float)g.lo, hi = (float)g.hi;
     float d[PER];
-    const float end = (float)(g.kbin < BINS ? g.kbin + 1 : BINS);
-    bool some = false;
 #pragma unroll
-    for (int e = 0; e < PER; e++) {
+    for (int e = 0; e < PER; e++)
         d[e] = place - floorf(x[e] * rate);
-        some = some || d[e] < end;
-    }
-    if (!__any(some))
-        return mine;                             // a wave of what top-k leaves out
-    const float lo = (float)g.lo, hi = (float)g.hi, kbin = (float)g.kbin;
-    // whole numbers below 2^50: exact in any order
-    const double min_w = (double)s.min_w;
-    double kept = 0.0, below = 0.0, limit = 0.0;
     uint32_t question = 0;
     if (g.kbin < BINS) {                         // top-k leaves few
+        const float kbin = (float)g.kbin, end = kbin + 1.0f;
+        bool some = false;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            some = some || d[e] < end;
+        if (!__any(some))
+            return mine;                         // a wave of what top-k leaves out
+        // whole numbers below 2^50: exact in any order
+        const double min_w = (double)s.min_w;
+        double kept = 0.0, below = 0.0, limit = 0.0;
 #pragma unroll
         for (int e = 0; e < PER; e++)
             if (d[e] < end) {
@@ -794,25 +804,31 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
                 kept += b >= min_w ? b : 0.0;
                 question |= w > 0.0 && ((d[e] >= lo && d[e] <= hi) || d[e] == kbin) ? 1u << e : 0u;
             }
+        mine = {whole_bits(kept + 0x1p52), whole_bits(below + 0x1p52), whole_bits(limit + 0x1p52)};
     } else {
-        // the weights of all without branches, for their instructions to overlap
-        double b[PER];
+        // Without branches, for the weights' instructions to overlap.  Each is 2^52 + w,
+        // whose bits as whole numbers add up to the sum of w in their low 52.  What is
+        // in no bin weighs nothing; what weighs nothing is in no prefix, listed or not.
+        double w[PER];
+        uint64_t below = 0, limit = 0;
 #pragma unroll
         for (int e = 0; e < PER; e++) {
-            double w = weight_in_bin(x[e], top, s);
-            w = d[e] < end ? w : 0.0;
-            b[e] = d[e] < lo ? w : 0.0;
-            limit += w;
-            below += b[e];
-            question |= w > 0.0 && d[e] >= lo && d[e] <= hi ? 1u << e : 0u;
+            w[e] = whole_exp2(fmax(((double)x[e] - (double)top) * s.rate + (double)s.bits, -2.0));
+            const uint64_t bits = __builtin_bit_cast(uint64_t, w[e]);
+            const bool under = d[e] < lo;
+            limit += bits;
+            below += under ? bits : 0;
+            question |= (uint32_t)(!under && d[e] <= hi) << e;
         }
-        kept = below;
+        uint64_t kept = below;
         if (s.min_w) {
-            kept = 0.0;
+            const double least = 0x1p52 + (double)s.min_w;
+            kept = 0;
 #pragma unroll
             for (int e = 0; e < PER; e++)
-                kept += b[e] >= min_w ? b[e] : 0.0;
+                kept += d[e] < lo && w[e] >= least ? __builtin_bit_cast(uint64_t, w[e]) : 0;
         }
+        mine = {kept & LOW52, below & LOW52, limit & LOW52};
     }
     if (question) {
         uint32_t at = atomicAdd(listed, (uint32_t)__builtin_popcount(question));
@@ -824,7 +840,7 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
                 at++;
             }
     }
-    return Sums{(uint64_t)kept, (uint64_t)below, (uint64_t)limit};
+    return mine;
 }
 
 // Small workgroups, four for a tile, so that some load while others compute (128
@@ -851,7 +867,9 @@ __global__ __launch_bounds__(GATHER_THREADS, PER == 8 ? 8 : 4) void k_gather(Sam
         listed = 0;
     __syncthreads();
     Sums v = gather(x, i0, top, s, g, list, MOST, &listed);
-    v = {wave_sum(v.kept), wave_sum(v.below), wave_sum(v.limit)};
+    v.below = wave_sum(v.below);
+    v.kept = s.min_w ? wave_sum(v.kept) : v.below;
+    v.limit = wave_sum(v.limit);
     if ((tid & 63) == 0)
         sums[tid >> 6] = v;
     __syncthreads();
