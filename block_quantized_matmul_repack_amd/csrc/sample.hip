@@ -483,6 +483,7 @@ __device__ __forceinline__ int bin_of(float x, float place, float rate)
 
 __device__ __forceinline__ bool cuts(const Setting &s) { return s.k > 0 || s.p < 1.0; }
 
+// -infinity past the row's end.  A NaN has no bin, no weight and the key of -infinity.
 template <int PER, int DT>
 __device__ __forceinline__ void load_tile(float (&x)[PER], const SampleArgs &a, int64_t row,
                                           int64_t i0)
@@ -500,7 +501,7 @@ __device__ __forceinline__ void load_tile(float (&x)[PER], const SampleArgs &a, 
         }
 #pragma unroll
         for (int k = 0; k < 8; k++)
-            x[e + k] = v[k] != v[k] ? -__builtin_inff() : v[k];
+            x[e + k] = v[k];
     }
 }
 
@@ -520,14 +521,16 @@ template <int PER>
 __device__ __forceinline__ void add_bins(const float (&x)[PER], float top, float rate, bool counted,
                                          uint64_t *bins)
 {
+    constexpr float ONE = 1 << MASS_BITS;
     const float place = floorf(top * rate);
 #pragma unroll
     for (int e = 0; e < PER; e++) {
         const float whole = floorf(x[e] * rate), d = place - whole;
         if (d < (float)BINS) {
+            // e^(part / BIN_RATE) of 0 <= part < 1: a square's error is below 2^-20
             const float part = fmaf(x[e], rate, -whole);
-            const float m = __builtin_amdgcn_exp2f(part * (1.44269504f / BIN_RATE));
-            const uint32_t units = (uint32_t)fmaf(m, (float)(1 << MASS_BITS), 0.5f);
+            const float more = fmaf(part, ONE / (2 * BIN_RATE * BIN_RATE), ONE / BIN_RATE);
+            const uint32_t units = (uint32_t)fmaf(part, more, ONE + 0.5f);
             if (counted)
                 atomicAdd((unsigned long long *)&bins[(int)d], (1ull << 32) | units);
             else
@@ -1174,11 +1177,9 @@ __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, Cut
     const int64_t j0 = ((int64_t)part * THREADS + tid) * E;
     if (!loaded) {
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-            const float one =
-                j0 + e < a.vocab ? load_one(a.logits, DT, row * a.stride + j0 + e) : -__builtin_inff();
-            x[e] = one != one ? -__builtin_inff() : one;
-        }
+        for (int e = 0; e < E; e++)
+            x[e] = j0 + e < a.vocab ? load_one(a.logits, DT, row * a.stride + j0 + e)
+                                    : -__builtin_inff();
     }
     uint64_t w[E] = {}, own = 0, whole;
     uint32_t in = 0;
