@@ -424,6 +424,7 @@ constexpr float STEP = 0.98347145f;
 constexpr int GUARD = 4, PLANE = GUARD + BINS;   // a tile's bins in scratch, behind entries of nothing
 constexpr int MASS_BITS = 17;                    // of a bin's first weight: 16384 elements fit 32 bits
 constexpr int MOST_TILES = 64;
+constexpr int PAIRS = 1024;                      // tiles of a launch from which two share their bins
 constexpr int LIST = 32768;                      // entries of a row
 constexpr int GATHER_THREADS = 256;
 constexpr int PARTS = THREADS / GATHER_THREADS, MOST_PARTS = MOST_TILES * PARTS;    // of a tile, a row
@@ -1209,7 +1210,8 @@ __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, Cut
 }
 
 template <int PER, int DT>
-__global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scratch, int tiles)
+__global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scratch, int tiles,
+                                                 int parts)
 {
     __shared__ CutLds l;
     __shared__ RowLds rl;
@@ -1242,15 +1244,15 @@ __global__ __launch_bounds__(THREADS) void k_cut(SampleArgs a, RowScratch *scrat
         Sums v{0, 0, 0};
         const uint32_t n = r.listed;
         const Range g = r.range;
-        if (tid < tiles * PARTS) {
+        if (tid < parts) {
             v = r.sums[tid];
             l.part_kept[tid] = v.kept;
         }
         l.list[tid] = e0;
         const Sums all = sum_up(v, sums);
         float x[PER / PARTS];
-        sum = finish<PER / PARTS, DT>(a, row, l, rl, s, g, all, r.list, n, LIST, top, tiles * PARTS, c,
-                                      x, false);
+        sum = finish<PER / PARTS, DT>(a, row, l, rl, s, g, all, r.list, n, LIST, top, parts, c, x,
+                                      false);
     }
     if (a.probs && tid == 0) {
         r.key = c.key;
@@ -1404,11 +1406,16 @@ hipError_t launch_tiles(SampleArgs a, int64_t tiles, void *scratch, hipStream_t 
     for (int64_t at = 0; at < rows; at += most) {
         const int64_t n = std::min(rows - at, most);
         const dim3 grid((unsigned)tiles, (unsigned)n);
-        k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
-        k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)tiles);
+        const bool pairs = PER == 8 && n * tiles >= PAIRS;
+        const int64_t binned = pairs ? (tiles + 1) / 2 : tiles;
+        if (pairs)
+            k_bins<16, DT><<<dim3((unsigned)binned, (unsigned)n), THREADS, 0, s>>>(a, r, planes);
+        else
+            k_bins<PER, DT><<<grid, THREADS, 0, s>>>(a, r, planes);
+        k_range<<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, planes, (int)binned);
         k_gather<PER, DT><<<dim3((unsigned)(tiles * PARTS), (unsigned)n),
                             GATHER_THREADS, 0, s>>>(a, r);
-        k_cut<PER, DT><<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, (int)tiles);
+        k_cut<PER, DT><<<dim3((unsigned)n), THREADS, 0, s>>>(a, r, (int)binned, (int)tiles * PARTS);
         if (a.probs)
             k_probs<PER, DT><<<grid, THREADS, 0, s>>>(a, r);
         const hipError_t e = hipGetLastError();
