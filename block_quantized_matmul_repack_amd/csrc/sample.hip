@@ -413,7 +413,7 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 // k_probs writes the distribution instead.
 // A vocabulary of one tile takes one launch (k_one) and no scratch.  Rows that the
 // grid does not suit (logits far above the temperature) or whose list does not fit
-// (tens of thousands of logits within 2 %, or thousands of equal ones) are left to
+// (tens of thousands of logits within 2 %, thousands within 2e-5) are left to
 // the search through the whole row, by k_cut's workgroup: 0.4 ms for 128001.
 
 // 32 in the exponent and more weigh nothing (2^-46); a bin more for the grid.
@@ -904,7 +904,7 @@ struct CutLds {
     uint64_t scan[WAVES];
     uint32_t scan32[WAVES];
     unsigned long long cut, low_mass, part;
-    uint32_t low, least, most, n_in;
+    uint32_t low, least, most, n_in, sub_least, sub_most;
     int k_sub, p_sub;
     uint32_t sub_before;
     uint64_t sub_mass_before;
@@ -916,25 +916,78 @@ struct Ranked {
     uint64_t before;
 };
 
-// The entries of sub-bin `sub`, each with how many and how much of the list come
-// before it; false (nothing done) if they do not fit.
-template <typename F>
-__device__ __forceinline__ bool rank_in(CutLds &l, const uint64_t *list, uint32_t n, int sub,
-                                        uint32_t least, int shift, float top, const Setting &s, F f)
+// Brings the entries of sub-bin `sub` together, as far as they fit, and says whether
+// their logits are all equal.
+__device__ __forceinline__ bool collect(CutLds &l, const uint64_t *list, uint32_t n, int sub,
+                                        uint32_t least, int shift)
 {
     const int tid = threadIdx.x;
-    if (tid == 0)
-        l.n_in = 0;
+    if (tid == 0) {
+        l.n_in = l.sub_most = 0;
+        l.sub_least = ~0u;
+    }
     __syncthreads();
     for (uint32_t i = tid; i < n; i += THREADS) {
         const uint64_t e = list[i];
-        if ((int)(((uint32_t)(e >> 32) - least) >> shift) == sub) {
+        const uint32_t key = (uint32_t)(e >> 32);
+        if ((int)((key - least) >> shift) == sub) {
             const uint32_t at = atomicAdd(&l.n_in, 1u);
             if (at < MOST_ALIKE)
                 l.in_sub[at] = e;
+            atomicMin(&l.sub_least, key);
+            atomicMax(&l.sub_most, key);
         }
     }
     __syncthreads();
+    return l.sub_least == l.sub_most;
+}
+
+// The m-th entry (from 1) of equal logits, key in the list, into l.cut: by sub-bins of
+// the index, then among the few of one (vocabularies of tiles: up to 2048).
+__device__ __forceinline__ void nth_alike(CutLds &l, const uint64_t *list, uint32_t n, uint32_t key,
+                                          uint32_t m, int64_t vocab)
+{
+    const int tid = threadIdx.x;
+    const int shift = max(32 - __builtin_clz((uint32_t)vocab | 1) - 10, 0);
+    l.sub_count[tid] = 0;
+    if (tid == 0)
+        l.n_in = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < n; i += THREADS)
+        if ((uint32_t)(list[i] >> 32) == key)
+            atomicAdd(&l.sub_count[(uint32_t)list[i] >> shift], 1u);
+    __syncthreads();
+    const uint32_t own = l.sub_count[tid];
+    uint32_t all;
+    const uint32_t before = scan_before<WAVES>(own, l.scan32, all);
+    if (before < m && m <= before + own) {
+        l.low = tid;
+        l.sub_before = before;
+    }
+    __syncthreads();
+    const uint32_t sub = l.low, need = m - l.sub_before;
+    for (uint32_t i = tid; i < n; i += THREADS)
+        if ((uint32_t)(list[i] >> 32) == key && (uint32_t)list[i] >> shift == sub)
+            l.in_sub[atomicAdd(&l.n_in, 1u)] = list[i];
+    __syncthreads();
+    const uint32_t few = l.n_in;
+    for (uint32_t i = tid; i < few; i += THREADS) {
+        const uint64_t e = l.in_sub[i];
+        uint32_t rank = 1;
+        for (uint32_t j = 0; j < few; j++)
+            rank += l.in_sub[j] < e;
+        if (rank == need)
+            l.cut = e;
+    }
+    __syncthreads();
+}
+
+// The entries collected of a sub-bin, each with how many and how much of the list come
+// before it; false (nothing done) if they do not fit.
+template <typename F>
+__device__ __forceinline__ bool rank_in(CutLds &l, float top, const Setting &s, F f)
+{
+    const int tid = threadIdx.x;
     const uint32_t m = l.n_in, rank0 = l.sub_before;
     const uint64_t before0 = l.sub_mass_before;
     if (m > MOST_ALIKE)
@@ -1038,7 +1091,7 @@ __device__ __forceinline__ Cut rank_short(CutLds &l, const Setting &s, const Ran
 // elements around a cut; those are ranked one by one.  false: too many are alike.
 __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Range &g,
                                           const uint64_t *list, uint32_t n, const Sums &all, float top,
-                                          int part_size, Cut &c)
+                                          int part_size, int64_t vocab, Cut &c)
 {
     const int tid = threadIdx.x;
     const float rate = s.grid, place = floorf(top * rate);
@@ -1106,13 +1159,18 @@ __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Ran
             l.sub_before = before;
             l.sub_mass_before = mass_before;
         }
-        if (!rank_in(l, list, n, l.k_sub, least, shift, top, s,
-                     [&](uint64_t, uint64_t w, const Ranked &r) {
-                         if (r.rank < k_rank)
-                             atomicAdd(&l.part, (unsigned long long)w);
-                     }))
-            return false;
-        total += l.sub_mass_before + l.part - l.low_mass;
+        if (collect(l, list, n, l.k_sub, least, shift)) {
+            const uint64_t w = weight(key_value(~l.sub_least), top, s);
+            total += min(l.n_in, k_rank - l.sub_before) * w;
+        } else {
+            if (!rank_in(l, top, s, [&](uint64_t, uint64_t w, const Ranked &r) {
+                    if (r.rank < k_rank)
+                        atomicAdd(&l.part, (unsigned long long)w);
+                }))
+                return false;
+            total += l.part;
+        }
+        total += l.sub_mass_before - l.low_mass;
     }
     note_last(count && before < k_rank && inside(all.below + mass_before, s.p, total), tid, &l.p_sub);
     __syncthreads();
@@ -1120,12 +1178,18 @@ __device__ __forceinline__ bool rank_list(CutLds &l, const Setting &s, const Ran
         l.sub_before = before;
         l.sub_mass_before = mass_before;
     }
-    if (!rank_in(l, list, n, l.p_sub, least, shift, top, s,
-                 [&](uint64_t e, uint64_t, const Ranked &r) {
-                     if (r.rank < k_rank && inside(all.below + r.before, s.p, total))
-                         atomicMax(&l.cut, (unsigned long long)e);
-                 }))
+    if (collect(l, list, n, l.p_sub, least, shift)) {
+        const uint32_t key = l.sub_least, m = min(l.n_in, k_rank - l.sub_before);
+        const uint64_t w = weight(key_value(~key), top, s), ahead = all.below + l.sub_mass_before;
+        const uint32_t in = s.p < 1.0 ? ties_inside(ahead, w, m, s.p, total) : m;
+        __syncthreads();
+        nth_alike(l, list, n, key, in, vocab);
+    } else if (!rank_in(l, top, s, [&](uint64_t e, uint64_t, const Ranked &r) {
+                   if (r.rank < k_rank && inside(all.below + r.before, s.p, total))
+                       atomicMax(&l.cut, (unsigned long long)e);
+               })) {
         return false;
+    }
     const uint64_t cut = l.cut;
     for (uint32_t i = tid; i < n; i += THREADS) {
         const uint64_t e = list[i];
@@ -1155,7 +1219,8 @@ __device__ __forceinline__ uint64_t finish(const SampleArgs &a, int64_t row, Cut
         if (n <= SHORT)
             c = rank_short(l, s, g, n, all, top, E * THREADS);
         else
-            ranked = rank_list(l, s, g, n <= THREADS ? l.list : list, n, all, top, E * THREADS, c);
+            ranked = rank_list(l, s, g, n <= THREADS ? l.list : list, n, all, top, E * THREADS,
+                               a.vocab, c);
     }
     if (!ranked) {
         const Walker walker{a.logits, row * a.stride, a.vocab, a.dtype, top};

@@ -213,3 +213,23 @@ def test_the_longest_rows(V, dtype):
     x[2, ::3] = -INF
     check(x, u, [0.8, 1.0, 0.0], [0, 40, 3], [0.95, 1.0, 0.5], [0.0, 0.02, 0.1])
     check(x[:2], u[:2], [1.0, 0.6], [100000, 0], [0.5, 0.05])
+
+
+@pytest.mark.parametrize("V", [3000, 8192, 40000, 530000])
+def test_thousands_of_equal_logits_at_the_cut(V):
+    """Which of the equal ones are kept, wherever they lie: evenly, all at one end, or
+    among others close by."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((6, V), -9.0)
+    x[0, torch.randperm(V, generator=g)[:2000]] = 1.0
+    x[1, :2000] = 1.0
+    x[2, V - 2000:] = 1.0
+    x[3] = 1.0 + 2.0 ** -9 * torch.randint(0, 3, (V,), generator=g)
+    x[4] = 1.0 + 1e-5 * torch.rand(V, generator=g)
+    x[4, ::3] = 1.0
+    x[5, :7] = 3.0
+    x[5, V - 2500:] = 1.0
+    x, u = x.cuda(), [0.0, 0.2, 0.4, 0.6, 0.8, 0.999]
+    check(x, u, top_k=[1, 500, 1999, 900, 1500, 2000])
+    check(x, u, top_p=[0.3, 0.5, 0.9, 0.2, 0.05, 0.7])
+    check(x, u, top_k=[1700, 1500, 1999, 2500, 900, 2000], top_p=[0.3, 0.9, 0.5, 0.99, 0.6, 0.7])
