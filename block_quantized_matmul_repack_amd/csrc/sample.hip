@@ -14,11 +14,13 @@
 // Of rows of several tiles four launches read the logits twice: bins (k_bins),
 // the bins that the cuts are in (k_range), those bins' elements and the tiles' sums
 // of the others (k_gather), the cuts and the token (k_cut); distributions are a
-// third reading (k_probs).  us of each, rows of 128001: one, all filters, 4.4 + 7.6 +
-// 3.8 + 7.2, latency; 64, top-p, 11.8 + 7.3 + 18.9 + 12.4, where 13 of k_gather's are
+// third reading (k_probs).  us of each, rows of 128001: one, all filters, 4.1 + 5.8 +
+// 3.8 + 6.0, latency; 64, top-p, 10.2 + 4.2 + 15.8 + 10.5, where 11 of k_gather's are
 // its vector instructions, most of them the fp64 of the weights (two readings from
-// memory are 9); 128 of bf16, top-k and top-p, 19.6 + 9.0 + 13.4 + 5.8 and
-// k_probs 22.0, 4.5 TB/s.  A workgroup for each row that does it all took 418 us for
+// memory are 9); 128 of bf16, top-k and top-p, 16.6 + 6.0 + 12.2 + 5.8 and
+// k_probs 21.9, 4.5 TB/s.  The launches of one workgroup a row are bound by its own
+// instructions (400 to 800 a wave, sixteen waves on a unit: 3 to 6 us), whence a pair
+// of bins and few elements a thread there.  A workgroup for each row that does it all took 418 us for
 // one row and 493 for 64.
 #include <algorithm>
 #include <type_traits>
@@ -407,14 +409,14 @@ __global__ __launch_bounds__(THREADS) void k_sample_row(SampleArgs a)
 // weights lie within 2 % of each other.
 // k_range: one workgroup a row adds up its bins and learns in which of them top-k and
 // top-p cut (the masses err by a known margin, so at times two come into question).
-// k_gather: each workgroup, a quarter of a tile, sums the exact weights of what is surely kept, and lists
-// the elements of the bins in question.
+// k_gather: each workgroup, a quarter of a tile (a part), sums the exact weights of what
+// is surely kept, and lists the elements of the bins in question.
 // k_cut: one workgroup a row ranks the list, which gives the cut, and draws.
 // k_probs writes the distribution instead.
 // A vocabulary of one tile takes one launch (k_one) and no scratch.  Rows that the
 // grid does not suit (logits far above the temperature) or whose list does not fit
 // (tens of thousands of logits within 2 %, thousands within 2e-5) are left to
-// the search through the whole row, by k_cut's workgroup: 0.4 ms for 128001.
+// the search through the whole row, by k_cut's workgroup: 0.5 ms for 128001.
 
 // 32 in the exponent and more weigh nothing (2^-46); a bin more for the grid.
 constexpr int BINS = 2048, EACH = BINS / THREADS;
@@ -850,8 +852,8 @@ __device__ __forceinline__ Sums gather(const float (&x)[PER], int64_t i0, float 
 }
 
 // Small workgroups, four for a tile, so that some load while others compute (128
-// rows of 128001, top-k and top-p: 13 us, one for a tile 17; 64 rows, top-p alone: 19
-// both ways).
+// rows of 128001, top-k and top-p: 13 us, one for a tile 17; 64 rows, top-p alone,
+// level).
 template <int PER, int DT>
 __global__ __launch_bounds__(GATHER_THREADS, PER == 8 ? 8 : 4) void k_gather(SampleArgs a, RowScratch *scratch)
 {
