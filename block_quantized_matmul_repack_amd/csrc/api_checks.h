@@ -60,6 +60,38 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
     return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// An array of `rows` rows of n bytes, `stride` bytes apart (0: one for all).
+struct Span {
+    const void *p;
+    int64_t stride, n, rows;
+};
+
+// Whether rows of the two have a byte in common; rows that lie between each other's
+// (columns of one buffer) do not.
+bool meet(const Span &a, const Span &b)
+{
+    if (a.rows < 1 || b.rows < 1 ||
+        !overlap(a.p, (a.rows - 1) * a.stride + a.n, b.p, (b.rows - 1) * b.stride + b.n))
+        return false;
+    const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    // Row j of b and a row at place `at` of a meet if at - b.n < d + j * b.stride < at
+    // + a.n; the first j from `least` on that passes the lower end
+    auto any = [&](int64_t at, int64_t least, int64_t rows) {
+        const int64_t below = at - b.n - d;
+        int64_t j = least;
+        if (b.stride && below >= j * b.stride)
+            j += (below - j * b.stride) / b.stride + 1;
+        const int64_t place = d + j * b.stride;
+        return j < rows && place > at - b.n && place < at + a.n;
+    };
+    if (a.stride == b.stride)                    // j: b's row less a's
+        return any(0, 1 - a.rows, b.rows);
+    for (int64_t i = 0; i < a.rows; i++)
+        if (any(i * a.stride, 0, b.rows))
+            return true;
+    return false;
+}
+
 // The scratch region of a workspace of `bytes` bytes, or a status.
 int scratch_of(void *workspace, size_t bytes, size_t need, uint32_t **counters, void **scratch)
 {

@@ -110,6 +110,24 @@ int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const 
         !aligned(post_weight, wal) || !aligned(pre_weight, wal) || !aligned(gate, wal) ||
         !aligned(q, 4) || !aligned(d, 2))
         return TQ_E_ALIGN;
+    // rows are read by other workgroups than those that write near them; only x' may take
+    // x's place, and z that of x', which it then is
+    const int64_t one = al, wone = wal, yone = size_of(y_dtype), T = tokens;
+    const Span ins[] = {{y, y_ts * yone, N * yone, T}, {x, x_ts * one, N * one, T},
+                        {post_weight, 0, N * wone, 1}, {pre_weight, 0, N * wone, 1},
+                        {gate, gate_ts * wone, gate_es ? N * wone : wone, T}};
+    const bool same_z = z == x_out && !pre_weight && (z_ts == xo_ts || T == 1);
+    const Span outs[] = {{x_out, xo_ts * one, N * one, T},
+                         {same_z ? nullptr : z, z_ts * one, N * one, T},
+                         {q, N, N, T}, {d, N / 32 * 2, N / 32 * 2, T}};
+    for (int o = 0; o < 4; o++) {
+        for (int i = 0; i < 5; i++)
+            if (!(o == 0 && i == 1 && x == x_out) && meet(outs[o], ins[i]))
+                return TQ_E_SHAPE;
+        for (int i = 0; i < o; i++)
+            if (meet(outs[o], outs[i]))
+                return TQ_E_SHAPE;
+    }
     const tq::ResNormArgs a{y, x, y_ts, x_ts, y_dtype, w_dtype, post_weight, pre_weight, gate,
                             gate_ts, gate_es, scale, eps, tokens, (int)N, x_out, z, xo_ts, z_ts,
                             q, d};

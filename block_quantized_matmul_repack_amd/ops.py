@@ -838,7 +838,8 @@ def residual_norm(y, x, pre_weight=None, post_weight=None, gate=None, scale=1.0,
     fp16), normed (RMS) and times post_weight [N] if that is given; z is x' (of
     x's type), normed and times pre_weight [N] if given, in x's type or, with
     quantize, as the int8 activations (q [T, N], d [T, N/32]) that matmul takes.
-    gate: [N], [T, N], [T, 1] or [1], of the weights' type.  x_out may be x.
+    gate: [N], [T, N], [T, 1] or [1], of the weights' type.  x_out may be x; outputs
+    that overlap an input otherwise, or each other, are refused.
     Returns (x', z) or (x', (q, d))."""
     name = "tq_residual_norm"
     dtype, dev, shape = x.dtype, x.get_device(), x.shape

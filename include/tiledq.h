@@ -617,7 +617,9 @@ int tq_release_pages(int64_t batch, const int32_t *done, const int32_t *owned, i
  *   z       : of dtype at row stride z_ts, or NULL and instead
  *   q, d    : int8 [tokens][N] (4-byte aligned) and fp16 bits [tokens][N/32], z
  *             by tq_quantize_act's rule (from its fp32 value), for tq_matmul.
- * Outputs must not overlap inputs otherwise.  Domain: N 1..32768 (with q: a
+ * Outputs must not overlap inputs otherwise, nor one another (TQ_E_SHAPE; rows
+ * between each other's, as columns of one buffer are, do not), but for z, which may
+ * be x_out (same stride) without a pre_weight.  Domain: N 1..32768 (with q: a
  * multiple of 32), tokens 0..2^20, scale finite. */
 int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const void *x,
                      int64_t x_ts, int64_t tokens, int64_t N, int w_dtype, const void *post_weight,
