@@ -166,6 +166,18 @@ int sample(int dtype, const void *logits, int64_t stride, int64_t rows, int64_t 
         !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(uniforms, 4) || !aligned(tokens, 4) ||
         !aligned(probs, 4))
         return TQ_E_ALIGN;
+    // a row's logits are read by several workgroups and launches; the last one reads
+    // each element where it writes its probability, if anywhere
+    const int64_t size = size_of(dtype);
+    const Span ins[] = {{logits, stride * size, vocab * size, rows}, {temperature, 0, 4 * rows, 1},
+                        {top_k, 0, 4 * rows, 1}, {top_p, 0, 4 * rows, 1}, {min_p, 0, 4 * rows, 1},
+                        {uniforms, 0, 4 * rows, 1}};
+    const Span out = probs ? Span{probs, probs_stride * 4, vocab * 4, rows}
+                           : Span{tokens, 0, 4 * rows, 1};
+    const bool in_place = probs == logits && dtype == TQ_F32 && (probs_stride == stride || rows == 1);
+    for (int i = in_place ? 1 : 0; i < 6; i++)
+        if (meet(out, ins[i]))
+            return TQ_E_SHAPE;
     uint32_t *counters;                          // unused: the layout that all calls share
     void *scratch;
     const int st = scratch_of(workspace, workspace_bytes,

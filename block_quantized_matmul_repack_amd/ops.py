@@ -951,7 +951,7 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
 
 def sample_probs(logits, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
     """The distributions fp32 [N, V] that sample draws from: a target or draft of
-    verify_draft."""
+    verify_draft.  out may be fp32 logits."""
     name = "tq_sample_probs"
     code, dev, N, V, ptr = _sample_args(name, logits, (temperature, top_k, top_p, min_p))
     if out is None:

@@ -644,7 +644,8 @@ int tq_residual_norm(int dtype, int y_dtype, const void *y, int64_t y_ts, const 
  * A logit that is NaN or -infinity weighs nothing; at +infinity all such share the
  * row.  Sums are exact, so results do not depend on any order: deterministic.
  *   logits : of dtype, rows of vocab at row stride `stride` elements (0: one row
- *     for all); probs must not overlap them.
+ *     for all).  tokens and probs must not overlap an input (TQ_E_SHAPE; rows
+ *     between each other's do not), but probs may be fp32 logits (same stride).
  *   workspace : as tq_tree_attention's, tq_sample_workspace_bytes() (0: NULL will
  *     do).
  * Domain: rows 0..2^20, vocab 1..2^27, rows * vocab below 2^34. */

@@ -4,8 +4,8 @@ import ctypes
 
 import pytest
 
-from test_abi_decode import NUL, SHAPE
-from test_abi_serving import P, residual
+from test_abi_decode import NUL, NULL, SHAPE
+from test_abi_serving import P, probs, residual, sample
 
 
 @pytest.fixture(scope="module")
@@ -61,3 +61,63 @@ def test_residual_norm_outputs_in_outputs(L):
                 dict(q=at(APART["x_out"], 380)), dict(d=at(APART["x_out"], -10)),
                 dict(d=at(P(7), 190)), dict(q=at(P(8), 8)), dict(d=APART["pre"])):
         assert c(**bad) == SHAPE, bad
+
+
+# arrays of 8200 logits a row, which takes a workspace: without one a call that gets past
+# the comparison of its arrays is refused as NULL
+V = 8200
+SETTINGS = dict(temp=P(10), top_k=P(11), top_p=P(12), min_p=P(13))
+
+
+def test_sampling_outputs_in_inputs(L):
+    c = sample(L)
+    c.good.update(SETTINGS, vocab=V, stride=V, rows=3, logits=P(0), u=P(14), tokens=P(15), ws=NUL)
+    assert c() == NULL
+    for name in (*SETTINGS, "u"):
+        for offset in (0, 8, -8):
+            assert c(tokens=at(c.good[name], offset)) == SHAPE, (name, offset)
+        assert c(tokens=at(c.good[name], 12)) == NULL == c(tokens=at(c.good[name], -12))
+    for offset in (-8, 0, 4 * V, 12 * V - 4):
+        assert c(tokens=at(P(0), offset)) == SHAPE, offset
+    assert c(tokens=at(P(0), 12 * V)) == NULL == c(tokens=at(P(0), -12))
+    # behind each row's logits, where the stride leaves room
+    assert c(stride=V + 3, tokens=at(P(0), 4 * V)) == NULL
+    assert c(stride=V + 2, tokens=at(P(0), 4 * V)) == SHAPE
+    c = probs(L)
+    c.good.update(SETTINGS, vocab=V, stride=V, rows=3, logits=P(0), probs=P(15), probs_stride=V,
+                  ws=NUL)
+    assert c() == NULL
+    for name in SETTINGS:
+        assert c(probs=c.good[name]) == SHAPE == c(probs=at(c.good[name], 4 - 12 * V))
+    # in place: fp32 at the same stride, or one row
+    assert c(probs=P(0)) == NULL == c(probs=P(0), rows=1, probs_stride=V + 9)
+    assert c(probs=P(0), dtype=1) == SHAPE == c(probs=P(0), dtype=2)
+    assert c(probs=P(0), probs_stride=V + 1) == SHAPE == c(probs=P(0), stride=0)
+    assert c(probs=at(P(0), 4)) == SHAPE == c(probs=at(P(0), 4 * V)) == c(probs=at(P(0), -4))
+
+
+def rows_meet(offset, stride_a, n_a, stride_b, n_b, rows):
+    """Row i of a at i * stride_a, of b at offset + i * stride_b, all against all."""
+    return any(offset + j * stride_b < i * stride_a + n_a and i * stride_a < offset + j * stride_b + n_b
+               for i in range(rows) for j in range(rows))
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 4), (1, 2)])
+def test_rows_between_rows(L, dtype, size):
+    """Every place of a few strides against all pairs of rows."""
+    c = probs(L)
+    c.good.update(SETTINGS, vocab=V, rows=4, dtype=dtype, logits=P(0), ws=NUL)
+    seen = set()
+    for stride in (0, V, 2 * V, 3 * V + 1, 9 * V):
+        for probs_stride in (V, V + 5, 2 * V, 3 * V + 1, 5 * V):
+            for part in range(-8, 40):
+                for near in (-4, 0, 4):
+                    offset = part * 2 * V + near
+                    want = rows_meet(offset, stride * size, V * size, probs_stride * 4, V * 4, 4)
+                    if dtype == 0 and offset == 0 and stride == probs_stride:
+                        want = False             # in place
+                    got = c(stride=stride, probs_stride=probs_stride, probs=at(P(40), offset),
+                            logits=P(40))
+                    assert got == (SHAPE if want else NULL), (stride, probs_stride, offset)
+                    seen.add(want)
+    assert seen == {True, False}

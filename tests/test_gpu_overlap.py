@@ -61,3 +61,23 @@ def test_residual_norm_without_a_second_norm_may_write_one_array(T, N):
     assert got[0] is one and torch.equal(one, want[0]) and torch.equal(one, want[1])
     tq().residual_norm(y, x, scale=0.5, x_out=x, z_out=x)
     assert torch.equal(x, want[0])
+
+
+@pytest.mark.parametrize("V", [50, 8192, 20001, 128001, 600001, 1048577])
+@pytest.mark.parametrize("kw", [dict(top_p=0.9), dict(top_k=40, top_p=0.8), dict(temperature=0.0), {}])
+def test_distributions_in_place_of_the_logits(V, kw):
+    kw = {k: torch.full((3,), v, dtype=torch.int32 if k == "top_k" else torch.float32, device="cuda")
+          for k, v in kw.items()}
+    x = 2.5 * randn(3, V, dtype=torch.float32)
+    x[1] = x[1].round()                          # thousands of equal ones
+    x[2, :] = 1.0
+    want = tq().sample_probs(x, **kw)
+    wide = torch.full((3, V + 7), 9.0, device="cuda")
+    inside = wide[:, 3:V + 3]
+    inside.copy_(x)
+    assert tq().sample_probs(inside, **kw, out=inside) is inside
+    assert torch.equal(inside, want) and (wide[:, :3] == 9).all() and (wide[:, V + 3:] == 9).all()
+    tq().sample_probs(x, **kw, out=x)
+    assert torch.equal(x, want)
+    with pytest.raises(tq().TiledqError):
+        tq().sample_probs(wide[:, :V], **kw, out=wide[:, 1:V + 1])
