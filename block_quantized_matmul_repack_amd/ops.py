@@ -506,13 +506,20 @@ def _heads_of(name, what, t, dtypes):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+@functools.lru_cache(maxsize=None)
+def _several_devices():
+    """Whether device 0 may not be the current one: asking which is takes a call of
+    11 us 0.1 us longer."""
+    return torch.cuda.device_count() > 1
+
+
 def _stream_of(dev):
     """The current HIP stream of GPU number dev, as an int handle."""
     if _raw_stream is not None:
         stream = _raw_stream(dev)
     else:
         stream = torch.cuda.current_stream(dev).cuda_stream
-    if not stream and _current_device() != dev:
+    if not stream and (dev or _several_devices()) and _current_device() != dev:
         # the null handle names the default stream of whichever device is current
         raise TiledqError(f"the tensors are on device {dev} and its default stream is asked for: "
                           "make that device the current one")
