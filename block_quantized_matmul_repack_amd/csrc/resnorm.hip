@@ -234,9 +234,12 @@ __device__ __forceinline__ void convert(float (&v)[8], const Raw8 &r, int dtype)
 
 // The same for many tokens of up to 8192 elements, two waves and more: a workgroup
 // takes every gridDim-th token, has the weights in registers, and the next token on
-// its way while it works on one.  8192 tokens, bf16, a workgroup each / so: 4096
-// elements 59.1 / 56.9 us (quantized 61.7 / 56.0), 5120 elements 85 / 67; a wave each
-// of 512 is faster alone (50.2, so 53.8, for 65536 tokens).
+// its way while it works on one.  bf16, norms on both sides, three sets of inputs in
+// turn, a workgroup for each token / so, us: 8192 x 4096 51.2 / 53.0, with one gate for
+// all tokens 55.1 / 52.5, quantized 50.6 / 49.7, of fp32 y 60.0 / 62.9; 8192 x 5120
+// 77.7 / 66.8, with the gate 85.5 / 67.5; 32768 x 1024 49.4 / 52.0, with the gate 53.8 /
+// 52.8; 4096 x 8192 53.1 / 54.9, with the gate 56.6 / 54.9, quantized 56.3 / 64.3.  A wave
+// each of 512 is faster alone (50.2, so 53.8, for 65536 tokens).
 template <int DT> __global__ __launch_bounds__(1024) void k_residual_norm_many(ResNormArgs a)
 {
     __shared__ float red[2][2][16];

@@ -21,12 +21,18 @@ namespace tq {
 namespace {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
-typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVES = 4, THREADS = 64 * WAVES;
 constexpr int SEL_WAVES = 8, SEL_THREADS = 64 * SEL_WAVES;
 constexpr int CHOOSE_WAVES = 16;
 constexpr int MOST_KEYS = 8192;                  // pages whose keys LDS holds
+// Heads of more than two turns of pages, as long as they are fewer than half the
+// compute units, have their pages spread over workgroups.  One workgroup a head /
+// spread, one query row group, us: 8 heads, 128 pages 6.4 / 7.7, 256 8.3 / 8.0, 512 11.0 / 8.6,
+// 2048 27 / 11.3; 120 heads, 512 pages 11.2 / 10.6, 2048 34.8 / 29.1; 128 heads 11.6 / 10.5,
+// 35 / 30; 192 heads 12.4 / 14.0 (1024 pages 21.3 / 23.0); 512 heads 20 / 27.  124 query rows:
+// 32 heads, 64 pages 12.8 / 14.0, 256 17.8 / 15.0, 1024 39.5 / 17.1.  Tables past MOST_KEYS take
+// two launches whatever lies in them: 8 heads of 2047 pages 11.4, in a table of 8192 11.1.
 constexpr int SPREAD_TURNS = 2, SPREAD_UNITS = 128;
 constexpr int COUNTER_STRIDE = 64;               // words: a cache line for each head
 

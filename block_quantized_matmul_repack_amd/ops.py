@@ -3,6 +3,9 @@
 Argument marshalling only: device pointers, sizes and the current HIP stream
 go to libtiledq.so; every step of the computation runs in its HIP kernels.
 Tensors must live on the GPU; outputs are allocated with torch unless given.
+The operators of decode and serving steps refuse tensors of a device whose
+default stream is asked for while another device is current: the null handle
+would name that one's stream.
 """
 import ctypes
 import functools

@@ -670,7 +670,9 @@ int tq_sample_probs(int dtype, const void *logits, int64_t stride, int64_t rows,
  * tq_cache_bounds writes them for every page that holds a position in [begin[b],
  * end[b]) of sequence b, over all of the page's positions below end[b]; to be
  * called once tq_cache_write has stored those.  Other pages' stay as they were.
- *   max_new : at least every end[b] - begin[b]; pages past it are not done.
+ *   max_new : at least every end[b] - begin[b]; pages past it are not done.  The
+ *     pages that max_new positions can touch, at most table_pages, times kv_heads * D
+ *     stay below 2^31.
  *   Table entries outside the cache are passed over; a page must not lie in two
  *   ranges of one call unless both give the same.
  *
